@@ -244,6 +244,7 @@ def _prepare_fork(c, g):
     s["refs"][pm[pm >= 0]] = 1
     s["free"] = torch.full((pages,), -1, dtype=torch.int32, device=DEV)
     s["free_count"] = torch.zeros(1, dtype=torch.int32, device=DEV)
+    s["status"] = torch.zeros(max(1, nc), dtype=torch.int32, device=DEV)
     if own:
         x = s["ctx"] = _context(n, NL, H, 64, P, T, B, R, min(B, 64), pages, s["tail"], s["pool"],
                                 s["hot"], s["host"],
@@ -458,7 +459,7 @@ def _fork_own(s):
     x.release_requests(m, s["dst"])
     x.list_free_pages(s["free"], s["free_count"], s["workspace"])
     x.fork_requests(m, s["src"], s["dst"])
-    x.copy_pages(s["copy_req"].numel(), s["copy_req"], s["copy_page"], s["spare"])
+    x.copy_pages(s["copy_req"].numel(), s["copy_req"], s["copy_page"], s["spare"], s["status"])
     return _fork_outputs(s)
 
 
