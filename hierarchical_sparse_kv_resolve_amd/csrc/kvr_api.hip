@@ -8,6 +8,7 @@
 #include <new>
 
 #include "kvr_internal.h"
+#include "rowformat.h"
 
 namespace kvr {
 bool tile_magic_exact(int32_t row_bytes);
@@ -724,6 +725,277 @@ int kvr_restore_pages(kvr_ctx *ctx, int32_t n, const int32_t *req_ids, const int
         return ok();
     hipError_t e = kvr::launch_restore(ctx, n, req_ids, pages, phys, status, s);
     return e == hipSuccess ? ok() : hip_fail(e, "restore launch");
+}
+
+// ---------------------------------------------------- pages shared by requests
+
+int kvr_bind_page_refs(kvr_ctx *ctx, int32_t *refs)
+{
+    if (int rc = check_ctx(ctx, false))
+        return rc;
+    ctx->page_refs = refs;
+    return ok();
+}
+
+static int check_refs(const kvr_ctx *ctx)
+{
+    if (int rc = check_ctx(ctx))
+        return rc;
+    if (ctx->shape.pool_rows > 0 && !ctx->page_refs)
+        return fail(KVR_E_ARG, "page reference counts not bound");
+    return KVR_OK;
+}
+
+int kvr_count_page_refs(kvr_ctx *ctx, void *stream)
+{
+    if (int rc = check_refs(ctx))
+        return rc;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (int rc = check_stream(ctx, s))
+        return rc;
+    hipError_t e = kvr::launch_count_refs(ctx, s);
+    return e == hipSuccess ? ok() : hip_fail(e, "page count launch");
+}
+
+int kvr_release_requests(kvr_ctx *ctx, int32_t n, const int32_t *req_ids, int32_t *status,
+                         void *stream)
+{
+    if (int rc = check_refs(ctx))
+        return rc;
+    if (int rc = check_n(ctx, n))
+        return rc;
+    if (n > 0 && !req_ids)
+        return fail(KVR_E_ARG, "req_ids is required");
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (int rc = check_stream(ctx, s))
+        return rc;
+    if (n == 0)
+        return ok();
+    hipError_t e = kvr::launch_release(ctx, n, req_ids, status, s);
+    return e == hipSuccess ? ok() : hip_fail(e, "release launch");
+}
+
+int kvr_fork_requests(kvr_ctx *ctx, int32_t n, const int32_t *src_ids, const int32_t *dst_ids,
+                      int32_t *status, void *stream)
+{
+    if (int rc = check_refs(ctx))
+        return rc;
+    if (int rc = check_n(ctx, n))
+        return rc;
+    if (n > 0 && (!src_ids || !dst_ids))
+        return fail(KVR_E_ARG, "src_ids and dst_ids are required");
+    if (int rc = check_all_layers(ctx))
+        return rc;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (int rc = check_stream(ctx, s))
+        return rc;
+    if (n == 0)
+        return ok();
+    hipError_t e = kvr::launch_fork(ctx, n, src_ids, dst_ids, status, s);
+    return e == hipSuccess ? ok() : hip_fail(e, "fork launch");
+}
+
+int kvr_copy_pages(kvr_ctx *ctx, int32_t n, const int32_t *req_ids, const int32_t *pages,
+                   const int32_t *phys, int32_t *status, void *stream)
+{
+    if (int rc = check_refs(ctx))
+        return rc;
+    if (int rc = check_page_list(ctx, n, req_ids, pages, phys))
+        return rc;
+    if (n > 0 && !status)
+        return fail(KVR_E_ARG, "status is required");
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (int rc = check_stream(ctx, s))
+        return rc;
+    if (n == 0)
+        return ok();
+    hipError_t e = kvr::launch_copy_pages(ctx, n, req_ids, pages, phys, status, s);
+    return e == hipSuccess ? ok() : hip_fail(e, "page copy launch");
+}
+
+int64_t kvr_pool_workspace(const kvr_ctx *ctx)
+{
+    if (int rc = check_ctx(ctx, false))
+        return rc;
+    ok();
+    return (int64_t)kvr::pool_workspace_bytes(ctx);
+}
+
+static int check_pool_workspace(const kvr_ctx *ctx, const void *workspace, size_t bytes)
+{
+    if (bytes < kvr::pool_workspace_bytes(ctx) || !workspace)
+        return fail(KVR_E_ARG, "the workspace has %zu bytes, the call needs %zu", workspace ? bytes : 0,
+                    kvr::pool_workspace_bytes(ctx));
+    if (reinterpret_cast<uintptr_t>(workspace) % 4 != 0)
+        return fail(KVR_E_ARG, "the workspace is not aligned to 4 bytes");
+    return KVR_OK;
+}
+
+int kvr_list_free_pages(kvr_ctx *ctx, int32_t *free_list, int32_t *free_count, void *workspace,
+                        size_t workspace_bytes, void *stream)
+{
+    if (int rc = check_refs(ctx))
+        return rc;
+    if ((!free_list && ctx->shape.pool_rows > 0) || !free_count)
+        return fail(KVR_E_ARG, "free_list and free_count are required");
+    if (int rc = check_pool_workspace(ctx, workspace, workspace_bytes))
+        return rc;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (int rc = check_stream(ctx, s))
+        return rc;
+    hipError_t e = kvr::launch_list_free(ctx, free_list, free_count, workspace, s);
+    return e == hipSuccess ? ok() : hip_fail(e, "free list launch");
+}
+
+int kvr_compact_pool(kvr_ctx *ctx, int32_t max_moves, int32_t *moves, int32_t *move_count,
+                     void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (int rc = check_refs(ctx))
+        return rc;
+    if (max_moves < 0)
+        return fail(KVR_E_ARG, "negative max_moves");
+    if ((!moves && max_moves > 0 && ctx->shape.pool_rows > 0) || !move_count)
+        return fail(KVR_E_ARG, "moves and move_count are required");
+    if (int rc = check_all_layers(ctx))
+        return rc;
+    if (int rc = check_pool_workspace(ctx, workspace, workspace_bytes))
+        return rc;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (int rc = check_stream(ctx, s))
+        return rc;
+    hipError_t e = kvr::launch_compact(ctx, max_moves, moves, move_count, workspace, s);
+    return e == hipSuccess ? ok() : hip_fail(e, "compaction launch");
+}
+
+// ------------------------------------------------- rows in a model's format
+
+static int check_row_format(int32_t format, int32_t d_v, int32_t d_rope)
+{
+    if (format != KVR_ROW_BF16 && format != KVR_ROW_F16 && format != KVR_ROW_FP8)
+        return fail(KVR_E_ARG, "unknown row format %d", format);
+    if (!kvr::row_dims_ok(d_v, d_rope))
+        return fail(KVR_E_ARG, "d_v %d with d_rope %d: d_v is 256 or 512, d_rope 0 or 64", d_v, d_rope);
+    return KVR_OK;
+}
+
+int kvr_row_layout(int32_t format, int32_t d_v, int32_t d_rope)
+{
+    if (int rc = check_row_format(format, d_v, d_rope))
+        return rc;
+    ok();
+    return kvr::row_bytes_of(format, d_v, d_rope);
+}
+
+// The format's rows are the context's rows.
+static int check_rows_of(const kvr_ctx *ctx, int32_t format, int32_t d_v, int32_t d_rope)
+{
+    if (int rc = check_row_format(format, d_v, d_rope))
+        return rc;
+    const int32_t need = kvr::row_bytes_of(format, d_v, d_rope);
+    if (need != ctx->cfg.row_bytes)
+        return fail(KVR_E_ARG, "rows of this format have %d bytes, the context's have %d", need,
+                    ctx->cfg.row_bytes);
+    return KVR_OK;
+}
+
+int kvr_pack_rows(kvr_ctx *ctx, const kvr_pack_call *call, void *stream)
+{
+    if (int rc = check_ctx(ctx, false))
+        return rc;
+    if (!call)
+        return fail(KVR_E_ARG, "null call");
+    const kvr_pack_call &p = *call;
+    if (int rc = check_rows_of(ctx, p.format, p.d_v, p.d_rope))
+        return rc;
+    if (p.value_type != KVR_VALUE_BF16 && p.value_type != KVR_VALUE_F16 &&
+        p.value_type != KVR_VALUE_F32)
+        return fail(KVR_E_ARG, "unknown value type %d", p.value_type);
+    if (p.n < 0)
+        return fail(KVR_E_ARG, "negative row count");
+    if (p.latent_stride < 0 || p.rope_stride < 0)
+        return fail(KVR_E_ARG, "negative stride");
+    if (p.n > 0 && (!p.latent || !p.rows || (p.d_rope > 0 && !p.rope)))
+        return fail(KVR_E_ARG, "latent, rows and (with d_rope > 0) rope are required");
+    const uintptr_t e = p.value_type == KVR_VALUE_F32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(p.latent) % e != 0 ||
+        reinterpret_cast<uintptr_t>(p.rope) % e != 0 ||
+        reinterpret_cast<uintptr_t>(p.weight) % 4 != 0 || reinterpret_cast<uintptr_t>(p.rows) % 16 != 0)
+        return fail(KVR_E_ARG, "latent, rope, weight or rows is not aligned");
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (int rc = check_stream(ctx, s))
+        return rc;
+    if (p.n == 0)
+        return ok();
+    hipError_t err = kvr::launch_pack(ctx, p, s);
+    return err == hipSuccess ? ok() : hip_fail(err, "pack launch");
+}
+
+// Sizes of an attention call that its kernels' 32-bit indexing covers.
+static int check_attend_sizes(int32_t n, int32_t nq, int32_t heads, int32_t rows)
+{
+    if (n < 0 || nq < 1 || heads < 1 || rows < 0)
+        return fail(KVR_E_ARG, "n and rows must be >= 0, nq and heads >= 1");
+    if (nq > 4096 || heads > 4096 || rows > (1 << 24))
+        return fail(KVR_E_ARG, "at most 4096 queries, 4096 heads and 2^24 rows per query");
+    if ((int64_t)n * nq * heads > (1 << 24))
+        return fail(KVR_E_ARG, "n * nq * heads must be at most 2^24");
+    return KVR_OK;
+}
+
+int64_t kvr_attend_workspace(int32_t n, int32_t nq, int32_t heads, int32_t d_v, int32_t rows)
+{
+    if (int rc = check_attend_sizes(n, nq, heads, rows))
+        return rc;
+    if (!kvr::row_dims_ok(d_v, 0))
+        return fail(KVR_E_ARG, "d_v must be 256 or 512");
+    ok();
+    return kvr::attend_workspace_bound(n, nq, heads, d_v, rows);
+}
+
+int kvr_attend_rows(kvr_ctx *ctx, const kvr_attend_call *call, void *stream)
+{
+    if (int rc = check_ctx(ctx, false))
+        return rc;
+    if (!call)
+        return fail(KVR_E_ARG, "null call");
+    const kvr_attend_call &a = *call;
+    if (int rc = check_rows_of(ctx, a.format, a.d_v, a.d_rope))
+        return rc;
+    if (int rc = check_n(ctx, a.n))
+        return rc;
+    if (a.stride < 0 || (a.map && a.k < 0))
+        return fail(KVR_E_ARG, "negative stride or k");
+    const int32_t rows = a.map ? a.k : a.stride;
+    if (int rc = check_attend_sizes(a.n, a.nq, a.heads, rows))
+        return rc;
+    if (a.stride > (1 << 24))
+        return fail(KVR_E_ARG, "stride above 2^24");
+    if (!a.rows)
+        if (int rc = check_layer(ctx, a.layer))
+            return rc;
+    if (a.n > 0 && (!a.q || !a.out || (a.stride > 0 && !a.rows && !a.loc)))
+        return fail(KVR_E_ARG, "q, out and rows or loc are required");
+    if (a.q_stride_entry < 0 || a.q_stride_query < 0 || a.q_stride_head < 0)
+        return fail(KVR_E_ARG, "negative stride of q");
+    if (reinterpret_cast<uintptr_t>(a.q) % 2 != 0 || reinterpret_cast<uintptr_t>(a.out) % 16 != 0 ||
+        reinterpret_cast<uintptr_t>(a.rows) % 16 != 0)
+        return fail(KVR_E_ARG, "q, out or rows is not aligned");
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (int rc = check_stream(ctx, s))
+        return rc;
+    if (a.n == 0)
+        return ok();
+    const kvr::AttendPlan plan =
+        kvr::attend_plan(a.n, a.nq, a.heads, a.d_v, rows, a.map != nullptr);
+    if (plan.workspace > 0) {
+        if (!a.workspace || a.workspace_bytes < (size_t)plan.workspace)
+            return fail(KVR_E_ARG, "the workspace has %zu bytes, the call needs %lld",
+                        a.workspace ? a.workspace_bytes : 0, (long long)plan.workspace);
+        if (reinterpret_cast<uintptr_t>(a.workspace) % 16 != 0)
+            return fail(KVR_E_ARG, "the workspace is not aligned to 16 bytes");
+    }
+    hipError_t e = kvr::launch_attend(ctx, a, plan, s);
+    return e == hipSuccess ? ok() : hip_fail(e, "attention launch");
 }
 
 int kvr_status_summary(const int32_t *status, int32_t n, int32_t *first_bad)

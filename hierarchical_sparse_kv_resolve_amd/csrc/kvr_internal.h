@@ -63,6 +63,7 @@ struct kvr_ctx {
     int32_t *tag;
     uint32_t *stamp;
     uint32_t *clock;
+    int32_t *page_refs;  // map entries naming each physical page, or null
     bool meta_bound;
     // per-layer pointers: host-side mirror and device table
     kvr::LayerPtrs *layers_h;
@@ -168,5 +169,35 @@ hipError_t launch_reclaim(const kvr_ctx *c, int32_t n, const int32_t *req, const
                           int32_t *freed, int32_t *status, hipStream_t s);
 hipError_t launch_restore(const kvr_ctx *c, int32_t n, const int32_t *req, const int32_t *page,
                           const int32_t *phys, int32_t *status, hipStream_t s);
+
+// Pages shared between requests.
+size_t pool_workspace_bytes(const kvr_ctx *c);
+hipError_t launch_count_refs(const kvr_ctx *c, hipStream_t s);
+hipError_t launch_release(const kvr_ctx *c, int32_t n, const int32_t *ids, int32_t *status,
+                          hipStream_t s);
+hipError_t launch_fork(const kvr_ctx *c, int32_t n, const int32_t *src, const int32_t *dst,
+                       int32_t *status, hipStream_t s);
+hipError_t launch_copy_pages(const kvr_ctx *c, int32_t n, const int32_t *req, const int32_t *page,
+                             const int32_t *phys, int32_t *status, hipStream_t s);
+hipError_t launch_list_free(const kvr_ctx *c, int32_t *free_list, int32_t *free_count,
+                            void *workspace, hipStream_t s);
+hipError_t launch_compact(const kvr_ctx *c, int32_t max_moves, int32_t *moves, int32_t *move_count,
+                          void *workspace, hipStream_t s);
+
+hipError_t launch_pack(const kvr_ctx *c, const kvr_pack_call &p, hipStream_t s);
+
+// How a kvr_attend_rows call is cut: `block` query rows (heads, or heads of
+// several queries that share a selection) per workgroup, `shares` shares of
+// the rows.  Workspace bytes of exactly that call, and the largest over calls
+// of fewer entries, queries, heads or rows.
+struct AttendPlan {
+    int32_t block, groups, shares;
+    int64_t workspace;
+};
+AttendPlan attend_plan(int32_t n, int32_t nq, int32_t heads, int32_t d_v, int32_t rows,
+                       bool mapped);
+int64_t attend_workspace_bound(int32_t n, int32_t nq, int32_t heads, int32_t d_v, int32_t rows);
+hipError_t launch_attend(const kvr_ctx *c, const kvr_attend_call &call, const AttendPlan &plan,
+                         hipStream_t s);
 
 }  // namespace kvr

@@ -38,6 +38,7 @@ struct PageArgs {
     const int32_t *phys;      // restore only
     int32_t *freed;           // reclaim only
     int32_t *status;
+    int32_t *refs;            // map entries naming each physical page, or null
 };
 
 // Copies P rows (P * R contiguous bytes) of every layer from a page of one
@@ -110,6 +111,8 @@ __global__ __launch_bounds__(NT) void reclaim_kernel(PageArgs a)
             if (threadIdx.x == 0) {
                 a.host_valid[e] = 1;
                 a.page_map[e] = -1;
+                if (a.refs)
+                    atomicSub(&a.refs[ph], 1);
             }
         }
     }
@@ -131,15 +134,18 @@ __global__ __launch_bounds__(NT) void restore_kernel(PageArgs a)
     const int64_t e = (int64_t)r * a.sh.n_pages + p;
     if (st == KVR_OK && (ph < 0 || (int64_t)ph * a.sh.P >= a.sh.pool_rows))
         st = KVR_E_RANGE;
-    if (st == KVR_OK && a.page_map[e] >= 0)
+    if (st == KVR_OK && (a.page_map[e] >= 0 || (a.refs && a.refs[ph] > 0)))
         st = KVR_E_STATE;
     if (st == KVR_OK && !a.host_valid[e])
         st = KVR_E_NO_HOST_COPY;
     if (st == KVR_OK) {
         move_page(a, r, p, ph, false);
         __syncthreads();
-        if (threadIdx.x == 0)
+        if (threadIdx.x == 0) {
             a.page_map[e] = ph;
+            if (a.refs)
+                a.refs[ph] = 1;
+        }
     }
     if (threadIdx.x == 0 && a.status)
         a.status[i] = st;
@@ -154,6 +160,7 @@ PageArgs page_args(const kvr_ctx *c, const int32_t *req, const int32_t *page)
     a.host_valid = c->host_valid;
     a.req = req;
     a.page = page;
+    a.refs = c->page_refs;
     return a;
 }
 

@@ -43,10 +43,20 @@ EXPORTS = ("kvr_create", "kvr_destroy", "kvr_last_error", "kvr_bind_metadata", "
            "kvr_residency_refill", "kvr_residency_counts", "kvr_draft_create",
            "kvr_draft_destroy", "kvr_draft_reset", "kvr_draft_append", "kvr_draft_rollback",
            "kvr_draft_window", "kvr_staging_create", "kvr_staging_destroy",
-           "kvr_staging_acquire", "kvr_staging_release")
+           "kvr_staging_acquire", "kvr_staging_release", "kvr_row_layout", "kvr_pack_rows",
+           "kvr_attend_rows", "kvr_attend_workspace", "kvr_bind_page_refs", "kvr_count_page_refs",
+           "kvr_release_requests", "kvr_fork_requests", "kvr_copy_pages", "kvr_pool_workspace",
+           "kvr_list_free_pages", "kvr_compact_pool")
 
 # kvr_kernel: kinds of the library's kernel launches (launch timing).
-KERNEL_NAMES = ("append", "resolve", "refill", "gather", "dedup", "state", "fused", "step")
+KERNEL_NAMES = ("append", "resolve", "refill", "gather", "dedup", "state", "fused", "step",
+                "attend", "pack", "pages")
+
+# kvr_row_format, and the 16-bit type of queries, outputs and rope parts.
+ROW_FORMATS = {"bf16": 0, "f16": 1, "fp8": 2}
+_ROW_TYPES = {"bf16": "bfloat16", "f16": "float16", "fp8": "bfloat16"}
+# kvr_value_type by torch dtype name.
+_VALUE_TYPES = {"bfloat16": 0, "float16": 1, "float32": 2}
 
 
 class KvrError(RuntimeError):
@@ -85,6 +95,29 @@ class ResolveCall(ctypes.Structure):
                 ("loc", ctypes.c_void_p), ("fills", ctypes.c_void_p),
                 ("fill_count", ctypes.c_void_p), ("status", ctypes.c_void_p),
                 ("stats", ctypes.c_void_p)]
+
+
+class PackCall(ctypes.Structure):
+    """kvr_pack_call of include/kvr.h."""
+    _fields_ = [("format", ctypes.c_int32), ("value_type", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("d_v", ctypes.c_int32), ("d_rope", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("latent", ctypes.c_void_p), ("rope", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p), ("rows", ctypes.c_void_p),
+                ("latent_stride", ctypes.c_int64), ("rope_stride", ctypes.c_int64)]
+
+
+class AttendCall(ctypes.Structure):
+    """kvr_attend_call of include/kvr.h."""
+    _fields_ = [("layer", ctypes.c_int32), ("format", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("nq", ctypes.c_int32), ("heads", ctypes.c_int32), ("d_v", ctypes.c_int32),
+                ("d_rope", ctypes.c_int32), ("stride", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("req_ids", ctypes.c_void_p), ("loc", ctypes.c_void_p),
+                ("rows", ctypes.c_void_p), ("count", ctypes.c_void_p), ("map", ctypes.c_void_p),
+                ("q", ctypes.c_void_p), ("q_stride_entry", ctypes.c_int64),
+                ("q_stride_query", ctypes.c_int64), ("q_stride_head", ctypes.c_int64),
+                ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("status", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
 
 _lib = None
 
@@ -139,11 +172,25 @@ def lib():
             "kvr_staging_destroy": [P],
             "kvr_staging_acquire": [P, P, P],
             "kvr_staging_release": [P, I, P],
+            "kvr_row_layout": [I, I, I],
+            "kvr_pack_rows": [P, P, P],
+            "kvr_attend_rows": [P, P, P],
+            "kvr_attend_workspace": [I, I, I, I, I],
+            "kvr_bind_page_refs": [P, P],
+            "kvr_count_page_refs": [P, P],
+            "kvr_release_requests": [P, I, P, P, P],
+            "kvr_fork_requests": [P, I, P, P, P, P],
+            "kvr_copy_pages": [P, I, P, P, P, P, P],
+            "kvr_pool_workspace": [P],
+            "kvr_list_free_pages": [P, P, P, P, U, P],
+            "kvr_compact_pool": [P, I, P, P, P, U, P],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
             fn.argtypes = args
             fn.restype = ctypes.c_int
+        for name in ("kvr_attend_workspace", "kvr_pool_workspace"):
+            getattr(L, name).restype = ctypes.c_int64
         L.kvr_last_error.argtypes = []
         L.kvr_last_error.restype = ctypes.c_char_p
         _lib = L
@@ -211,6 +258,59 @@ def _check(rc: int):
     if rc != OK:
         raise KvrError(rc, lib().kvr_last_error().decode())
     return rc
+
+
+def _typed(x, name: str, dtypes, shape=None):
+    """A strided device tensor of one of the dtypes (names) whose last
+    dimension is contiguous, on the current device."""
+    import torch
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name}: expected a GPU tensor, got {type(x)}")
+    if not x.is_cuda:
+        raise TypeError(f"{name}: expected a GPU tensor, got one on {x.device}")
+    if str(x.dtype)[6:] not in dtypes:
+        raise TypeError(f"{name}: expected {' or '.join(dtypes)}, got {x.dtype}")
+    if shape is not None and tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(x.shape)}, the call needs {tuple(shape)}")
+    if x.numel() and x.shape[-1] > 1 and x.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension is not contiguous")
+    _same_device(x, name)
+    return x
+
+
+def _same_device(x, name: str):
+    """A tensor of another device than the current one (which the library
+    requires to be the context's) is refused; addresses pass."""
+    if getattr(x, "is_cuda", False):
+        import torch
+        if x.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name}: on {x.device}, the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+    return x
+
+
+def _dev_here(x, name: str, nbytes: int = 0) -> int | None:
+    return _dev(_same_device(x, name), name, nbytes)
+
+
+def _workspace(x):
+    """(address, bytes) of a workspace tensor; an address is taken to hold what
+    the call needs."""
+    if x is None or isinstance(x, int):
+        return x, (1 << 62 if x else 0)
+    return _dev_here(x, "workspace"), x.numel() * x.element_size()
+
+
+def row_layout(fmt: str, d_v: int, d_rope: int) -> int:
+    """Bytes of one row of a format ("bf16", "f16" or "fp8")."""
+    rc = lib().kvr_row_layout(_row_format(fmt), d_v, d_rope)
+    return rc if rc >= 0 else _check(rc)
+
+
+def _row_format(fmt: str) -> int:
+    if fmt not in ROW_FORMATS:
+        raise ValueError(f"unknown row format {fmt!r}: one of {', '.join(ROW_FORMATS)}")
+    return ROW_FORMATS[fmt]
 
 
 def last_error() -> str:
@@ -471,6 +571,117 @@ class Context:
                                          stride, _dev(fills, "fills", 8 * n * B),
                                          _dev(fill_count, "fill_count", 4 * n),
                                          _dev(status, "status", 4 * n), _stream(stream)))
+
+    # ------------------------------------------- rows in a model's format
+
+    def pack_rows(self, n, latent, rope, rows, *, fmt, d_v, d_rope, weight=None, eps=0.0,
+                  stream=None):
+        """Rows of n tokens: latent [n, d_v] and rope [n, d_rope] (bf16, fp16 or
+        fp32, both of one type; rows may be strided slices), normalised where a
+        float32 weight [d_v] is given, into rows (n * row_bytes bytes, on the
+        device or pinned)."""
+        types = tuple(_VALUE_TYPES)
+        _typed(latent, "latent", types, (n, d_v))
+        kind = str(latent.dtype)[6:]
+        if d_rope:
+            _typed(rope, "rope", (kind,), (n, d_rope))
+        if weight is not None:
+            _typed(weight, "weight", ("float32",), (d_v,))
+        need = max(n, 0) * self.cfg.row_bytes
+        on_host = hasattr(rows, "is_cuda") and not rows.is_cuda
+        call = PackCall(_row_format(fmt), _VALUE_TYPES[kind], n, d_v, d_rope, eps,
+                        latent.data_ptr(), rope.data_ptr() if d_rope else None,
+                        None if weight is None else weight.data_ptr(),
+                        _pinned(rows, "rows", need) if on_host else _dev_here(rows, "rows", need),
+                        latent.stride(0), rope.stride(0) if d_rope else 0)
+        _check(lib().kvr_pack_rows(self.handle, ctypes.byref(call), _stream(stream)))
+
+    @staticmethod
+    def attend_workspace(n, nq, heads, d_v, rows) -> int:
+        """Workspace bytes for attend_rows calls of up to these sizes; rows is
+        the rows per query (the map's k, or stride without a map)."""
+        got = lib().kvr_attend_workspace(n, nq, heads, d_v, rows)
+        return got if got >= 0 else _check(got)
+
+    def attend_rows(self, layer, n, req_ids, q, out, *, fmt, d_v, d_rope, scale, stride, loc=None,
+                    rows=None, count=None, map_=None, lse=None, status=None, workspace=None,
+                    stream=None):
+        """Attention of q [n, nq, heads, d_v + d_rope] over the rows that loc
+        names in `layer` (or over the gathered rows), into out [n, nq, heads,
+        d_v] and lse [n, nq, heads]; with map_ [n, nq, k] query a of entry i
+        attends to the entries map_[i, a] only.  See kvr_attend_rows."""
+        kind = (_ROW_TYPES.get(fmt, ""),)
+        code = _row_format(fmt)
+        if getattr(q, "ndim", 4) != 4:
+            raise ValueError(f"q: {q.ndim} dimensions, the call needs [n, nq, heads, d_v + d_rope]")
+        _typed(q, "q", kind)
+        nq, heads = int(q.shape[1]), int(q.shape[2])
+        _typed(q, "q", kind, (n, nq, heads, d_v + d_rope))
+        _typed(out, "out", kind, (n, nq, heads, d_v))
+        if lse is not None:
+            _typed(lse, "lse", ("float32",), (n, nq, heads))
+        k = 0
+        if map_ is not None:
+            if getattr(map_, "ndim", 3) != 3:
+                raise ValueError(f"map: {map_.ndim} dimensions, the call needs [n, nq, k]")
+            _typed(map_, "map", ("int32",))
+            k = int(map_.shape[2])
+            _typed(map_, "map", ("int32",), (n, nq, k))
+        if count is not None and not isinstance(count, int):
+            _typed(count, "count", ("int32",))
+        m = max(n, 0) * max(stride, 0)
+        ws, ws_bytes = _workspace(workspace)
+        call = AttendCall(layer, code, n, nq, heads, d_v, d_rope, stride, k, scale,
+                          _dev_here(req_ids, "req_ids", 4 * n), _dev_here(loc, "loc", 4 * m),
+                          _dev_here(rows, "rows", m * self.cfg.row_bytes),
+                          _dev_here(count, "count", 4 * n), _dev_here(map_, "map"),
+                          q.data_ptr(), q.stride(0), q.stride(1), q.stride(2),
+                          _dev_here(out, "out"), _dev_here(lse, "lse"),
+                          _dev_here(status, "status", 4 * n), ws, ws_bytes)
+        _check(lib().kvr_attend_rows(self.handle, ctypes.byref(call), _stream(stream)))
+
+    # ------------------------------------------- pages shared by requests
+
+    def bind_page_refs(self, refs):
+        """int32 [pool_pages] map entries naming each physical page, or None."""
+        _check(lib().kvr_bind_page_refs(self.handle,
+                                        _dev_here(refs, "refs", 4 * self.cfg.pool_pages)))
+
+    def count_page_refs(self, stream=None):
+        _check(lib().kvr_count_page_refs(self.handle, _stream(stream)))
+
+    def release_requests(self, n, req_ids, status=None, stream=None):
+        _check(lib().kvr_release_requests(self.handle, n, _dev_here(req_ids, "req_ids", 4 * n),
+                                          _dev_here(status, "status", 4 * n), _stream(stream)))
+
+    def fork_requests(self, n, src_ids, dst_ids, status=None, stream=None):
+        _check(lib().kvr_fork_requests(self.handle, n, _dev_here(src_ids, "src_ids", 4 * n),
+                                       _dev_here(dst_ids, "dst_ids", 4 * n),
+                                       _dev_here(status, "status", 4 * n), _stream(stream)))
+
+    def copy_pages(self, n, req_ids, pages, phys, status, stream=None):
+        _check(lib().kvr_copy_pages(self.handle, n, _dev_here(req_ids, "req_ids", 4 * n),
+                                    _dev_here(pages, "pages", 4 * n),
+                                    _dev_here(phys, "phys", 4 * n),
+                                    _dev_here(status, "status", 4 * n), _stream(stream)))
+
+    def pool_workspace(self) -> int:
+        """Workspace bytes of list_free_pages and compact_pool."""
+        got = lib().kvr_pool_workspace(self.handle)
+        return got if got >= 0 else _check(got)
+
+    def list_free_pages(self, free_list, free_count, workspace, stream=None):
+        ws, ws_bytes = _workspace(workspace)
+        _check(lib().kvr_list_free_pages(
+            self.handle, _dev_here(free_list, "free_list", 4 * self.cfg.pool_pages),
+            _dev_here(free_count, "free_count", 4), ws, ws_bytes, _stream(stream)))
+
+    def compact_pool(self, max_moves, moves, move_count, workspace, stream=None):
+        ws, ws_bytes = _workspace(workspace)
+        need = 8 * max(0, min(max_moves, self.cfg.pool_pages))
+        _check(lib().kvr_compact_pool(self.handle, max_moves, _dev_here(moves, "moves", need),
+                                      _dev_here(move_count, "move_count", 4), ws, ws_bytes,
+                                      _stream(stream)))
 
 
 class Residency:

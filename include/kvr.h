@@ -422,6 +422,209 @@ int kvr_reclaim_pages(kvr_ctx *ctx, int32_t n, const int32_t *req_ids, const int
 int kvr_restore_pages(kvr_ctx *ctx, int32_t n, const int32_t *req_ids, const int32_t *pages,
                       const int32_t *phys, int32_t *status, void *stream);
 
+/* Formats of the rows a model's attention reads (every other call moves rows
+ * as opaque bytes).  A row holds one token's latent (d_v values) and the
+ * rotated part of its key (d_rope values); its key is both, its value the
+ * latent, and every head shares it.
+ *   KVR_ROW_BF16, KVR_ROW_F16: d_v + d_rope values of 16 bits
+ *   KVR_ROW_FP8: d_v e4m3 codes, then one 32-bit scale for each 128 of them
+ *     (the scales padded with zeros to a multiple of 16 bytes), then d_rope
+ *     values of bf16.  A code stands for code * scale.
+ * d_v is 256 or 512, d_rope 0 or 64. */
+typedef enum kvr_row_format {
+    KVR_ROW_BF16 = 0,
+    KVR_ROW_F16 = 1,
+    KVR_ROW_FP8 = 2,
+} kvr_row_format;
+
+/* Type of the values handed to kvr_pack_rows. */
+typedef enum kvr_value_type {
+    KVR_VALUE_BF16 = 0,
+    KVR_VALUE_F16 = 1,
+    KVR_VALUE_F32 = 2,
+} kvr_value_type;
+
+/* Bytes of one row of a format (1152 for 16-bit and 656 for fp8 rows of
+ * d_v 512, d_rope 64), or KVR_E_ARG for a format or size not offered. */
+int kvr_row_layout(int32_t format, int32_t d_v, int32_t d_rope);
+
+/* Arguments of kvr_pack_rows.
+ *   rows (device or pinned) [n][row_bytes] out, aligned to 16 bytes and
+ *     disjoint from the inputs; row_bytes must be kvr_row_layout's
+ *   latent (device) [n][d_v] of value_type, consecutive rows latent_stride
+ *     elements apart; rope [n][d_rope] likewise (NULL when d_rope is 0);
+ *     slices of one projection's output are taken as they are
+ *   weight (device) float [d_v] or NULL: with it the latent is normalised,
+ *     x = latent / sqrt(mean(latent^2) + eps) * weight (sums in 32 bits);
+ *     without it x = latent */
+typedef struct kvr_pack_call {
+    int32_t format;      /* kvr_row_format */
+    int32_t value_type;  /* kvr_value_type */
+    int32_t n;
+    int32_t d_v;
+    int32_t d_rope;
+    float eps;
+    const void *latent;
+    const void *rope;
+    const float *weight;
+    void *rows;
+    int64_t latent_stride;
+    int64_t rope_stride;
+} kvr_pack_call;
+
+/* Rows of n new (or imported) tokens in the cache's format, for
+ * kvr_append_rows, a host store or the optional pool.  x is rounded once, to
+ * nearest, to the row's 16-bit type; in fp8 rows each group of 128 values has
+ * scale = max|x| / 448 (1 for a group of zeros) and codes e4m3(x / scale).
+ * The rope part is rounded to 16 bits as it is.  A NaN or an infinity makes
+ * its own scale group (its own value, in 16-bit rows; the whole latent when
+ * it is normalised) NaN or infinite, no other.  One kernel; n = 0 is a no-op. */
+int kvr_pack_rows(kvr_ctx *ctx, const kvr_pack_call *call, void *stream);
+
+/* Arguments of kvr_attend_rows.  Names shared with kvr_gather_rows mean the
+ * same.
+ *   rows, loc: where row j of request entry i is read.  rows (device)
+ *     [n][stride][R] is a gathered buffer (kvr_gather_rows' out; aligned to 16
+ *     bytes); with rows NULL the row is read where loc[i][j] names it in
+ *     `layer` (tail, optional pool or hot cache; a fresh row's host fill must
+ *     have run).  loc (device) uint32 [n][stride] is required with rows NULL;
+ *     otherwise it may be NULL.  Entries whose word is KVR_LOC_INVALID are
+ *     left out of the attention in both cases.
+ *   count (device) int32 [n] or NULL (= stride): only entries j < count[i]
+ *     are attended to
+ *   map (device) int32 [n][nq][k] or NULL: with it (kvr_dedup_verify_selections'
+ *     map) query a of entry i attends to the k entries map[i][a][0..k) of the
+ *     union; indices outside [0, count[i]) are left out.  Without it (k is
+ *     ignored) every query attends to all count[i] entries.
+ *   q (device) [n][nq][heads][d_v + d_rope], 16-bit values of the format's type
+ *     (bf16 with fp8 rows); strides in elements between entries, queries and
+ *     heads, the last dimension contiguous
+ *   out (device) [n][nq][heads][d_v] contiguous, of q's type, aligned to 16
+ *     bytes; lse (device) float [n][nq][heads] or NULL
+ *   status (device) int32 [n] or NULL: KVR_E_RANGE for an entry with a
+ *     location outside its place (which is left out), KVR_E_ARG for a request
+ *     id out of range (which attends to nothing), otherwise not written
+ *   workspace (device), aligned to 16 bytes: at least
+ *     kvr_attend_workspace(n, nq, heads, d_v, rows per query) bytes; written
+ *     by the call, so calls that may run at once (two streams, two graphs)
+ *     each need their own */
+typedef struct kvr_attend_call {
+    int32_t layer;
+    int32_t format;  /* kvr_row_format */
+    int32_t n;
+    int32_t nq;
+    int32_t heads;
+    int32_t d_v;
+    int32_t d_rope;
+    int32_t stride;
+    int32_t k;
+    float scale;
+    const int32_t *req_ids;
+    const uint32_t *loc;
+    const void *rows;
+    const int32_t *count;
+    const int32_t *map;
+    const void *q;
+    int64_t q_stride_entry;
+    int64_t q_stride_query;
+    int64_t q_stride_head;
+    void *out;
+    float *lse;
+    int32_t *status;
+    void *workspace;
+    size_t workspace_bytes;
+} kvr_attend_call;
+
+/* Attention of each request's new tokens over its resolved rows ("Adaptive
+ * DHiSparse", section "How it works", paragraph "Model-specific reuse":
+ * attention consumes the rows the location vector names):
+ *   s_j = scale * (q . key_j),  out = sum_j exp(s_j - lse) value_j,
+ *   lse = ln sum_j exp(s_j)
+ * over the entries of the query.  A query without any gets out = 0 and
+ * lse = -infinity.  Rows left out are not read, whatever they hold; a NaN in
+ * a row that takes part shows in the result.  Products of 16-bit values (an
+ * e4m3 code is exact in bf16), sums, maxima and exponentials in 32 bits;
+ * probabilities are rounded to 16 bits before their product with the values.
+ * A selection may be cut into shares that are attended to apart and joined in
+ * a fixed order: results do not vary from run to run.  One kernel, or two
+ * with shares. */
+int kvr_attend_rows(kvr_ctx *ctx, const kvr_attend_call *call, void *stream);
+
+/* Workspace bytes of kvr_attend_rows for calls of up to n entries, nq
+ * queries, heads heads and `rows` rows per query (k with a map, stride without
+ * one); 0 is possible.  Negative or too large arguments give KVR_E_ARG. */
+int64_t kvr_attend_workspace(int32_t n, int32_t nq, int32_t heads, int32_t d_v, int32_t rows);
+
+/* Pages shared between requests.
+ *
+ * A ready page is never written again, so several requests may map one
+ * physical page.  refs (device) int32 [pool_pages] counts, for each physical
+ * page, the page_map entries that name it; a page is free when its count is 0
+ * (the calls treat a count below 0 as free too).
+ *
+ * kvr_bind_page_refs: bind the counts (NULL: none, as after kvr_create).
+ *   While they are bound, kvr_reclaim_pages lowers the count of each page it
+ *   releases (freed_phys[i] still names the page entry i let go of, which is
+ *   free only once its count is 0) and kvr_restore_pages refuses a physical
+ *   page whose count is not 0 with KVR_E_STATE and sets the count of each page
+ *   it fills to 1.  kvr_residency_* expects each physical page in one map
+ *   entry: give entries pages of their own (kvr_copy_pages) before a map is
+ *   handed to it.
+ * kvr_count_page_refs: set the counts from page_map.
+ *
+ * The calls below need the counts bound when pool_pages > 0.
+ *
+ * kvr_release_requests: each listed request gives up its rows: the counts of
+ *   its pages go down, page_map becomes -1, host_valid 0, tags -1, stamps 0,
+ *   clock 0 and L 0.  Payload stays as it is.
+ * kvr_fork_requests: request dst_ids[i] becomes a copy of src_ids[i]: L,
+ *   clock, tags and stamps; the ready pages, shared; and of every payload layer
+ *   the tail ring, the hot slots with a tag, the host rows of imported pages
+ *   that have a host copy and are not ready, and those of decoded rows.  What
+ *   dst held before is given up as by kvr_release_requests.  In the copy a
+ *   ready page has no host copy (its backup is made when it is reclaimed).
+ *   Deferred appends of the source must have been completed.
+ *   src_ids, dst_ids (device) int32 [n]; a request may be the source of several
+ *   entries.  status (device) int32 [n] or NULL: KVR_E_ARG (nothing changes)
+ *   for an id out of range, a destination that an earlier entry names or a
+ *   request that is both a source and a destination of the call.
+ * kvr_copy_pages: request req_ids[i]'s ready page pages[i] is copied into
+ *   physical page phys[i], which it maps from then on; the old page's count
+ *   goes down.  status (device) int32 [n], required: KVR_E_ARG for a request or
+ *   page out of range, an incomplete page, or a page or physical page that an
+ *   earlier entry names; else KVR_E_RANGE for a physical page outside the pool;
+ *   else KVR_E_STATE for a page that is not ready or a physical page in use.
+ *   Entries are judged on the state before the call; a failed one changes
+ *   nothing.
+ * kvr_list_free_pages: free_list (device) int32 [pool_pages] receives the free
+ *   physical pages, ascending, in its first free_count[0] (device) entries;
+ *   the others are not written.
+ * kvr_compact_pool: while free pages lie below live ones, the highest live
+ *   page moves into the lowest free one, at most max_moves times: the payload
+ *   of every layer, its count and every page_map entry naming it.  moves
+ *   (device) int32 [min(max_moves, pool_pages)][2] receives (source,
+ *   destination) of each in that order, move_count (device) int32 [1] their
+ *   number.  After a call that reached no limit the live pages are the lowest.
+ *   Location words resolved before it that name pages no longer hold: no
+ *   compaction between a resolve and the gathers and attention that use it.
+ *   workspace (device), aligned to 4 bytes: kvr_pool_workspace(ctx) bytes, for
+ *   calls that may run at once one each.
+ * n is at most n_req for lists of requests, min(n_req * ceil(H/P), 65536) for
+ * lists of pages; n = 0 is a no-op. */
+int kvr_bind_page_refs(kvr_ctx *ctx, int32_t *refs);
+int kvr_count_page_refs(kvr_ctx *ctx, void *stream);
+int kvr_release_requests(kvr_ctx *ctx, int32_t n, const int32_t *req_ids, int32_t *status,
+                         void *stream);
+int kvr_fork_requests(kvr_ctx *ctx, int32_t n, const int32_t *src_ids, const int32_t *dst_ids,
+                      int32_t *status, void *stream);
+int kvr_copy_pages(kvr_ctx *ctx, int32_t n, const int32_t *req_ids, const int32_t *pages,
+                   const int32_t *phys, int32_t *status, void *stream);
+int64_t kvr_pool_workspace(const kvr_ctx *ctx);
+int kvr_list_free_pages(kvr_ctx *ctx, int32_t *free_list, int32_t *free_count, void *workspace,
+                        size_t workspace_bytes, void *stream);
+int kvr_compact_pool(kvr_ctx *ctx, int32_t max_moves, int32_t *moves, int32_t *move_count,
+                     void *workspace, size_t workspace_bytes, void *stream);
+
 /* Host-side residency policy of one KV source's optional pool (no device
  * work; the caller applies its decisions with the two calls above).
  *
@@ -553,6 +756,9 @@ typedef enum kvr_kernel {
     KVR_KERNEL_STATE = 5,    /* state initialisation, location copies */
     KVR_KERNEL_FUSED = 6,    /* fill pass and resident gather in one launch */
     KVR_KERNEL_STEP = 7,     /* a fused gather beside the next resolve */
+    KVR_KERNEL_ATTEND = 8,   /* attention over resolved rows, and the join of its shares */
+    KVR_KERNEL_PACK = 9,     /* rows of new tokens */
+    KVR_KERNEL_PAGES = 10,   /* fork, release, page copies, free list, compaction */
 } kvr_kernel;
 
 int kvr_timing_begin(kvr_ctx *ctx, int32_t capacity);
