@@ -1,4 +1,40 @@
-// Attention of new tokens over resolved rows.
+// Attention of new tokens over resolved rows ("Adaptive DHiSparse:
+// Speculative Decoding over a Load-Adaptive KV Hierarchy", section "How it
+// works", paragraph "Model-specific reuse": attention consumes the rows that
+// the location vector names).
+//
+// A row is one token's latent c (d_v values) and rope part r; its key is
+// (c, r), its value c, shared by all heads.  For a query row x (a head of a
+// query) over the rows j it attends to:
+//   t_j = log2(e) * scale * (q . key_j),  p_j = 2^(t_j - m),  l = sum p_j,
+//   out = sum p_j c_j / l,                lse = ln 2 * (m + log2 l)
+// with one pass over the rows: m is a reference at most 8 below the running
+// maximum (so p <= 2^8); when a tile exceeds it, it becomes the maximum and l
+// and the sums are scaled down.
+//
+// A workgroup of NW waves owns MB blocks of 16 query rows and a share of the
+// selection, which it walks in tiles of 64 rows, two tiles in LDS: while one
+// is worked on, the next is on its way (16-byte direct loads to LDS, addresses
+// from the location words, which are read a tile earlier still).
+//   scores   wave w computes 16 of the tile's rows (w mod 4) for its part of
+//            the query rows (w / 4), by 16x16x32 MFMA with the keys from LDS
+//            and the queries in registers;
+//   values   every wave takes d_v / NW columns of all query rows; the
+//            probabilities pass through LDS, the latents are read transposed
+//            (ds_read_tr), so the product needs no copy of the tile.
+// Both products leave a query row in one lane (mod 16), so the running
+// maximum, the sums and their corrections stay in registers.
+//
+// 16-byte chunks of a row lie in LDS at chunk ^ swizzle(row): the 8 (keys) or
+// 4 (latents) rows that a read touches at once are then in different banks.
+// The permutation is applied to the source address of the direct loads.
+//
+// 8-bit rows stay 8-bit in LDS.  Codes are exact in bf16, so no product is
+// rounded: the scores sum each 128-value group apart and weigh it with its
+// scale, and the probabilities are multiplied by the row's scale of the
+// columns' group before they are rounded to bf16.
+//
+// Rows left out are read from a row of zeros and their p is 0.
 #include "block.h"
 #include "kvr_internal.h"
 #include "rowformat.h"
@@ -6,25 +42,112 @@
 namespace kvr {
 namespace {
 
-constexpr int NT = 256;
+constexpr int kTile = 64;     // rows per tile
+constexpr float kSlack = 8.f; // log2 of the largest probability kept
+constexpr int kRowGroups = kTile / 16;
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// A workgroup barrier that leaves direct loads to LDS in flight (the next
+// tile's), unlike __syncthreads.
+__device__ __forceinline__ void barrier_lds()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// The same once this wave's direct loads have arrived.
+__device__ __forceinline__ void barrier_all()
+{
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+#define LDS_PTR(T, p) ((__attribute__((address_space(3))) T *)(p))
+#define GLOBAL_PTR(T, p) ((const __attribute__((address_space(1))) T *)(p))
+
+// What a row that is left out is read from (the longest row is 1152 bytes).
+__device__ __attribute__((aligned(16))) uint8_t zero_row[1152];
 
 struct AttendArgs {
     Shape sh;
-    const LayerPtrs *layers;
+    const LayerPtrs *layers;  // device table
     kvr_attend_call c;
+    int32_t units;      // selections: entries, or (entry, query) with a map
+    int32_t unit_rows;  // query rows that share a selection
+    int32_t groups;     // workgroups per selection and share
+    int32_t shares;
+    bool wide;          // q may be read 16 bytes at a time
+    float *partial;     // [units][shares][unit_rows][d_v], with shares > 1
+    float *stat;        // [units][shares][unit_rows][2]: m, l
 };
 
-// Address of entry j of request entry i, or null when it is left out.
-__device__ __forceinline__ const uint8_t *row_address(const AttendArgs &a, const LayerPtrs &lp, int i,
-                                                      int r, int64_t j, bool &bad)
+// MFMA operands of a 16-bit type.
+template <typename E>
+struct Mfma;
+template <>
+struct Mfma<__bf16> {
+    typedef __bf16 frag __attribute__((ext_vector_type(8)));
+    static __device__ __forceinline__ f32x4 mul(frag a, frag b, f32x4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+};
+template <>
+struct Mfma<_Float16> {
+    typedef _Float16 frag __attribute__((ext_vector_type(8)));
+    static __device__ __forceinline__ f32x4 mul(frag a, frag b, f32x4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    }
+};
+
+// Swizzle of a row: bijective on any 8 consecutive rows, and different in its
+// upper two bits on any 4 (a transposed 16-bit read takes pairs of chunks).
+__device__ __forceinline__ constexpr int swizzle(int row)
+{
+    return ((row & 3) << 1) | ((row >> 2) & 1);
+}
+
+// 8 e4m3 codes as bf16 values.
+__device__ __forceinline__ Mfma<__bf16>::frag widen(uint32_t lo, uint32_t hi)
+{
+    typedef Mfma<__bf16>::frag frag;
+    frag f;
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+    f[0] = a[0], f[1] = a[1], f[2] = b[0], f[3] = b[1];
+    f[4] = c[0], f[5] = c[1], f[6] = d[0], f[7] = d[1];
+    return f;
+}
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// The rows of one (entry, query) and where they are read.
+struct RowList {
+    const int32_t *map;   // this query's entries of the union, or null
+    const uint32_t *loc;  // this entry's words, or null
+    const uint8_t *rows;  // this entry's gathered rows, or null
+    int len;              // entries of the list
+    int count;            // entries of the selection
+};
+
+// Address of the row of word w (position j of the selection), or null when it
+// is left out.
+__device__ __forceinline__ const uint8_t *row_address(const AttendArgs &a, const LayerPtrs &lp,
+                                                      const RowList &list, int r, int j, uint32_t w,
+                                                      bool &bad)
 {
     bad = false;
-    const int64_t e = (int64_t)i * a.c.stride + j;
-    const uint32_t w = a.c.loc ? a.c.loc[e] : 0;
     if (w == KVR_LOC_INVALID)
         return nullptr;
-    if (a.c.rows)
-        return static_cast<const uint8_t *>(a.c.rows) + e * a.sh.R;
+    if (list.rows)
+        return list.rows + (int64_t)j * a.sh.R;
     const uint32_t place = w >> kPlaceShift, idx = w & kIndexMask;
     if (place == KVR_PLACE_TAIL && idx < (uint32_t)a.sh.T)
         return lp.tail + ((int64_t)r * a.sh.T + idx) * a.sh.R;
@@ -36,119 +159,577 @@ __device__ __forceinline__ const uint8_t *row_address(const AttendArgs &a, const
     return nullptr;
 }
 
-template <int FMT>
-__device__ float key_value(const uint8_t *row, int d_v, int d)
+// A tile in LDS: latents, rope parts and (8-bit rows) scales, each part
+// [kTile rows][its bytes].
+template <int FMT, int DV, int DR>
+struct Tile {
+    static constexpr bool kFp8 = FMT == KVR_ROW_FP8;
+    static constexpr int kLatent = kFp8 ? DV : 2 * DV;  // bytes of a row's parts
+    static constexpr int kRope = 2 * DR;
+    static constexpr int kScales = kFp8 ? scale_bytes(DV) : 0;
+    static constexpr int kRopeAt = kTile * kLatent;
+    static constexpr int kScalesAt = kRopeAt + kTile * kRope;
+    static constexpr int kBytes = kScalesAt + kTile * kScales;
+
+    // Loads rows [first, first + ROWS) of the tile, lane i < ROWS holding the
+    // address of row first + i.  Each instruction writes 1024 consecutive
+    // bytes of a part.
+    template <int ROWS>
+    static __device__ __forceinline__ void load(uint8_t *lds, int first, const uint8_t *row)
+    {
+        const int lane = lane_id();
+        const uint32_t lo = (uint32_t)(uintptr_t)row, hi = (uint32_t)((uintptr_t)row >> 32);
+        auto part = [&](auto per_row, int at, int from) {
+            constexpr int C = decltype(per_row)::value / 16;  // chunks per row
+            constexpr int N = 64 / C;                         // rows per instruction
+            static_assert(ROWS % N == 0, "a wave loads whole instructions");
+#pragma unroll
+            for (int i = 0; i < ROWS; i += N) {
+                const int k = i + lane / C;
+                const uint64_t p = (uint64_t)__shfl((int)lo, k) & 0xFFFFFFFFull;
+                const uint64_t ph = (uint64_t)(uint32_t)__shfl((int)hi, k) << 32;
+                const int chunk = (lane % C) ^ swizzle(first + k);
+                const uint8_t *src =
+                    reinterpret_cast<const uint8_t *>(ph | p) + from + chunk * 16;
+                __builtin_amdgcn_global_load_lds(GLOBAL_PTR(uint32_t, src),
+                                                 LDS_PTR(uint32_t, lds + at + (first + i) * C * 16),
+                                                 16, 0, 0);
+            }
+        };
+        part(std::integral_constant<int, kLatent>(), 0, 0);
+        if constexpr (DR > 0)
+            part(std::integral_constant<int, kRope>(), kRopeAt, kLatent + kScales);
+        if constexpr (kFp8)
+            if (lane < ROWS)
+                __builtin_amdgcn_global_load_lds(GLOBAL_PTR(uint32_t, row + kLatent),
+                                                 LDS_PTR(uint32_t, lds + kScalesAt + first * 16),
+                                                 16, 0, 0);
+    }
+};
+
+template <int FMT, int DV, int DR, int MB, int NW>
+__global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
 {
     typedef typename Elem<FMT>::type E;
-    if constexpr (FMT == KVR_ROW_FP8) {
-        if (d >= d_v)
-            return (float)reinterpret_cast<const E *>(row + d_v + scale_bytes(d_v))[d - d_v];
-        const float sc = reinterpret_cast<const float *>(row + d_v)[d / kScaleGroup];
-        return __builtin_amdgcn_cvt_f32_fp8((int)row[d], 0) * sc;
-    } else {
-        return (float)reinterpret_cast<const E *>(row)[d];
+    typedef Mfma<E> M;
+    typedef typename M::frag frag;
+    typedef Tile<FMT, DV, DR> TL;
+    constexpr bool kFp8 = FMT == KVR_ROW_FP8;
+    constexpr int kSteps = (DV + DR) / 32;        // MFMA steps of a score
+    constexpr int kHeadGroups = NW / kRowGroups;  // waves that share 16 rows of the tile
+    constexpr int MQ = MB / kHeadGroups;          // score blocks of a wave
+    constexpr int NC = DV / NW / 16;              // value column blocks of a wave
+    constexpr int kGroups = kFp8 ? DV / kScaleGroup : 1;
+    constexpr int kPitch = kTile + 8;             // of a query row's probabilities
+    constexpr int kRows = kTile / NW;             // rows a wave loads
+    static_assert(MB % kHeadGroups == 0 && DV % (NW * 16) == 0, "");
+
+    __shared__ __attribute__((aligned(1024))) uint8_t buf0[TL::kBytes];
+    __shared__ __attribute__((aligned(1024))) uint8_t buf1[TL::kBytes];
+    __shared__ __attribute__((aligned(16))) E sP[kGroups][MB * 16][kPitch];
+    __shared__ float sMax[kRowGroups][MB * 16];
+    __shared__ __attribute__((aligned(8))) uint8_t sValid[2][kTile / 8];
+    __shared__ int sExceeds[2];
+
+    const int lane = lane_id(), col = lane & 15, grp = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(wave_id());
+    const int rg = wave % kRowGroups, hg = wave / kRowGroups;
+
+    // workgroups of one selection and share are 8 apart: the same XCD's L2
+    // serves their rows
+    const int64_t b = blockIdx.x;
+    const int64_t us = b / (8 * a.groups) * 8 + (b & 7);
+    const int g = (int)(b / 8 % a.groups);
+    if (us >= (int64_t)a.units * a.shares)
+        return;
+    const int unit = (int)(us / a.shares), share = (int)(us % a.shares);
+    const int i = a.c.map ? unit / a.c.nq : unit;
+    const int r = a.c.req_ids ? a.c.req_ids[i] : i;
+    const bool known = r >= 0 && r < a.sh.n_req;
+
+    RowList list;
+    int cnt = a.c.count ? a.c.count[i] : a.c.stride;
+    list.count = known ? (cnt < 0 ? 0 : (cnt > a.c.stride ? a.c.stride : cnt)) : 0;
+    list.len = a.c.map ? (known ? a.c.k : 0) : list.count;
+    list.map = a.c.map ? a.c.map + (int64_t)unit * a.c.k : nullptr;
+    list.loc = a.c.loc ? a.c.loc + (int64_t)i * a.c.stride : nullptr;
+    list.rows = a.c.rows ? static_cast<const uint8_t *>(a.c.rows) +
+                               (int64_t)i * a.c.stride * a.sh.R
+                         : nullptr;
+    if (!known && a.c.status && threadIdx.x == 0)
+        a.c.status[i] = KVR_E_ARG;
+    LayerPtrs lp{};
+    if (!list.rows && list.len > 0)
+        lp = a.layers[a.c.layer];
+
+    const int tiles = (list.len + kTile - 1) / kTile;
+    const int per = (tiles + a.shares - 1) / a.shares;
+    const int t0 = share * per;
+    const int t1 = t0 + per < tiles ? t0 + per : tiles;
+
+    // query row x of the unit: query x / heads, head x % heads (with a map the
+    // unit is one query)
+    const E *q = static_cast<const E *>(a.c.q) + (int64_t)i * a.c.q_stride_entry;
+    const int x0 = g * (MB * 16);
+    frag qf[MQ][kSteps];
+#pragma unroll
+    for (int mb = 0; mb < MQ; ++mb) {
+        const int x = x0 + (hg * MQ + mb) * 16 + col;
+        const bool in = x < a.unit_rows && t0 < t1;
+        const int xc = in ? x : 0;
+        const int qi = a.c.map ? unit % a.c.nq : xc / a.c.heads;
+        const int h = a.c.map ? xc : xc % a.c.heads;
+        const E *p = q + (int64_t)qi * a.c.q_stride_query + (int64_t)h * a.c.q_stride_head;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            // an 8-bit key fragment holds 8 of the 16 codes of one LDS read
+            const int d = kFp8 && s < DV / 32 ? s / 2 * 64 + grp * 16 + (s & 1) * 8
+                                              : s * 32 + grp * 8;
+            frag f;
+            if (a.wide) {
+                f = *reinterpret_cast<const frag *>(p + d);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    f[e] = p[d + e];
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                f[e] = in ? f[e] : (E)0.f;
+            qf[mb][s] = f;
+        }
+    }
+
+    // m: the reference of this lane's query row in each block; mq, l: those of
+    // the wave's own score blocks and this lane's share of their sums
+    float m[MB], mq[MQ], l[MQ];
+    f32x4 o[NC][MB];
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+        m[mb] = -__builtin_inff();
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+            o[c][mb] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+#pragma unroll
+    for (int mb = 0; mb < MQ; ++mb) {
+        mq[mb] = -__builtin_inff();
+        l[mb] = 0.f;
+    }
+    if (threadIdx.x < 2)
+        sExceeds[threadIdx.x] = 0;
+
+    // The list's entry at this lane's row of tile t (a wave's first kRows
+    // lanes): its position in the selection, its word, its address.
+    const int mine = wave * kRows + (lane & (kRows - 1));
+    auto position = [&](int t) {
+        const int j = t * kTile + mine;
+        int e = -1;
+        if (t < t1 && j < list.len)
+            e = list.map ? list.map[j] : j;
+        return e >= 0 && e < list.count ? e : -1;
+    };
+    auto word = [&](int e) { return e >= 0 ? (list.loc ? list.loc[e] : 0u) : KVR_LOC_INVALID; };
+    auto address = [&](int e, uint32_t w) {
+        bool bad = false;
+        const uint8_t *p = e >= 0 ? row_address(a, lp, list, r, e, w, bad) : nullptr;
+        if (bad && a.c.status)
+            a.c.status[i] = KVR_E_RANGE;
+        return p;
+    };
+    // Starts tile t's loads into a buffer and notes which of its rows count.
+    auto fetch = [&](uint8_t *buf, int t, const uint8_t *row) {
+        const uint64_t valid = __ballot(row != nullptr);
+        if (lane == 0) {
+            if constexpr (kRows == 8)
+                sValid[t & 1][wave] = (uint8_t)valid;
+            else
+                reinterpret_cast<uint16_t *>(sValid[t & 1])[wave] = (uint16_t)valid;
+        }
+        TL::template load<kRows>(buf, wave * kRows, row ? row : zero_row);
+    };
+
+    const float to_log2 = a.c.scale * 1.44269504088896340736f;
+
+    // Tile t out of cur, while tile t + 1 (row: its addresses) is loaded into
+    // nxt; e: the positions of tile t + 2.
+    auto step = [&](const uint8_t *cur, uint8_t *nxt, int t, const uint8_t *&row, int &e) {
+        // tile t has arrived, and no wave reads nxt any more
+        barrier_all();
+        const uint32_t w2 = word(e);
+        const int e3 = position(t + 3);
+        if (t + 1 < t1)
+            fetch(nxt, t + 1, row);
+        if (threadIdx.x == 0)
+            sExceeds[(t + 1) & 1] = 0;
+
+        // scores of this wave's 16 rows
+        f32x4 s[MQ];
+        const int krow = rg * 16 + col;
+        float sc[kFp8 ? 4 : 1][kGroups];  // scales of this lane's 4 rows
+#pragma unroll
+        for (int mb = 0; mb < MQ; ++mb)
+            s[mb] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if constexpr (DR > 0) {
+            const uint8_t *base = cur + TL::kRopeAt + krow * TL::kRope;
+#pragma unroll
+            for (int st = 0; st < DR / 32; ++st) {
+                const int chunk = (st * 4 + grp) ^ swizzle(krow);
+                const frag kf = *reinterpret_cast<const frag *>(base + chunk * 16);
+#pragma unroll
+                for (int mb = 0; mb < MQ; ++mb)
+                    s[mb] = M::mul(kf, qf[mb][DV / 32 + st], s[mb]);
+            }
+        }
+        const uint8_t *base = cur + krow * TL::kLatent;
+        if constexpr (kFp8) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float *p = reinterpret_cast<const float *>(cur + TL::kScalesAt +
+                                                                 (rg * 16 + grp * 4 + k) * 16);
+#pragma unroll
+                for (int gi = 0; gi < kGroups; ++gi)
+                    sc[k][gi] = p[gi];
+            }
+#pragma unroll
+            for (int gi = 0; gi < kGroups; ++gi) {
+                f32x4 part[MQ];
+#pragma unroll
+                for (int mb = 0; mb < MQ; ++mb)
+                    part[mb] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int chunk = (gi * 8 + h * 4 + grp) ^ swizzle(krow);
+                    const u32x4 v = *reinterpret_cast<const u32x4 *>(base + chunk * 16);
+                    const frag k0 = widen(v[0], v[1]), k1 = widen(v[2], v[3]);
+#pragma unroll
+                    for (int mb = 0; mb < MQ; ++mb) {
+                        part[mb] = M::mul(k0, qf[mb][gi * 4 + h * 2], part[mb]);
+                        part[mb] = M::mul(k1, qf[mb][gi * 4 + h * 2 + 1], part[mb]);
+                    }
+                }
+#pragma unroll
+                for (int mb = 0; mb < MQ; ++mb)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        s[mb][k] = fmaf(part[mb][k], sc[k][gi], s[mb][k]);
+            }
+        } else {
+#pragma unroll
+            for (int st = 0; st < DV / 32; ++st) {
+                const int chunk = (st * 4 + grp) ^ swizzle(krow);
+                const frag kf = *reinterpret_cast<const frag *>(base + chunk * 16);
+#pragma unroll
+                for (int mb = 0; mb < MQ; ++mb)
+                    s[mb] = M::mul(kf, qf[mb][st], s[mb]);
+            }
+        }
+
+        // t_j of the rows that count; whether one exceeds its reference
+        const uint64_t valid = *reinterpret_cast<const uint64_t *>(sValid[t & 1]);
+        const uint32_t mask = (uint32_t)(valid >> (rg * 16 + grp * 4)) & 15u;
+        bool exceeds = false;
+#pragma unroll
+        for (int mb = 0; mb < MQ; ++mb) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                s[mb][k] = (mask >> k) & 1 ? s[mb][k] * to_log2 : -__builtin_inff();
+                exceeds |= s[mb][k] > mq[mb] + kSlack;
+            }
+        }
+        if (__any(exceeds) && lane == 0)
+            sExceeds[t & 1] = 1;
+        float sum[MQ];
+        auto write_p = [&]() {
+#pragma unroll
+            for (int mb = 0; mb < MQ; ++mb) {
+                const float ref = mq[mb] == -__builtin_inff() ? 0.f : mq[mb];
+                float p[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    p[k] = exp2_hw(s[mb][k] - ref);
+                sum[mb] = (p[0] + p[1]) + (p[2] + p[3]);
+#pragma unroll
+                for (int gi = 0; gi < kGroups; ++gi) {
+                    typedef E e4 __attribute__((ext_vector_type(4)));
+                    e4 v;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if constexpr (kFp8)
+                            v[k] = (E)(p[k] * sc[k][gi]);
+                        else
+                            v[k] = (E)p[k];
+                    }
+                    *reinterpret_cast<e4 *>(&sP[gi][(hg * MQ + mb) * 16 + col][rg * 16 + grp * 4]) = v;
+                }
+            }
+        };
+        write_p();
+        barrier_lds();
+        if (sExceeds[t & 1]) {
+            // the maximum becomes the reference: sums so far are scaled down,
+            // this tile's probabilities written again
+#pragma unroll
+            for (int mb = 0; mb < MQ; ++mb) {
+                float top = fmaxf(fmaxf(s[mb][0], s[mb][1]), fmaxf(s[mb][2], s[mb][3]));
+                top = fmaxf(top, __shfl_xor(top, 16));
+                top = fmaxf(top, __shfl_xor(top, 32));
+                if (grp == 0)
+                    sMax[rg][(hg * MQ + mb) * 16 + col] = top;
+            }
+            barrier_lds();
+            float alpha[MB];
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb) {
+                float top = m[mb];
+#pragma unroll
+                for (int k = 0; k < kRowGroups; ++k)
+                    top = fmaxf(top, sMax[k][mb * 16 + col]);
+                alpha[mb] = top == -__builtin_inff() ? 1.f : exp2_hw(m[mb] - top);
+                m[mb] = top;
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+                    o[c][mb] *= alpha[mb];
+            }
+#pragma unroll
+            for (int mb = 0; mb < MQ; ++mb) {
+                // the wave's own blocks (constant register indices)
+                mq[mb] = m[mb];
+                float al = alpha[mb];
+                if constexpr (kHeadGroups == 2) {
+                    mq[mb] = hg ? m[MQ + mb] : mq[mb];
+                    al = hg ? alpha[MQ + mb] : al;
+                }
+                l[mb] *= al;
+            }
+            write_p();
+            barrier_lds();
+        }
+#pragma unroll
+        for (int mb = 0; mb < MQ; ++mb)
+            l[mb] += sum[mb];
+
+        // values: o[column][query row] += latent[row][column] * p[query row][row]
+        const int gi = kFp8 ? wave * (DV / NW) / kScaleGroup : 0;
+#pragma unroll
+        for (int st = 0; st < kTile / 32; ++st) {
+            frag pf[MB];
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb)
+                pf[mb] = *reinterpret_cast<const frag *>(&sP[gi][mb * 16 + col][st * 32 + grp * 8]);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const int cb = wave * NC + c;  // block of 16 columns
+                frag vf;
+                if constexpr (kFp8) {
+                    const int vrow = st * 32 + grp * 8 + (col >> 1);
+                    const int chunk = cb ^ swizzle(vrow);
+                    const i32x2 v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                        LDS_PTR(i32x2, cur + vrow * TL::kLatent + chunk * 16 + (col & 1) * 8));
+                    vf = widen((uint32_t)v[0], (uint32_t)v[1]);
+                } else {
+                    union {
+                        s16x4 half[2];
+                        frag f;
+                    } u;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int vrow = st * 32 + grp * 8 + h * 4 + (col >> 2);
+                        const int chunk = (cb * 2 + ((col >> 1) & 1)) ^ swizzle(vrow);
+                        u.half[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                            LDS_PTR(s16x4, cur + vrow * TL::kLatent + chunk * 16 + (col & 1) * 8));
+                    }
+                    vf = u.f;
+                }
+#pragma unroll
+                for (int mb = 0; mb < MB; ++mb)
+                    o[c][mb] = M::mul(vf, pf[mb], o[c][mb]);
+            }
+        }
+        row = address(e, w2);
+        e = e3;
+    };
+
+    if (t0 < t1) {
+        const int e0 = position(t0), e1 = position(t0 + 1);
+        int e = position(t0 + 2);
+        const uint32_t w0 = word(e0), w1 = word(e1);
+        const uint8_t *row = address(e0, w0);
+        fetch(buf0, t0, row);
+        row = address(e1, w1);
+        for (int t = t0; t < t1; t += 2) {
+            step(buf0, buf1, t, row, e);
+            if (t + 1 < t1)
+                step(buf1, buf0, t + 1, row, e);
+        }
+    }
+
+    // the sums of the four waves (and 4 lane groups) that share a query row
+#pragma unroll
+    for (int mb = 0; mb < MQ; ++mb) {
+        l[mb] += __shfl_xor(l[mb], 16);
+        l[mb] += __shfl_xor(l[mb], 32);
+    }
+    barrier_lds();
+#pragma unroll
+    for (int mb = 0; mb < MQ; ++mb)
+        if (grp == 0)
+            sMax[rg][(hg * MQ + mb) * 16 + col] = l[mb];
+    barrier_lds();
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+        const int x = x0 + mb * 16 + col;
+        if (x >= a.unit_rows)
+            continue;
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < kRowGroups; ++k)
+            sum += sMax[k][mb * 16 + col];
+        const int64_t at = (int64_t)unit * a.unit_rows + x;  // query row of the call
+        const int c0 = wave * (DV / NW) + grp * 4;
+        if (a.shares > 1) {
+            const int64_t ps = us * a.unit_rows + x;
+            if (wave == 0 && grp == 0)
+                *reinterpret_cast<float2 *>(a.stat + 2 * ps) = make_float2(m[mb], sum);
+            if (m[mb] == -__builtin_inff() && sum == 0.f)
+                continue;  // an empty share: its sums are not read
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                *reinterpret_cast<f32x4 *>(a.partial + ps * DV + c0 + c * 16) = o[c][mb];
+            continue;
+        }
+        const float inv = m[mb] == -__builtin_inff() && sum == 0.f ? 0.f : 1.f / sum;
+        if (wave == 0 && grp == 0 && a.c.lse)
+            a.c.lse[at] = 0.69314718055994530942f * (m[mb] + __log2f(sum));
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            typedef E e4 __attribute__((ext_vector_type(4)));
+            e4 v;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                v[k] = (E)(o[c][mb][k] * inv);
+            *reinterpret_cast<e4 *>(static_cast<E *>(a.c.out) + at * DV + c0 + c * 16) = v;
+        }
     }
 }
 
-// One workgroup per (entry, query, head), one row per thread and step.
-template <int FMT>
-__global__ __launch_bounds__(NT) void attend_kernel(AttendArgs a)
+// Joins the shares of each query row, in their order: a workgroup per row.
+template <typename E, int DV>
+__global__ __launch_bounds__(DV / 4) void join_kernel(AttendArgs a)
 {
-    typedef typename Elem<FMT>::type E;
-    __shared__ float sQ[576], sP[NT], sRed[NT];
-    __shared__ const uint8_t *sRow[NT];
-    const int64_t b = blockIdx.x;
-    const int h = (int)(b % a.c.heads), qi = (int)(b / a.c.heads % a.c.nq),
-              i = (int)(b / a.c.heads / a.c.nq);
-    const int r = a.c.req_ids ? a.c.req_ids[i] : i;
-    const bool badr = r < 0 || r >= a.sh.n_req;
-    int cnt = a.c.count ? a.c.count[i] : a.c.stride;
-    cnt = cnt < 0 ? 0 : (cnt > a.c.stride ? a.c.stride : cnt);
-    const int D = a.c.d_v + a.c.d_rope;
-    const E *q = static_cast<const E *>(a.c.q) + i * a.c.q_stride_entry +
-                 qi * a.c.q_stride_query + h * a.c.q_stride_head;
-    for (int d = threadIdx.x; d < D; d += NT)
-        sQ[d] = (float)q[d];
-    const int n = badr ? 0 : (a.c.map ? a.c.k : cnt);
-    if (badr && threadIdx.x == 0 && a.c.status)
-        a.c.status[i] = KVR_E_ARG;
-    LayerPtrs lp{};
-    if (!a.c.rows && n > 0)
-        lp = a.layers[a.c.layer];
-    float m = -__builtin_inff(), l = 0.f, o[2] = {0.f, 0.f};
-    for (int j0 = 0; j0 < n; j0 += NT) {
-        __syncthreads();
-        const int j = j0 + threadIdx.x;
-        const uint8_t *row = nullptr;
-        if (j < n) {
-            const int64_t e = a.c.map ? a.c.map[((int64_t)i * a.c.nq + qi) * a.c.k + j] : j;
-            bool bad = false;
-            if (e >= 0 && e < cnt)
-                row = row_address(a, lp, i, r, e, bad);
-            if (bad && a.c.status)
-                a.c.status[i] = KVR_E_RANGE;
-        }
-        float s = -__builtin_inff();
-        if (row) {
-            s = 0.f;
-            for (int d = 0; d < D; ++d)
-                s += sQ[d] * key_value<FMT>(row, a.c.d_v, d);
-            s *= a.c.scale;
-        }
-        sRow[threadIdx.x] = row;
-        sRed[threadIdx.x] = s;
-        __syncthreads();
-        float mt = m;
-        for (int t = 0; t < NT; ++t)
-            mt = (mt > sRed[t] || mt != mt) ? mt : sRed[t];
-        const float base = mt == -__builtin_inff() ? 0.f : mt;
-        const float alpha = expf(m - base);
-        sP[threadIdx.x] = row ? expf(s - base) : 0.f;
-        __syncthreads();
-        l *= alpha;
-        o[0] *= alpha;
-        o[1] *= alpha;
-        for (int t = 0; t < NT; ++t) {
-            if (!sRow[t])
-                continue;
-            l += sP[t];
-            for (int u = 0; u < 2; ++u) {
-                const int d = u * NT + threadIdx.x;
-                if (d < a.c.d_v)
-                    o[u] += sP[t] * key_value<FMT>(sRow[t], a.c.d_v, d);
-            }
-        }
-        m = mt;
+    const int64_t at = blockIdx.x;
+    const int unit = (int)(at / a.unit_rows), x = (int)(at % a.unit_rows);
+    const int64_t first = (int64_t)unit * a.shares * a.unit_rows + x;
+    float m = -__builtin_inff();
+    for (int s = 0; s < a.shares; ++s)
+        m = fmaxf(m, a.stat[2 * (first + (int64_t)s * a.unit_rows)]);
+    float l = 0.f;
+    f32x4 o{0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < a.shares; ++s) {
+        const int64_t ps = first + (int64_t)s * a.unit_rows;
+        const float2 st = *reinterpret_cast<const float2 *>(a.stat + 2 * ps);
+        if (st.x == -__builtin_inff() && st.y == 0.f)
+            continue;
+        const float w = st.x == -__builtin_inff() ? 1.f : exp2_hw(st.x - m);
+        l += w * st.y;
+        o += w * *reinterpret_cast<const f32x4 *>(a.partial + ps * DV + threadIdx.x * 4);
     }
-    E *out = static_cast<E *>(a.c.out) + b * a.c.d_v;
-    for (int u = 0; u < 2; ++u) {
-        const int d = u * NT + threadIdx.x;
-        if (d < a.c.d_v)
-            out[d] = (E)(m == -__builtin_inff() ? 0.f : o[u] / l);
-    }
+    const float inv = m == -__builtin_inff() && l == 0.f ? 0.f : 1.f / l;
+    typedef E e4 __attribute__((ext_vector_type(4)));
+    e4 v;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        v[k] = (E)(o[k] * inv);
+    *reinterpret_cast<e4 *>(static_cast<E *>(a.c.out) + at * DV + threadIdx.x * 4) = v;
     if (threadIdx.x == 0 && a.c.lse)
-        a.c.lse[b] = m == -__builtin_inff() ? m : m + logf(l);
+        a.c.lse[at] = 0.69314718055994530942f * (m + __log2f(l));
 }
+
+template <int FMT, int DV, int DR>
+hipError_t launch_dims(const kvr_ctx *c, const AttendArgs &a, int block, dim3 grid, hipStream_t s)
+{
+    if (block == 16)
+        return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 1, 4>, grid, dim3(256), 0, s, a);
+    if (block == 32)
+        return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 2, 8>, grid, dim3(512), 0, s, a);
+    return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 4, 8>, grid, dim3(512), 0, s, a);
+}
+
+template <int FMT>
+hipError_t launch_format(const kvr_ctx *c, const AttendArgs &a, int block, dim3 grid, hipStream_t s)
+{
+    if (a.c.d_v == 512)
+        return a.c.d_rope ? launch_dims<FMT, 512, 64>(c, a, block, grid, s)
+                          : launch_dims<FMT, 512, 0>(c, a, block, grid, s);
+    return a.c.d_rope ? launch_dims<FMT, 256, 64>(c, a, block, grid, s)
+                      : launch_dims<FMT, 256, 0>(c, a, block, grid, s);
+}
+
+constexpr int64_t kWorkgroups = 256;  // compute units: one workgroup each
+
+int64_t partial_bytes(int64_t rows, int32_t d_v) { return rows * (d_v + 2) * (int64_t)sizeof(float); }
 
 }  // namespace
 
-AttendPlan attend_plan(int32_t, int32_t, int32_t, int32_t, int32_t, bool)
+// A selection shared by unit_rows query rows is cut into blocks of at most 64
+// of them, and into shares (of at least one tile) until every compute unit has
+// a workgroup.
+AttendPlan attend_plan(int32_t n, int32_t nq, int32_t heads, int32_t d_v, int32_t rows, bool mapped)
 {
-    return AttendPlan{1, 1, 1, 0};
+    AttendPlan p{};
+    const int64_t units = mapped ? (int64_t)n * nq : n;
+    const int32_t unit_rows = mapped ? heads : nq * heads;
+    p.block = unit_rows <= 16 ? 16 : unit_rows <= 32 ? 32 : 64;
+    p.groups = (unit_rows + p.block - 1) / p.block;
+    const int64_t tiles = (rows + kTile - 1) / kTile;
+    int64_t shares = kWorkgroups / (units * p.groups);
+    shares = shares < tiles ? shares : tiles;
+    p.shares = (int32_t)(shares < 1 ? 1 : shares);
+    p.workspace = p.shares > 1 ? partial_bytes(units * p.shares * unit_rows, d_v) : 0;
+    return p;
 }
 
-int64_t attend_workspace_bound(int32_t, int32_t, int32_t, int32_t, int32_t) { return 0; }
+// Over all smaller calls: their query rows times shares are at most the query
+// rows times tiles, and at most a block of 64 for each workgroup.
+int64_t attend_workspace_bound(int32_t n, int32_t nq, int32_t heads, int32_t d_v, int32_t rows)
+{
+    const int64_t all = (int64_t)n * nq * heads, tiles = (rows + kTile - 1) / kTile;
+    const int64_t most = all * tiles;
+    if (tiles < 2)
+        return 0;
+    return partial_bytes(most < kWorkgroups * 64 ? most : kWorkgroups * 64, d_v);
+}
 
-hipError_t launch_attend(const kvr_ctx *c, const kvr_attend_call &call, const AttendPlan &,
+hipError_t launch_attend(const kvr_ctx *c, const kvr_attend_call &call, const AttendPlan &plan,
                          hipStream_t s)
 {
-    AttendArgs a{c->shape, c->layers_d, call};
-    const dim3 grid((unsigned)((int64_t)call.n * call.nq * call.heads));
-    if (call.format == KVR_ROW_FP8)
-        return launch(c, KVR_KERNEL_ATTEND, attend_kernel<KVR_ROW_FP8>, grid, dim3(NT), 0, s, a);
-    if (call.format == KVR_ROW_BF16)
-        return launch(c, KVR_KERNEL_ATTEND, attend_kernel<KVR_ROW_BF16>, grid, dim3(NT), 0, s, a);
-    return launch(c, KVR_KERNEL_ATTEND, attend_kernel<KVR_ROW_F16>, grid, dim3(NT), 0, s, a);
+    AttendArgs a{};
+    a.sh = c->shape;
+    a.layers = c->layers_d;
+    a.c = call;
+    a.units = call.map ? call.n * call.nq : call.n;
+    a.unit_rows = call.map ? call.heads : call.nq * call.heads;
+    a.groups = plan.groups;
+    a.shares = plan.shares;
+    a.wide = reinterpret_cast<uintptr_t>(call.q) % 16 == 0 && call.q_stride_entry % 8 == 0 &&
+             call.q_stride_query % 8 == 0 && call.q_stride_head % 8 == 0;
+    const int64_t parts = (int64_t)a.units * a.shares;
+    a.partial = static_cast<float *>(call.workspace);
+    a.stat = a.partial ? a.partial + parts * a.unit_rows * call.d_v : nullptr;
+    const dim3 grid((unsigned)((parts + 7) / 8 * 8 * a.groups));
+    hipError_t e = call.format == KVR_ROW_FP8    ? launch_format<KVR_ROW_FP8>(c, a, plan.block, grid, s)
+                   : call.format == KVR_ROW_BF16 ? launch_format<KVR_ROW_BF16>(c, a, plan.block, grid, s)
+                                                 : launch_format<KVR_ROW_F16>(c, a, plan.block, grid, s);
+    if (e != hipSuccess || a.shares == 1)
+        return e;
+    const dim3 rows((unsigned)((int64_t)a.units * a.unit_rows));
+    if (call.format == KVR_ROW_F16)
+        return call.d_v == 512
+                   ? launch(c, KVR_KERNEL_ATTEND, join_kernel<_Float16, 512>, rows, dim3(128), 0, s, a)
+                   : launch(c, KVR_KERNEL_ATTEND, join_kernel<_Float16, 256>, rows, dim3(64), 0, s, a);
+    return call.d_v == 512
+               ? launch(c, KVR_KERNEL_ATTEND, join_kernel<__bf16, 512>, rows, dim3(128), 0, s, a)
+               : launch(c, KVR_KERNEL_ATTEND, join_kernel<__bf16, 256>, rows, dim3(64), 0, s, a);
 }
 
 }  // namespace kvr
