@@ -16,9 +16,9 @@
 // selection, which it walks in tiles of 64 rows, two tiles in LDS: while one
 // is worked on, the next is on its way (16-byte direct loads to LDS, addresses
 // from the location words, which are read a tile earlier still).
-//   scores   wave w computes 16 of the tile's rows (w mod 4) for its part of
-//            the query rows (w / 4), by 16x16x32 MFMA with the keys from LDS
-//            and the queries in registers;
+//   scores   a wave computes a part of the tile's rows for one block of query
+//            rows, by 16x16x32 MFMA with the keys from LDS and the queries in
+//            registers;
 //   values   every wave takes d_v / NW columns of all query rows; the
 //            probabilities pass through LDS, the latents are read transposed
 //            (ds_read_tr), so the product needs no copy of the tile.
@@ -44,7 +44,6 @@ namespace {
 
 constexpr int kTile = 64;     // rows per tile
 constexpr float kSlack = 8.f; // log2 of the largest probability kept
-constexpr int kRowGroups = kTile / 16;
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -66,8 +65,32 @@ __device__ __forceinline__ void barrier_all()
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
+// Direct loads to LDS: lane i's 16 (or 4) bytes go to lds + 16 i (4 i).  They
+// are written as assembly because the compiler, which cannot tell the two
+// buffers of a tile apart, would otherwise wait for them before the next LDS
+// read; the kernel waits itself (barrier_all) before it reads what they bring.
+__device__ __forceinline__ uint32_t lds_offset(const void *p)
+{
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
+}
+
+__device__ __forceinline__ void load_lds16(uint32_t lds, const void *src)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                 :
+                 : "s"(lds), "v"(src)
+                 : "memory", "m0");
+}
+
+__device__ __forceinline__ void load_lds4(uint32_t lds, const void *src)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+                 :
+                 : "s"(lds), "v"(src)
+                 : "memory", "m0");
+}
+
 #define LDS_PTR(T, p) ((__attribute__((address_space(3))) T *)(p))
-#define GLOBAL_PTR(T, p) ((const __attribute__((address_space(1))) T *)(p))
 
 // What a row that is left out is read from (the longest row is 1152 bytes).
 __device__ __attribute__((aligned(16))) uint8_t zero_row[1152];
@@ -171,29 +194,26 @@ struct Tile {
     static constexpr int kScalesAt = kRopeAt + kTile * kRope;
     static constexpr int kBytes = kScalesAt + kTile * kScales;
 
-    // Loads rows [first, first + ROWS) of the tile, lane i < ROWS holding the
-    // address of row first + i.  Each instruction writes 1024 consecutive
-    // bytes of a part.
+    // Loads rows [first, first + ROWS) of the tile at LDS offset `lds`, lane
+    // i < ROWS holding the address of row first + i.  Each instruction writes
+    // 1024 consecutive bytes of a part.
     template <int ROWS>
-    static __device__ __forceinline__ void load(uint8_t *lds, int first, const uint8_t *row)
+    static __device__ __forceinline__ void load(uint32_t lds, int first, const uint8_t *row)
     {
         const int lane = lane_id();
         const uint32_t lo = (uint32_t)(uintptr_t)row, hi = (uint32_t)((uintptr_t)row >> 32);
         auto part = [&](auto per_row, int at, int from) {
             constexpr int C = decltype(per_row)::value / 16;  // chunks per row
             constexpr int N = 64 / C;                         // rows per instruction
-            static_assert(ROWS % N == 0, "a wave loads whole instructions");
+            static_assert(ROWS % N == 0 && ROWS % 8 == 0, "a wave loads whole instructions");
 #pragma unroll
             for (int i = 0; i < ROWS; i += N) {
                 const int k = i + lane / C;
-                const uint64_t p = (uint64_t)__shfl((int)lo, k) & 0xFFFFFFFFull;
-                const uint64_t ph = (uint64_t)(uint32_t)__shfl((int)hi, k) << 32;
-                const int chunk = (lane % C) ^ swizzle(first + k);
-                const uint8_t *src =
-                    reinterpret_cast<const uint8_t *>(ph | p) + from + chunk * 16;
-                __builtin_amdgcn_global_load_lds(GLOBAL_PTR(uint32_t, src),
-                                                 LDS_PTR(uint32_t, lds + at + (first + i) * C * 16),
-                                                 16, 0, 0);
+                const uint64_t p = (uint64_t)(uint32_t)__shfl((int)hi, k) << 32 |
+                                   (uint32_t)__shfl((int)lo, k);
+                const int chunk = (lane % C) ^ swizzle(k);  // first is a multiple of 8
+                load_lds16(lds + at + (first + i) * C * 16,
+                           reinterpret_cast<const uint8_t *>(p) + from + chunk * 16);
             }
         };
         part(std::integral_constant<int, kLatent>(), 0, 0);
@@ -201,13 +221,12 @@ struct Tile {
             part(std::integral_constant<int, kRope>(), kRopeAt, kLatent + kScales);
         if constexpr (kFp8)
             if (lane < ROWS)
-                __builtin_amdgcn_global_load_lds(GLOBAL_PTR(uint32_t, row + kLatent),
-                                                 LDS_PTR(uint32_t, lds + kScalesAt + first * 16),
-                                                 16, 0, 0);
+                load_lds16(lds + kScalesAt + first * 16, row + kLatent);
     }
 };
 
-template <int FMT, int DV, int DR, int MB, int NW>
+// RG: parts the tile's rows are cut into for the scores.
+template <int FMT, int DV, int DR, int MB, int NW, int RG>
 __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
 {
     typedef typename Elem<FMT>::type E;
@@ -216,24 +235,25 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
     typedef Tile<FMT, DV, DR> TL;
     constexpr bool kFp8 = FMT == KVR_ROW_FP8;
     constexpr int kSteps = (DV + DR) / 32;        // MFMA steps of a score
-    constexpr int kHeadGroups = NW / kRowGroups;  // waves that share 16 rows of the tile
-    constexpr int MQ = MB / kHeadGroups;          // score blocks of a wave
+    constexpr int RB = kTile / 16 / RG;           // row blocks of a wave's scores
     constexpr int NC = DV / NW / 16;              // value column blocks of a wave
     constexpr int kGroups = kFp8 ? DV / kScaleGroup : 1;
     constexpr int kPitch = kTile + 8;             // of a query row's probabilities
     constexpr int kRows = kTile / NW;             // rows a wave loads
-    static_assert(MB % kHeadGroups == 0 && DV % (NW * 16) == 0, "");
+    static_assert(MB * RG == NW && DV % (NW * 16) == 0, "one block of query rows per wave");
 
     __shared__ __attribute__((aligned(1024))) uint8_t buf0[TL::kBytes];
     __shared__ __attribute__((aligned(1024))) uint8_t buf1[TL::kBytes];
     __shared__ __attribute__((aligned(16))) E sP[kGroups][MB * 16][kPitch];
-    __shared__ float sMax[kRowGroups][MB * 16];
+    __shared__ float sMax[RG][MB * 16];
     __shared__ __attribute__((aligned(8))) uint8_t sValid[2][kTile / 8];
     __shared__ int sExceeds[2];
+    __shared__ uint32_t sWord[2][kTile];  // location words, and with a map the
+    __shared__ int32_t sEntry[2][kTile];  // entries, of tiles to come
 
     const int lane = lane_id(), col = lane & 15, grp = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(wave_id());
-    const int rg = wave % kRowGroups, hg = wave / kRowGroups;
+    const int rg = wave % RG, hg = wave / RG;
 
     // workgroups of one selection and share are 8 apart: the same XCD's L2
     // serves their rows
@@ -250,7 +270,7 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
     RowList list;
     int cnt = a.c.count ? a.c.count[i] : a.c.stride;
     list.count = known ? (cnt < 0 ? 0 : (cnt > a.c.stride ? a.c.stride : cnt)) : 0;
-    list.len = a.c.map ? (known ? a.c.k : 0) : list.count;
+    list.len = a.c.map && list.count > 0 ? a.c.k : list.count;
     list.map = a.c.map ? a.c.map + (int64_t)unit * a.c.k : nullptr;
     list.loc = a.c.loc ? a.c.loc + (int64_t)i * a.c.stride : nullptr;
     list.rows = a.c.rows ? static_cast<const uint8_t *>(a.c.rows) +
@@ -271,10 +291,9 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
     // unit is one query)
     const E *q = static_cast<const E *>(a.c.q) + (int64_t)i * a.c.q_stride_entry;
     const int x0 = g * (MB * 16);
-    frag qf[MQ][kSteps];
-#pragma unroll
-    for (int mb = 0; mb < MQ; ++mb) {
-        const int x = x0 + (hg * MQ + mb) * 16 + col;
+    frag qf[kSteps];  // of the wave's block
+    auto load_q = [&](auto read) {
+        const int x = x0 + hg * 16 + col;
         const bool in = x < a.unit_rows && t0 < t1;
         const int xc = in ? x : 0;
         const int qi = a.c.map ? unit % a.c.nq : xc / a.c.heads;
@@ -285,24 +304,27 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
             // an 8-bit key fragment holds 8 of the 16 codes of one LDS read
             const int d = kFp8 && s < DV / 32 ? s / 2 * 64 + grp * 16 + (s & 1) * 8
                                               : s * 32 + grp * 8;
-            frag f;
-            if (a.wide) {
-                f = *reinterpret_cast<const frag *>(p + d);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    f[e] = p[d + e];
-            }
+            frag f = read(p + d);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 f[e] = in ? f[e] : (E)0.f;
-            qf[mb][s] = f;
+            qf[s] = f;
         }
-    }
+    };
+    if (a.wide)
+        load_q([](const E *p) { return *reinterpret_cast<const frag *>(p); });
+    else
+        load_q([](const E *p) {
+            frag f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                f[e] = p[e];
+            return f;
+        });
 
-    // m: the reference of this lane's query row in each block; mq, l: those of
-    // the wave's own score blocks and this lane's share of their sums
-    float m[MB], mq[MQ], l[MQ];
+    // m: the reference of this lane's query row in each block; mq, l: the one
+    // of the wave's own block and this lane's share of its sum
+    float m[MB], mq = -__builtin_inff(), l = 0.f;
     f32x4 o[NC][MB];
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
@@ -311,25 +333,21 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
         for (int c = 0; c < NC; ++c)
             o[c][mb] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-#pragma unroll
-    for (int mb = 0; mb < MQ; ++mb) {
-        mq[mb] = -__builtin_inff();
-        l[mb] = 0.f;
-    }
     if (threadIdx.x < 2)
         sExceeds[threadIdx.x] = 0;
 
-    // The list's entry at this lane's row of tile t (a wave's first kRows
-    // lanes): its position in the selection, its word, its address.
+    // This lane's row of a tile (a wave's first kRows lanes; the others repeat
+    // them).  Its entry of the selection (-1: left out), its location word, its
+    // address; a row past the list's end reads the last entry's.
     const int mine = wave * kRows + (lane & (kRows - 1));
-    auto position = [&](int t) {
+    auto at = [&](int t) {
         const int j = t * kTile + mine;
-        int e = -1;
-        if (t < t1 && j < list.len)
-            e = list.map ? list.map[j] : j;
-        return e >= 0 && e < list.count ? e : -1;
+        return j < list.len ? j : list.len - 1;
     };
-    auto word = [&](int e) { return e >= 0 ? (list.loc ? list.loc[e] : 0u) : KVR_LOC_INVALID; };
+    auto entry = [&](int t, int mapped) {
+        const int e = list.map ? mapped : t * kTile + mine;
+        return t < t1 && t * kTile + mine < list.len && e >= 0 && e < list.count ? e : -1;
+    };
     auto address = [&](int e, uint32_t w) {
         bool bad = false;
         const uint8_t *p = e >= 0 ? row_address(a, lp, list, r, e, w, bad) : nullptr;
@@ -338,7 +356,7 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
         return p;
     };
     // Starts tile t's loads into a buffer and notes which of its rows count.
-    auto fetch = [&](uint8_t *buf, int t, const uint8_t *row) {
+    auto fetch = [&](const uint8_t *buf, int t, const uint8_t *row) {
         const uint64_t valid = __ballot(row != nullptr);
         if (lane == 0) {
             if constexpr (kRows == 8)
@@ -346,109 +364,111 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
             else
                 reinterpret_cast<uint16_t *>(sValid[t & 1])[wave] = (uint16_t)valid;
         }
-        TL::template load<kRows>(buf, wave * kRows, row ? row : zero_row);
+        TL::template load<kRows>(lds_offset(buf), wave * kRows, row ? row : zero_row);
     };
 
     const float to_log2 = a.c.scale * 1.44269504088896340736f;
 
     // Tile t out of cur, while tile t + 1 (row: its addresses) is loaded into
-    // nxt; e: the positions of tile t + 2.
-    auto step = [&](const uint8_t *cur, uint8_t *nxt, int t, const uint8_t *&row, int &e) {
+    // nxt, the words of tile t + 3 and the map's entries of tile t + 4 into
+    // LDS; e: the entries of tile t + 2, whose words have arrived.
+    auto step = [&](const uint8_t *cur, const uint8_t *nxt, int t, const uint8_t *&row, int &e) {
         // tile t has arrived, and no wave reads nxt any more
         barrier_all();
-        const uint32_t w2 = word(e);
-        const int e3 = position(t + 3);
         if (t + 1 < t1)
             fetch(nxt, t + 1, row);
+        const int e3 = entry(t + 3, list.map ? sEntry[(t + 3) & 1][mine] : 0);
+        if (t + 3 < t1) {
+            if (list.loc && lane < kRows)
+                load_lds4(lds_offset(&sWord[(t + 3) & 1][wave * kRows]),
+                          list.loc + (e3 >= 0 ? e3 : 0));
+            if (list.map && lane < kRows)
+                load_lds4(lds_offset(&sEntry[t & 1][wave * kRows]), list.map + at(t + 4));
+        }
         if (threadIdx.x == 0)
             sExceeds[(t + 1) & 1] = 0;
 
-        // scores of this wave's 16 rows
-        f32x4 s[MQ];
-        const int krow = rg * 16 + col;
-        float sc[kFp8 ? 4 : 1][kGroups];  // scales of this lane's 4 rows
+        // scores of this wave's rows: row block rb holds rows rowb + rb * 16 ..
+        const int rowb = rg * RB * 16;
+        const int swz = swizzle(col);  // of row rowb + rb * 16 + col
+        const int kchunk[2] = {(grp ^ swz) * 16, ((4 + grp) ^ swz) * 16};
+        f32x4 s[RB];
+        // scales of row k of this lane's 4 rows of a row block
+        auto scales = [&](int rb, int k) {
+            return reinterpret_cast<const float *>(cur + TL::kScalesAt +
+                                                   (rowb + rb * 16 + grp * 4 + k) * 16);
+        };
 #pragma unroll
-        for (int mb = 0; mb < MQ; ++mb)
-            s[mb] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if constexpr (DR > 0) {
-            const uint8_t *base = cur + TL::kRopeAt + krow * TL::kRope;
+        for (int rb = 0; rb < RB; ++rb) {
+            s[rb] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if constexpr (DR > 0) {
+                const uint8_t *base = cur + TL::kRopeAt + (rowb + rb * 16 + col) * TL::kRope;
 #pragma unroll
-            for (int st = 0; st < DR / 32; ++st) {
-                const int chunk = (st * 4 + grp) ^ swizzle(krow);
-                const frag kf = *reinterpret_cast<const frag *>(base + chunk * 16);
-#pragma unroll
-                for (int mb = 0; mb < MQ; ++mb)
-                    s[mb] = M::mul(kf, qf[mb][DV / 32 + st], s[mb]);
+                for (int st = 0; st < DR / 32; ++st)
+                    s[rb] = M::mul(*reinterpret_cast<const frag *>(base + kchunk[st & 1] + st / 2 * 128),
+                                   qf[DV / 32 + st], s[rb]);
             }
         }
-        const uint8_t *base = cur + krow * TL::kLatent;
+        const uint8_t *base = cur + (rowb + col) * TL::kLatent;
         if constexpr (kFp8) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float *p = reinterpret_cast<const float *>(cur + TL::kScalesAt +
-                                                                 (rg * 16 + grp * 4 + k) * 16);
-#pragma unroll
-                for (int gi = 0; gi < kGroups; ++gi)
-                    sc[k][gi] = p[gi];
-            }
-#pragma unroll
             for (int gi = 0; gi < kGroups; ++gi) {
-                f32x4 part[MQ];
+                f32x4 part[RB];
 #pragma unroll
-                for (int mb = 0; mb < MQ; ++mb)
-                    part[mb] = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int rb = 0; rb < RB; ++rb)
+                    part[rb] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int chunk = (gi * 8 + h * 4 + grp) ^ swizzle(krow);
-                    const u32x4 v = *reinterpret_cast<const u32x4 *>(base + chunk * 16);
-                    const frag k0 = widen(v[0], v[1]), k1 = widen(v[2], v[3]);
 #pragma unroll
-                    for (int mb = 0; mb < MQ; ++mb) {
-                        part[mb] = M::mul(k0, qf[mb][gi * 4 + h * 2], part[mb]);
-                        part[mb] = M::mul(k1, qf[mb][gi * 4 + h * 2 + 1], part[mb]);
+                    for (int rb = 0; rb < RB; ++rb) {
+                        const u32x4 v = *reinterpret_cast<const u32x4 *>(
+                            base + rb * 16 * TL::kLatent + kchunk[h] + gi * 128);
+                        part[rb] = M::mul(widen(v[0], v[1]), qf[gi * 4 + h * 2], part[rb]);
+                        part[rb] = M::mul(widen(v[2], v[3]), qf[gi * 4 + h * 2 + 1], part[rb]);
                     }
                 }
 #pragma unroll
-                for (int mb = 0; mb < MQ; ++mb)
+                for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        s[mb][k] = fmaf(part[mb][k], sc[k][gi], s[mb][k]);
+                        s[rb][k] = fmaf(part[rb][k], scales(rb, k)[gi], s[rb][k]);
             }
         } else {
 #pragma unroll
-            for (int st = 0; st < DV / 32; ++st) {
-                const int chunk = (st * 4 + grp) ^ swizzle(krow);
-                const frag kf = *reinterpret_cast<const frag *>(base + chunk * 16);
+            for (int st = 0; st < DV / 32; ++st)
 #pragma unroll
-                for (int mb = 0; mb < MQ; ++mb)
-                    s[mb] = M::mul(kf, qf[mb][st], s[mb]);
-            }
+                for (int rb = 0; rb < RB; ++rb)
+                    s[rb] = M::mul(*reinterpret_cast<const frag *>(base + rb * 16 * TL::kLatent +
+                                                                   kchunk[st & 1] + st / 2 * 128),
+                                   qf[st], s[rb]);
         }
 
         // t_j of the rows that count; whether one exceeds its reference
-        const uint64_t valid = *reinterpret_cast<const uint64_t *>(sValid[t & 1]);
-        const uint32_t mask = (uint32_t)(valid >> (rg * 16 + grp * 4)) & 15u;
+        const uint64_t valid = *reinterpret_cast<const uint64_t *>(sValid[t & 1]) >> (rowb + grp * 4);
         bool exceeds = false;
 #pragma unroll
-        for (int mb = 0; mb < MQ; ++mb) {
+        for (int rb = 0; rb < RB; ++rb) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                s[mb][k] = (mask >> k) & 1 ? s[mb][k] * to_log2 : -__builtin_inff();
-                exceeds |= s[mb][k] > mq[mb] + kSlack;
+                s[rb][k] = (valid >> (rb * 16 + k)) & 1 ? s[rb][k] * to_log2 : -__builtin_inff();
+                exceeds |= s[rb][k] > mq + kSlack;
             }
         }
         if (__any(exceeds) && lane == 0)
             sExceeds[t & 1] = 1;
-        float sum[MQ];
+        float sum;
         auto write_p = [&]() {
+            const float ref = mq == -__builtin_inff() ? 0.f : mq;
+            sum = 0.f;
+            if constexpr (kFp8)  // the scales are read again, not kept in registers
+                asm volatile("" ::: "memory");
 #pragma unroll
-            for (int mb = 0; mb < MQ; ++mb) {
-                const float ref = mq[mb] == -__builtin_inff() ? 0.f : mq[mb];
+            for (int rb = 0; rb < RB; ++rb) {
                 float p[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    p[k] = exp2_hw(s[mb][k] - ref);
-                sum[mb] = (p[0] + p[1]) + (p[2] + p[3]);
+                    p[k] = exp2_hw(s[rb][k] - ref);
+                sum += (p[0] + p[1]) + (p[2] + p[3]);
 #pragma unroll
                 for (int gi = 0; gi < kGroups; ++gi) {
                     typedef E e4 __attribute__((ext_vector_type(4)));
@@ -456,11 +476,11 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         if constexpr (kFp8)
-                            v[k] = (E)(p[k] * sc[k][gi]);
+                            v[k] = (E)(p[k] * scales(rb, k)[gi]);
                         else
                             v[k] = (E)p[k];
                     }
-                    *reinterpret_cast<e4 *>(&sP[gi][(hg * MQ + mb) * 16 + col][rg * 16 + grp * 4]) = v;
+                    *reinterpret_cast<e4 *>(&sP[gi][hg * 16 + col][rowb + rb * 16 + grp * 4]) = v;
                 }
             }
         };
@@ -469,45 +489,33 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
         if (sExceeds[t & 1]) {
             // the maximum becomes the reference: sums so far are scaled down,
             // this tile's probabilities written again
+            float top = -__builtin_inff();
 #pragma unroll
-            for (int mb = 0; mb < MQ; ++mb) {
-                float top = fmaxf(fmaxf(s[mb][0], s[mb][1]), fmaxf(s[mb][2], s[mb][3]));
-                top = fmaxf(top, __shfl_xor(top, 16));
-                top = fmaxf(top, __shfl_xor(top, 32));
-                if (grp == 0)
-                    sMax[rg][(hg * MQ + mb) * 16 + col] = top;
-            }
+            for (int rb = 0; rb < RB; ++rb)
+                top = fmaxf(top, fmaxf(fmaxf(s[rb][0], s[rb][1]), fmaxf(s[rb][2], s[rb][3])));
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            if (grp == 0)
+                sMax[rg][hg * 16 + col] = top;
             barrier_lds();
-            float alpha[MB];
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb) {
-                float top = m[mb];
+                float to = m[mb];
 #pragma unroll
-                for (int k = 0; k < kRowGroups; ++k)
-                    top = fmaxf(top, sMax[k][mb * 16 + col]);
-                alpha[mb] = top == -__builtin_inff() ? 1.f : exp2_hw(m[mb] - top);
-                m[mb] = top;
+                for (int k = 0; k < RG; ++k)
+                    to = fmaxf(to, sMax[k][mb * 16 + col]);
+                const float alpha = to == -__builtin_inff() ? 1.f : exp2_hw(m[mb] - to);
+                m[mb] = to;
+                mq = hg == mb ? to : mq;
+                l = hg == mb ? l * alpha : l;
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
-                    o[c][mb] *= alpha[mb];
-            }
-#pragma unroll
-            for (int mb = 0; mb < MQ; ++mb) {
-                // the wave's own blocks (constant register indices)
-                mq[mb] = m[mb];
-                float al = alpha[mb];
-                if constexpr (kHeadGroups == 2) {
-                    mq[mb] = hg ? m[MQ + mb] : mq[mb];
-                    al = hg ? alpha[MQ + mb] : al;
-                }
-                l[mb] *= al;
+                    o[c][mb] *= alpha;
             }
             write_p();
             barrier_lds();
         }
-#pragma unroll
-        for (int mb = 0; mb < MQ; ++mb)
-            l[mb] += sum[mb];
+        l += sum;
 
         // values: o[column][query row] += latent[row][column] * p[query row][row]
         const int gi = kFp8 ? wave * (DV / NW) / kScaleGroup : 0;
@@ -546,17 +554,23 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
                     o[c][mb] = M::mul(vf, pf[mb], o[c][mb]);
             }
         }
-        row = address(e, w2);
+        row = address(e, list.loc ? sWord[t & 1][mine] : 0);
         e = e3;
     };
 
     if (t0 < t1) {
-        const int e0 = position(t0), e1 = position(t0 + 1);
-        int e = position(t0 + 2);
-        const uint32_t w0 = word(e0), w1 = word(e1);
-        const uint8_t *row = address(e0, w0);
+        const int32_t *map = list.map;
+        const int e0 = entry(t0, map ? map[at(t0)] : 0);
+        const int e1 = entry(t0 + 1, map ? map[at(t0 + 1)] : 0);
+        int e = entry(t0 + 2, map ? map[at(t0 + 2)] : 0);
+        auto word = [&](int k) { return list.loc ? list.loc[k >= 0 ? k : 0] : 0u; };
+        if (map && lane < kRows)
+            sEntry[(t0 + 3) & 1][mine] = map[at(t0 + 3)];
+        if (lane < kRows)
+            sWord[t0 & 1][mine] = word(e);
+        const uint8_t *row = address(e0, word(e0));
         fetch(buf0, t0, row);
-        row = address(e1, w1);
+        row = address(e1, word(e1));
         for (int t = t0; t < t1; t += 2) {
             step(buf0, buf1, t, row, e);
             if (t + 1 < t1)
@@ -564,17 +578,12 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
         }
     }
 
-    // the sums of the four waves (and 4 lane groups) that share a query row
-#pragma unroll
-    for (int mb = 0; mb < MQ; ++mb) {
-        l[mb] += __shfl_xor(l[mb], 16);
-        l[mb] += __shfl_xor(l[mb], 32);
-    }
+    // the sums of the waves (and 4 lane groups) that share a query row
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
     barrier_lds();
-#pragma unroll
-    for (int mb = 0; mb < MQ; ++mb)
-        if (grp == 0)
-            sMax[rg][(hg * MQ + mb) * 16 + col] = l[mb];
+    if (grp == 0)
+        sMax[rg][hg * 16 + col] = l;
     barrier_lds();
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
@@ -583,7 +592,7 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
             continue;
         float sum = 0.f;
 #pragma unroll
-        for (int k = 0; k < kRowGroups; ++k)
+        for (int k = 0; k < RG; ++k)
             sum += sMax[k][mb * 16 + col];
         const int64_t at = (int64_t)unit * a.unit_rows + x;  // query row of the call
         const int c0 = wave * (DV / NW) + grp * 4;
@@ -649,10 +658,12 @@ template <int FMT, int DV, int DR>
 hipError_t launch_dims(const kvr_ctx *c, const AttendArgs &a, int block, dim3 grid, hipStream_t s)
 {
     if (block == 16)
-        return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 1, 4>, grid, dim3(256), 0, s, a);
+        return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 1, 4, 4>, grid, dim3(256), 0,
+                      s, a);
     if (block == 32)
-        return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 2, 8>, grid, dim3(512), 0, s, a);
-    return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 4, 8>, grid, dim3(512), 0, s, a);
+        return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 2, 8, 4>, grid, dim3(512), 0,
+                      s, a);
+    return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 4, 8, 2>, grid, dim3(512), 0, s, a);
 }
 
 template <int FMT>
