@@ -13,12 +13,14 @@
 // and the sums are scaled down.
 //
 // A workgroup of NW waves owns MB blocks of 16 query rows and a share of the
-// selection, which it walks in tiles of 64 rows, two tiles in LDS: while one
-// is worked on, the next is on its way (16-byte direct loads to LDS, addresses
-// from the location words, which are read a tile earlier still).
-//   scores   a wave computes a part of the tile's rows for one block of query
-//            rows, by 16x16x32 MFMA with the keys from LDS and the queries in
-//            registers;
+// selection, which it walks in tiles of 32 rows.  Three tiles are in LDS: the
+// values of one are summed while the scores of the next are computed and the
+// one after is on its way (16-byte direct loads to LDS, addresses from the
+// location words, which are read two tiles earlier still).
+//   scores   the d_v + d_rope products of a score are split over four waves,
+//            each with its quarter of the queries in registers and reading its
+//            quarter of the keys once (16x16x32 MFMA); the partial sums pass
+//            through LDS;
 //   values   every wave takes d_v / NW columns of all query rows; the
 //            probabilities pass through LDS, the latents are read transposed
 //            (ds_read_tr), so the product needs no copy of the tile.
@@ -42,7 +44,7 @@
 namespace kvr {
 namespace {
 
-constexpr int kTile = 64;     // rows per tile
+constexpr int kTile = 32;     // rows per tile
 constexpr float kSlack = 8.f; // log2 of the largest probability kept
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -196,7 +198,7 @@ struct Tile {
 
     // Loads rows [first, first + ROWS) of the tile at LDS offset `lds`, lane
     // i < ROWS holding the address of row first + i.  Each instruction writes
-    // 1024 consecutive bytes of a part.
+    // up to 1024 consecutive bytes of a part.
     template <int ROWS>
     static __device__ __forceinline__ void load(uint32_t lds, int first, const uint8_t *row)
     {
@@ -204,16 +206,17 @@ struct Tile {
         const uint32_t lo = (uint32_t)(uintptr_t)row, hi = (uint32_t)((uintptr_t)row >> 32);
         auto part = [&](auto per_row, int at, int from) {
             constexpr int C = decltype(per_row)::value / 16;  // chunks per row
-            constexpr int N = 64 / C;                         // rows per instruction
-            static_assert(ROWS % N == 0 && ROWS % 8 == 0, "a wave loads whole instructions");
+            constexpr int N = 64 / C < ROWS ? 64 / C : ROWS;  // rows per instruction
+            static_assert(ROWS % N == 0, "whole rows per instruction");
 #pragma unroll
             for (int i = 0; i < ROWS; i += N) {
                 const int k = i + lane / C;
                 const uint64_t p = (uint64_t)(uint32_t)__shfl((int)hi, k) << 32 |
                                    (uint32_t)__shfl((int)lo, k);
-                const int chunk = (lane % C) ^ swizzle(k);  // first is a multiple of 8
-                load_lds16(lds + at + (first + i) * C * 16,
-                           reinterpret_cast<const uint8_t *>(p) + from + chunk * 16);
+                const int chunk = (lane % C) ^ swizzle(first + k);
+                if (N * C == 64 || lane < N * C)
+                    load_lds16(lds + at + (first + i) * C * 16,
+                               reinterpret_cast<const uint8_t *>(p) + from + chunk * 16);
             }
         };
         part(std::integral_constant<int, kLatent>(), 0, 0);
@@ -225,35 +228,44 @@ struct Tile {
     }
 };
 
-// RG: parts the tile's rows are cut into for the scores.
-template <int FMT, int DV, int DR, int MB, int NW, int RG>
+template <int FMT, int DV, int DR, int MB, int NW>
 __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
 {
     typedef typename Elem<FMT>::type E;
     typedef Mfma<E> M;
     typedef typename M::frag frag;
+    typedef E e4 __attribute__((ext_vector_type(4)));
     typedef Tile<FMT, DV, DR> TL;
     constexpr bool kFp8 = FMT == KVR_ROW_FP8;
-    constexpr int kSteps = (DV + DR) / 32;        // MFMA steps of a score
-    constexpr int RB = kTile / 16 / RG;           // row blocks of a wave's scores
-    constexpr int NC = DV / NW / 16;              // value column blocks of a wave
+    constexpr int DQ = 4;                      // parts of a score
+    constexpr int kSteps = DV / DQ / 32;       // MFMA steps of a part of the latent
+    constexpr int RG = NW / DQ;                // row groups of the scores
+    constexpr int RB = kTile / 16 / RG;        // row blocks of a wave's scores
+    constexpr int kBlocks = kTile / 16 * MB;   // 16x16 blocks of scores
+    constexpr int kOwners = NW / kBlocks;      // waves that own one of them
+    constexpr int NC = DV / NW / 16;           // value column blocks of a wave
     constexpr int kGroups = kFp8 ? DV / kScaleGroup : 1;
-    constexpr int kPitch = kTile + 8;             // of a query row's probabilities
-    constexpr int kRows = kTile / NW;             // rows a wave loads
-    static_assert(MB * RG == NW && DV % (NW * 16) == 0, "one block of query rows per wave");
+    constexpr int kRows = kTile / NW;          // rows a wave loads
+    static_assert(NW % DQ == 0 && NW % kBlocks == 0 && DV % (NW * 16) == 0, "");
+    static_assert(kOwners == 1 || kOwners == 2, "");
 
-    __shared__ __attribute__((aligned(1024))) uint8_t buf0[TL::kBytes];
-    __shared__ __attribute__((aligned(1024))) uint8_t buf1[TL::kBytes];
-    __shared__ __attribute__((aligned(16))) E sP[kGroups][MB * 16][kPitch];
-    __shared__ float sMax[RG][MB * 16];
-    __shared__ __attribute__((aligned(8))) uint8_t sValid[2][kTile / 8];
+    __shared__ __attribute__((aligned(1024))) uint8_t sTile[3 * TL::kBytes];
+    __shared__ f32x4 sScore[kBlocks][DQ][64];
+    __shared__ __attribute__((aligned(16))) E sP[2][kGroups][MB * 16][kTile];
+    __shared__ float sMax[kTile / 16][MB * 16];
+    __shared__ uint8_t sValid[2][NW];
     __shared__ int sExceeds[2];
     __shared__ uint32_t sWord[2][kTile];  // location words, and with a map the
     __shared__ int32_t sEntry[2][kTile];  // entries, of tiles to come
 
     const int lane = lane_id(), col = lane & 15, grp = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(wave_id());
-    const int rg = wave % RG, hg = wave / RG;
+    const int dq = wave % DQ, rg = wave / DQ;
+    // the block of scores this wave owns: row block, query block, and which of
+    // its owners the wave is
+    const int orow = RG == 2 ? rg : dq & 1;
+    const int oblk = MB == 4 ? dq : MB == 2 ? dq & 1 : 0;
+    const int onum = kOwners == 2 ? dq >> 1 : 0;
 
     // workgroups of one selection and share are 8 apart: the same XCD's L2
     // serves their rows
@@ -291,24 +303,25 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
     // unit is one query)
     const E *q = static_cast<const E *>(a.c.q) + (int64_t)i * a.c.q_stride_entry;
     const int x0 = g * (MB * 16);
-    frag qf[kSteps];  // of the wave's block
+    frag qf[MB][kSteps], qr[MB];  // the wave's part of the queries
     auto load_q = [&](auto read) {
-        const int x = x0 + hg * 16 + col;
-        const bool in = x < a.unit_rows && t0 < t1;
-        const int xc = in ? x : 0;
-        const int qi = a.c.map ? unit % a.c.nq : xc / a.c.heads;
-        const int h = a.c.map ? xc : xc % a.c.heads;
-        const E *p = q + (int64_t)qi * a.c.q_stride_query + (int64_t)h * a.c.q_stride_head;
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            // an 8-bit key fragment holds 8 of the 16 codes of one LDS read
-            const int d = kFp8 && s < DV / 32 ? s / 2 * 64 + grp * 16 + (s & 1) * 8
-                                              : s * 32 + grp * 8;
-            frag f = read(p + d);
+        for (int mb = 0; mb < MB; ++mb) {
+            const int x = x0 + mb * 16 + col;
+            const bool in = x < a.unit_rows && t0 < t1;
+            const int xc = in ? x : 0;
+            const int qi = a.c.map ? unit % a.c.nq : xc / a.c.heads;
+            const int h = a.c.map ? xc : xc % a.c.heads;
+            const E *p = q + (int64_t)qi * a.c.q_stride_query + (int64_t)h * a.c.q_stride_head;
+            const frag zero = {};
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                f[e] = in ? f[e] : (E)0.f;
-            qf[s] = f;
+            for (int s = 0; s < kSteps; ++s) {
+                // an 8-bit key fragment holds 8 of the 16 codes of one LDS read
+                const int d = dq * (DV / DQ) + (kFp8 ? s / 2 * 64 + grp * 16 + (s & 1) * 8
+                                                     : s * 32 + grp * 8);
+                qf[mb][s] = in ? read(p + d) : zero;
+            }
+            qr[mb] = in && dq < DR / 32 ? read(p + DV + dq * 32 + grp * 8) : zero;
         }
     };
     if (a.wide)
@@ -323,7 +336,7 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
         });
 
     // m: the reference of this lane's query row in each block; mq, l: the one
-    // of the wave's own block and this lane's share of its sum
+    // of the block the wave owns scores of and this lane's share of its sum
     float m[MB], mq = -__builtin_inff(), l = 0.f;
     f32x4 o[NC][MB];
 #pragma unroll
@@ -355,210 +368,213 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
             a.c.status[i] = KVR_E_RANGE;
         return p;
     };
-    // Starts tile t's loads into a buffer and notes which of its rows count.
-    auto fetch = [&](const uint8_t *buf, int t, const uint8_t *row) {
+    // Starts tile t's loads and notes which of its rows count.
+    auto tile = [&](int t) { return sTile + (t - t0) % 3 * TL::kBytes; };
+    auto fetch = [&](int t, const uint8_t *row) {
         const uint64_t valid = __ballot(row != nullptr);
-        if (lane == 0) {
-            if constexpr (kRows == 8)
-                sValid[t & 1][wave] = (uint8_t)valid;
-            else
-                reinterpret_cast<uint16_t *>(sValid[t & 1])[wave] = (uint16_t)valid;
-        }
-        TL::template load<kRows>(lds_offset(buf), wave * kRows, row ? row : zero_row);
+        if (lane == 0)
+            sValid[t & 1][wave] = (uint8_t)(valid & ((1 << kRows) - 1));
+        TL::template load<kRows>(lds_offset(tile(t)), wave * kRows, row ? row : zero_row);
     };
 
     const float to_log2 = a.c.scale * 1.44269504088896340736f;
+    f32x4 s;         // t_j of the block this wave owns
+    float sum = 0.f;  // and the sum of their probabilities
 
-    // Tile t out of cur, while tile t + 1 (row: its addresses) is loaded into
-    // nxt, the words of tile t + 3 and the map's entries of tile t + 4 into
-    // LDS; e: the entries of tile t + 2, whose words have arrived.
-    auto step = [&](const uint8_t *cur, const uint8_t *nxt, int t, const uint8_t *&row, int &e) {
-        // tile t has arrived, and no wave reads nxt any more
-        barrier_all();
-        if (t + 1 < t1)
-            fetch(nxt, t + 1, row);
-        const int e3 = entry(t + 3, list.map ? sEntry[(t + 3) & 1][mine] : 0);
-        if (t + 3 < t1) {
-            if (list.loc && lane < kRows)
-                load_lds4(lds_offset(&sWord[(t + 3) & 1][wave * kRows]),
-                          list.loc + (e3 >= 0 ? e3 : 0));
-            if (list.map && lane < kRows)
-                load_lds4(lds_offset(&sEntry[t & 1][wave * kRows]), list.map + at(t + 4));
-        }
-        if (threadIdx.x == 0)
-            sExceeds[(t + 1) & 1] = 0;
-
-        // scores of this wave's rows: row block rb holds rows rowb + rb * 16 ..
-        const int rowb = rg * RB * 16;
-        const int swz = swizzle(col);  // of row rowb + rb * 16 + col
-        const int kchunk[2] = {(grp ^ swz) * 16, ((4 + grp) ^ swz) * 16};
-        f32x4 s[RB];
-        // scales of row k of this lane's 4 rows of a row block
-        auto scales = [&](int rb, int k) {
-            return reinterpret_cast<const float *>(cur + TL::kScalesAt +
-                                                   (rowb + rb * 16 + grp * 4 + k) * 16);
-        };
+    // This wave's part of tile t's scores, into LDS.
+    auto scores = [&](int t) {
+        const uint8_t *cur = tile(t);
+        const int swz = swizzle(col);  // of row 16 n + col
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb) {
-            s[rb] = f32x4{0.f, 0.f, 0.f, 0.f};
-            if constexpr (DR > 0) {
-                const uint8_t *base = cur + TL::kRopeAt + (rowb + rb * 16 + col) * TL::kRope;
+            const int row = (rg * RB + rb) * 16;
+            const uint8_t *base = cur + (row + col) * TL::kLatent + dq * (TL::kLatent / DQ);
+            f32x4 acc[MB];
 #pragma unroll
-                for (int st = 0; st < DR / 32; ++st)
-                    s[rb] = M::mul(*reinterpret_cast<const frag *>(base + kchunk[st & 1] + st / 2 * 128),
-                                   qf[DV / 32 + st], s[rb]);
-            }
-        }
-        const uint8_t *base = cur + (rowb + col) * TL::kLatent;
-        if constexpr (kFp8) {
+            for (int mb = 0; mb < MB; ++mb)
+                acc[mb] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if constexpr (kFp8) {
+                u32x4 v[kSteps / 2];
+                float sc[4];
+                // a quarter is 128 bytes (8 chunks) or, with d_v 256, half of that
 #pragma unroll
-            for (int gi = 0; gi < kGroups; ++gi) {
-                f32x4 part[RB];
-#pragma unroll
-                for (int rb = 0; rb < RB; ++rb)
-                    part[rb] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                    for (int rb = 0; rb < RB; ++rb) {
-                        const u32x4 v = *reinterpret_cast<const u32x4 *>(
-                            base + rb * 16 * TL::kLatent + kchunk[h] + gi * 128);
-                        part[rb] = M::mul(widen(v[0], v[1]), qf[gi * 4 + h * 2], part[rb]);
-                        part[rb] = M::mul(widen(v[2], v[3]), qf[gi * 4 + h * 2 + 1], part[rb]);
-                    }
+                for (int h = 0; h < kSteps / 2; ++h) {
+                    const int chunk = ((dq * (kSteps * 2) + h * 4 + grp) & 7) ^ swz;
+                    const int line = (dq * (kSteps * 2) + h * 4) / 8;
+                    v[h] = *reinterpret_cast<const u32x4 *>(cur + (row + col) * TL::kLatent +
+                                                            line * 128 + chunk * 16);
                 }
 #pragma unroll
-                for (int rb = 0; rb < RB; ++rb)
+                for (int k = 0; k < 4; ++k)
+                    sc[k] = reinterpret_cast<const float *>(
+                        cur + TL::kScalesAt + (row + grp * 4 + k) * 16)[dq * (DV / DQ) / kScaleGroup];
+#pragma unroll
+                for (int h = 0; h < kSteps / 2; ++h) {
+                    const frag k0 = widen(v[h][0], v[h][1]), k1 = widen(v[h][2], v[h][3]);
+#pragma unroll
+                    for (int mb = 0; mb < MB; ++mb)
+                        acc[mb] = M::mul(k0, qf[mb][2 * h], acc[mb]);
+#pragma unroll
+                    for (int mb = 0; mb < MB; ++mb)
+                        acc[mb] = M::mul(k1, qf[mb][2 * h + 1], acc[mb]);
+                }
+#pragma unroll
+                for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        s[rb][k] = fmaf(part[rb][k], scales(rb, k)[gi], s[rb][k]);
+                        acc[mb][k] *= sc[k];
+            } else {
+                frag kf[kSteps];
+#pragma unroll
+                for (int st = 0; st < kSteps; ++st) {
+                    const int chunk = ((st * 4 + grp) & 7) ^ swz;
+                    kf[st] = *reinterpret_cast<const frag *>(base + st / 2 * 128 + chunk * 16);
+                }
+#pragma unroll
+                for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+                    for (int mb = 0; mb < MB; ++mb)
+                        acc[mb] = M::mul(kf[st], qf[mb][st], acc[mb]);
             }
-        } else {
+            if (dq < DR / 32) {
+                const int chunk = (dq * 4 + grp) ^ swz;
+                const frag kf = *reinterpret_cast<const frag *>(
+                    cur + TL::kRopeAt + (row + col) * TL::kRope + chunk * 16);
 #pragma unroll
-            for (int st = 0; st < DV / 32; ++st)
+                for (int mb = 0; mb < MB; ++mb)
+                    acc[mb] = M::mul(kf, qr[mb], acc[mb]);
+            }
 #pragma unroll
-                for (int rb = 0; rb < RB; ++rb)
-                    s[rb] = M::mul(*reinterpret_cast<const frag *>(base + rb * 16 * TL::kLatent +
-                                                                   kchunk[st & 1] + st / 2 * 128),
-                                   qf[st], s[rb]);
+            for (int mb = 0; mb < MB; ++mb)
+                sScore[(rg * RB + rb) * MB + mb][dq][lane] = acc[mb];
         }
+    };
 
-        // t_j of the rows that count; whether one exceeds its reference
-        const uint64_t valid = *reinterpret_cast<const uint64_t *>(sValid[t & 1]) >> (rowb + grp * 4);
+    // Probabilities of the block this wave owns, of tile t, into LDS.
+    auto write_p = [&](int t) {
+        const float ref = mq == -__builtin_inff() ? 0.f : mq;
+        float p[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            p[k] = exp2_hw(s[k] - ref);
+        sum = (p[0] + p[1]) + (p[2] + p[3]);
+        const int head = oblk * 16 + col;
+        const int at = ((orow * 2 + (grp >> 1)) ^ ((col >> 1) & 3)) * 8 + (grp & 1) * 4;
+        if constexpr (kFp8) {
+            constexpr int G = kGroups / kOwners > 0 ? kGroups / kOwners : 1;
+            const uint8_t *sc = tile(t) + TL::kScalesAt + (orow * 16 + grp * 4) * 16;
+            f32x4 w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                w[k] = *reinterpret_cast<const f32x4 *>(sc + k * 16);
+#pragma unroll
+            for (int gi = 0; gi < G; ++gi) {
+                e4 v;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float f = w[k][gi];
+                    if constexpr (kOwners == 2)
+                        f = onum ? w[k][G + gi] : f;
+                    v[k] = (E)(p[k] * f);
+                }
+                *reinterpret_cast<e4 *>(&sP[t & 1][onum * G + gi][head][at]) = v;
+            }
+        } else if (onum == 0) {
+            e4 v;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                v[k] = (E)p[k];
+            *reinterpret_cast<e4 *>(&sP[t & 1][0][head][at]) = v;
+        }
+    };
+
+    auto softmax = [&](int t) {
+        const f32x4(*part)[64] = sScore[orow * MB + oblk];
+        s = ((part[0][lane] + part[1][lane]) + part[2][lane]) + part[3][lane];
+        const int first = orow * 16 + grp * 4;
+        const uint32_t valid = sValid[t & 1][first / kRows] >> (first % kRows);
         bool exceeds = false;
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                s[rb][k] = (valid >> (rb * 16 + k)) & 1 ? s[rb][k] * to_log2 : -__builtin_inff();
-                exceeds |= s[rb][k] > mq + kSlack;
-            }
+        for (int k = 0; k < 4; ++k) {
+            s[k] = (valid >> k) & 1 ? s[k] * to_log2 : -__builtin_inff();
+            exceeds |= s[k] > mq + kSlack;
         }
         if (__any(exceeds) && lane == 0)
             sExceeds[t & 1] = 1;
-        float sum;
-        auto write_p = [&]() {
-            const float ref = mq == -__builtin_inff() ? 0.f : mq;
-            sum = 0.f;
-            if constexpr (kFp8)  // the scales are read again, not kept in registers
-                asm volatile("" ::: "memory");
-#pragma unroll
-            for (int rb = 0; rb < RB; ++rb) {
-                float p[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    p[k] = exp2_hw(s[rb][k] - ref);
-                sum += (p[0] + p[1]) + (p[2] + p[3]);
-#pragma unroll
-                for (int gi = 0; gi < kGroups; ++gi) {
-                    typedef E e4 __attribute__((ext_vector_type(4)));
-                    e4 v;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if constexpr (kFp8)
-                            v[k] = (E)(p[k] * scales(rb, k)[gi]);
-                        else
-                            v[k] = (E)p[k];
-                    }
-                    *reinterpret_cast<e4 *>(&sP[gi][hg * 16 + col][rowb + rb * 16 + grp * 4]) = v;
-                }
-            }
-        };
-        write_p();
-        barrier_lds();
+        write_p(t);
+    };
+
+    // Once tile t's probabilities are in LDS: if one exceeded its reference,
+    // the maximum becomes the reference, the sums so far are scaled down and
+    // the tile's probabilities written again.
+    auto settle = [&](int t) {
         if (sExceeds[t & 1]) {
-            // the maximum becomes the reference: sums so far are scaled down,
-            // this tile's probabilities written again
-            float top = -__builtin_inff();
-#pragma unroll
-            for (int rb = 0; rb < RB; ++rb)
-                top = fmaxf(top, fmaxf(fmaxf(s[rb][0], s[rb][1]), fmaxf(s[rb][2], s[rb][3])));
+            float top = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
             top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
             if (grp == 0)
-                sMax[rg][hg * 16 + col] = top;
+                sMax[orow][oblk * 16 + col] = top;
             barrier_lds();
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb) {
                 float to = m[mb];
 #pragma unroll
-                for (int k = 0; k < RG; ++k)
+                for (int k = 0; k < kTile / 16; ++k)
                     to = fmaxf(to, sMax[k][mb * 16 + col]);
                 const float alpha = to == -__builtin_inff() ? 1.f : exp2_hw(m[mb] - to);
                 m[mb] = to;
-                mq = hg == mb ? to : mq;
-                l = hg == mb ? l * alpha : l;
+                mq = oblk == mb ? to : mq;
+                l = oblk == mb ? l * alpha : l;
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
                     o[c][mb] *= alpha;
             }
-            write_p();
+            write_p(t);
             barrier_lds();
         }
         l += sum;
+    };
 
-        // values: o[column][query row] += latent[row][column] * p[query row][row]
+    // o[column][query row] += latent[row][column] * p[query row][row] of tile t
+    auto values = [&](int t) {
+        const uint8_t *cur = tile(t);
         const int gi = kFp8 ? wave * (DV / NW) / kScaleGroup : 0;
+        frag pf[MB];
 #pragma unroll
-        for (int st = 0; st < kTile / 32; ++st) {
-            frag pf[MB];
+        for (int mb = 0; mb < MB; ++mb)
+            pf[mb] = *reinterpret_cast<const frag *>(
+                &sP[t & 1][gi][mb * 16 + col][(grp ^ ((col >> 1) & 3)) * 8]);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const int cb = wave * NC + c;  // block of 16 columns
+            frag vf;
+            if constexpr (kFp8) {
+                const int row = grp * 8 + (col >> 1);
+                const i32x2 v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(LDS_PTR(
+                    i32x2, cur + row * TL::kLatent + (cb ^ swizzle(row)) * 16 + (col & 1) * 8));
+                vf = widen((uint32_t)v[0], (uint32_t)v[1]);
+            } else {
+                union {
+                    s16x4 half[2];
+                    frag f;
+                } u;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int row = grp * 8 + h * 4 + (col >> 2);
+                    const int chunk = (cb * 2 + ((col >> 1) & 1)) ^ swizzle(row);
+                    u.half[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                        LDS_PTR(s16x4, cur + row * TL::kLatent + chunk * 16 + (col & 1) * 8));
+                }
+                vf = u.f;
+            }
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb)
-                pf[mb] = *reinterpret_cast<const frag *>(&sP[gi][mb * 16 + col][st * 32 + grp * 8]);
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                const int cb = wave * NC + c;  // block of 16 columns
-                frag vf;
-                if constexpr (kFp8) {
-                    const int vrow = st * 32 + grp * 8 + (col >> 1);
-                    const int chunk = cb ^ swizzle(vrow);
-                    const i32x2 v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                        LDS_PTR(i32x2, cur + vrow * TL::kLatent + chunk * 16 + (col & 1) * 8));
-                    vf = widen((uint32_t)v[0], (uint32_t)v[1]);
-                } else {
-                    union {
-                        s16x4 half[2];
-                        frag f;
-                    } u;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int vrow = st * 32 + grp * 8 + h * 4 + (col >> 2);
-                        const int chunk = (cb * 2 + ((col >> 1) & 1)) ^ swizzle(vrow);
-                        u.half[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                            LDS_PTR(s16x4, cur + vrow * TL::kLatent + chunk * 16 + (col & 1) * 8));
-                    }
-                    vf = u.f;
-                }
-#pragma unroll
-                for (int mb = 0; mb < MB; ++mb)
-                    o[c][mb] = M::mul(vf, pf[mb], o[c][mb]);
-            }
+                o[c][mb] = M::mul(vf, pf[mb], o[c][mb]);
         }
-        row = address(e, list.loc ? sWord[t & 1][mine] : 0);
-        e = e3;
     };
 
     if (t0 < t1) {
+        // the entries, words and addresses of the first tiles
         const int32_t *map = list.map;
         const int e0 = entry(t0, map ? map[at(t0)] : 0);
         const int e1 = entry(t0 + 1, map ? map[at(t0 + 1)] : 0);
@@ -569,30 +585,55 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
         if (lane < kRows)
             sWord[t0 & 1][mine] = word(e);
         const uint8_t *row = address(e0, word(e0));
-        fetch(buf0, t0, row);
+        fetch(t0, row);
         row = address(e1, word(e1));
-        for (int t = t0; t < t1; t += 2) {
-            step(buf0, buf1, t, row, e);
+        for (int t = t0; t < t1; ++t) {
+            // tile t has arrived, and the probabilities of tile t - 1 are in LDS
+            barrier_all();
+            if (t > t0)
+                settle(t - 1);
+            // on their way from here: the rows of tile t + 1, the words of
+            // tile t + 3, the map's entries of tile t + 4
             if (t + 1 < t1)
-                step(buf1, buf0, t + 1, row, e);
+                fetch(t + 1, row);
+            const int e3 = entry(t + 3, map ? sEntry[(t + 3) & 1][mine] : 0);
+            if (t + 3 < t1 && lane < kRows) {
+                if (list.loc)
+                    load_lds4(lds_offset(&sWord[(t + 3) & 1][wave * kRows]),
+                              list.loc + (e3 >= 0 ? e3 : 0));
+                if (map)
+                    load_lds4(lds_offset(&sEntry[t & 1][wave * kRows]), map + at(t + 4));
+            }
+            scores(t);
+            barrier_lds();
+            if (threadIdx.x == 0)
+                sExceeds[(t + 1) & 1] = 0;  // read by everyone, set again after the next barrier
+            if (t > t0)
+                values(t - 1);
+            softmax(t);
+            row = address(e, list.loc ? sWord[t & 1][mine] : 0);
+            e = e3;
         }
+        barrier_lds();
+        settle(t1 - 1);
+        values(t1 - 1);
     }
 
-    // the sums of the waves (and 4 lane groups) that share a query row
+    // the sums of the waves and lane groups that share a query row
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
     barrier_lds();
-    if (grp == 0)
-        sMax[rg][hg * 16 + col] = l;
+    if (grp == 0 && onum == 0)
+        sMax[orow][oblk * 16 + col] = l;
     barrier_lds();
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
         const int x = x0 + mb * 16 + col;
         if (x >= a.unit_rows)
             continue;
-        float sum = 0.f;
+        float sum = 0.f;  // of the query row
 #pragma unroll
-        for (int k = 0; k < RG; ++k)
+        for (int k = 0; k < kTile / 16; ++k)
             sum += sMax[k][mb * 16 + col];
         const int64_t at = (int64_t)unit * a.unit_rows + x;  // query row of the call
         const int c0 = wave * (DV / NW) + grp * 4;
@@ -658,12 +699,10 @@ template <int FMT, int DV, int DR>
 hipError_t launch_dims(const kvr_ctx *c, const AttendArgs &a, int block, dim3 grid, hipStream_t s)
 {
     if (block == 16)
-        return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 1, 4, 4>, grid, dim3(256), 0,
-                      s, a);
+        return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 1, 4>, grid, dim3(256), 0, s, a);
     if (block == 32)
-        return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 2, 8, 4>, grid, dim3(512), 0,
-                      s, a);
-    return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 4, 8, 2>, grid, dim3(512), 0, s, a);
+        return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 2, 8>, grid, dim3(512), 0, s, a);
+    return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 4, 8>, grid, dim3(512), 0, s, a);
 }
 
 template <int FMT>
