@@ -158,30 +158,31 @@ struct RowList {
     const int32_t *map;   // this query's entries of the union, or null
     const uint32_t *loc;  // this entry's words, or null
     const uint8_t *rows;  // this entry's gathered rows, or null
+    const uint8_t *tail, *pool, *hot;  // the request's places
     int len;              // entries of the list
     int count;            // entries of the selection
 };
 
-// Address of the row of word w (position j of the selection), or null when it
-// is left out.
-__device__ __forceinline__ const uint8_t *row_address(const AttendArgs &a, const LayerPtrs &lp,
-                                                      const RowList &list, int r, int j, uint32_t w,
-                                                      bool &bad)
+// Address of the row of word w (entry e of the selection, -1: none), or null
+// when it is left out; bad: w lies outside its place.
+__device__ __forceinline__ const uint8_t *row_address(const Shape &sh, const RowList &list, int e,
+                                                      uint32_t w, bool &bad)
 {
+    const bool in = e >= 0 && w != KVR_LOC_INVALID;
     bad = false;
-    if (w == KVR_LOC_INVALID)
-        return nullptr;
     if (list.rows)
-        return list.rows + (int64_t)j * a.sh.R;
-    const uint32_t place = w >> kPlaceShift, idx = w & kIndexMask;
-    if (place == KVR_PLACE_TAIL && idx < (uint32_t)a.sh.T)
-        return lp.tail + ((int64_t)r * a.sh.T + idx) * a.sh.R;
-    if (place == KVR_PLACE_PAGE && (int64_t)idx < a.sh.pool_rows)
-        return lp.pool + (int64_t)idx * a.sh.R;
-    if (place == KVR_PLACE_HOT && (idx & kSlotMask) < (uint32_t)a.sh.B)
-        return lp.hot + ((int64_t)r * a.sh.B + (idx & kSlotMask)) * a.sh.R;
-    bad = true;
-    return nullptr;
+        return in ? list.rows + (uint64_t)(uint32_t)e * (uint32_t)sh.R : nullptr;
+    const uint32_t place = w >> kPlaceShift;
+    const bool tail = place == KVR_PLACE_TAIL, page = place == KVR_PLACE_PAGE;
+    const uint32_t idx = w & (place == KVR_PLACE_HOT ? kSlotMask : kIndexMask);
+    const uint32_t limit = tail ? (uint32_t)sh.T : page ? (uint32_t)sh.pool_rows : (uint32_t)sh.B;
+    // (opaque, so that the choice is made between registers)
+    const uint8_t *at_tail = list.tail, *at_page = list.pool, *at_hot = list.hot;
+    asm("" : "+s"(at_tail), "+s"(at_page), "+s"(at_hot));
+    const uint8_t *base = tail ? at_tail : page ? at_page : at_hot;
+    const bool ok = place != KVR_PLACE_INVALID && idx < limit;
+    bad = in && !ok;
+    return in && ok ? base + (uint64_t)idx * (uint32_t)sh.R : nullptr;
 }
 
 // A tile in LDS: latents, rope parts and (8-bit rows) scales, each part
@@ -196,36 +197,56 @@ struct Tile {
     static constexpr int kScalesAt = kRopeAt + kTile * kRope;
     static constexpr int kBytes = kScalesAt + kTile * kScales;
 
-    // Loads rows [first, first + ROWS) of the tile at LDS offset `lds`, lane
-    // i < ROWS holding the address of row first + i.  Each instruction writes
-    // up to 1024 consecutive bytes of a part.
+    // The direct loads of ROWS rows, each of up to 1024 consecutive bytes of a
+    // part in LDS.
     template <int ROWS>
-    static __device__ __forceinline__ void load(uint32_t lds, int first, const uint8_t *row)
-    {
-        const int lane = lane_id();
-        const uint32_t lo = (uint32_t)(uintptr_t)row, hi = (uint32_t)((uintptr_t)row >> 32);
-        auto part = [&](auto per_row, int at, int from) {
-            constexpr int C = decltype(per_row)::value / 16;  // chunks per row
-            constexpr int N = 64 / C < ROWS ? 64 / C : ROWS;  // rows per instruction
-            static_assert(ROWS % N == 0, "whole rows per instruction");
-#pragma unroll
-            for (int i = 0; i < ROWS; i += N) {
-                const int k = i + lane / C;
+    struct Loads {
+        static constexpr int kLatentRows = 1024 / kLatent < ROWS ? 1024 / kLatent : ROWS;
+        static constexpr int kRopeRows = DR == 0 ? ROWS : 1024 / kRope < ROWS ? 1024 / kRope : ROWS;
+        static constexpr int kLatentLoads = ROWS / kLatentRows;
+        static constexpr int kRopeLoads = DR == 0 ? 0 : ROWS / kRopeRows;
+        const uint8_t *src[kLatentLoads + kRopeLoads + (kFp8 ? 1 : 0)];
+
+        // Lane i < ROWS holds the address of row first + i of the tile.
+        __device__ __forceinline__ void prepare(int first, const uint8_t *row)
+        {
+            const int lane = lane_id();
+            const uint32_t lo = (uint32_t)(uintptr_t)row, hi = (uint32_t)((uintptr_t)row >> 32);
+            auto source = [&](int k, int chunks, int from) __attribute__((always_inline)) {
                 const uint64_t p = (uint64_t)(uint32_t)__shfl((int)hi, k) << 32 |
                                    (uint32_t)__shfl((int)lo, k);
-                const int chunk = (lane % C) ^ swizzle(first + k);
-                if (N * C == 64 || lane < N * C)
-                    load_lds16(lds + at + (first + i) * C * 16,
-                               reinterpret_cast<const uint8_t *>(p) + from + chunk * 16);
-            }
-        };
-        part(std::integral_constant<int, kLatent>(), 0, 0);
-        if constexpr (DR > 0)
-            part(std::integral_constant<int, kRope>(), kRopeAt, kLatent + kScales);
-        if constexpr (kFp8)
-            if (lane < ROWS)
-                load_lds16(lds + kScalesAt + first * 16, row + kLatent);
-    }
+                const int chunk = (lane % chunks) ^ swizzle(first + k);
+                return reinterpret_cast<const uint8_t *>(p) + from + chunk * 16;
+            };
+#pragma unroll
+            for (int i = 0; i < kLatentLoads; ++i)
+                src[i] = source(i * kLatentRows + lane / (kLatent / 16), kLatent / 16, 0);
+#pragma unroll
+            for (int i = 0; i < kRopeLoads; ++i)
+                src[kLatentLoads + i] =
+                    source(i * kRopeRows + lane / (kRope / 16), kRope / 16, kLatent + kScales);
+            if constexpr (kFp8)
+                src[kLatentLoads + kRopeLoads] = row + kLatent;
+        }
+
+        // Starts them, into the tile at LDS offset `lds`.
+        __device__ __forceinline__ void start(uint32_t lds, int first) const
+        {
+            const int lane = lane_id();
+#pragma unroll
+            for (int i = 0; i < kLatentLoads; ++i)
+                if (kLatentRows * kLatent == 1024 || lane < kLatentRows * kLatent / 16)
+                    load_lds16(lds + (first + i * kLatentRows) * kLatent, src[i]);
+#pragma unroll
+            for (int i = 0; i < kRopeLoads; ++i)
+                if (kRopeRows * kRope == 1024 || lane < kRopeRows * kRope / 16)
+                    load_lds16(lds + kRopeAt + (first + i * kRopeRows) * kRope,
+                               src[kLatentLoads + i]);
+            if constexpr (kFp8)
+                if (lane < ROWS)
+                    load_lds16(lds + kScalesAt + first * 16, src[kLatentLoads + kRopeLoads]);
+        }
+    };
 };
 
 template <int FMT, int DV, int DR, int MB, int NW>
@@ -290,9 +311,13 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
                          : nullptr;
     if (!known && a.c.status && threadIdx.x == 0)
         a.c.status[i] = KVR_E_ARG;
-    LayerPtrs lp{};
-    if (!list.rows && list.len > 0)
-        lp = a.layers[a.c.layer];
+    list.tail = list.pool = list.hot = nullptr;
+    if (!list.rows && list.len > 0) {
+        const LayerPtrs lp = a.layers[a.c.layer];
+        list.tail = lp.tail + (int64_t)r * a.sh.T * a.sh.R;
+        list.pool = lp.pool;
+        list.hot = lp.hot + (int64_t)r * a.sh.B * a.sh.R;
+    }
 
     const int tiles = (list.len + kTile - 1) / kTile;
     const int per = (tiles + a.shares - 1) / a.shares;
@@ -361,29 +386,33 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
         const int e = list.map ? mapped : t * kTile + mine;
         return t < t1 && t * kTile + mine < list.len && e >= 0 && e < list.count ? e : -1;
     };
-    auto address = [&](int e, uint32_t w) {
-        bool bad = false;
-        const uint8_t *p = e >= 0 ? row_address(a, lp, list, r, e, w, bad) : nullptr;
-        if (bad && a.c.status)
+    const uint8_t *zeros = zero_row;
+    asm volatile("" : "+s"(zeros));  // kept, not looked up for each tile
+    typename TL::template Loads<kRows> loads;  // of the tile fetched next
+    uint64_t valid = 0;                        // and which of its rows count
+    auto prepare = [&](int e, uint32_t w) __attribute__((always_inline)) {
+        bool bad;
+        const uint8_t *p = row_address(a.sh, list, e, w, bad);
+        if (__any(bad) && bad && a.c.status)
             a.c.status[i] = KVR_E_RANGE;
-        return p;
+        valid = __ballot(p != nullptr);
+        loads.prepare(wave * kRows, p ? p : zeros);
     };
-    // Starts tile t's loads and notes which of its rows count.
-    auto tile = [&](int t) { return sTile + (t - t0) % 3 * TL::kBytes; };
-    auto fetch = [&](int t, const uint8_t *row) {
-        const uint64_t valid = __ballot(row != nullptr);
+    const uint32_t tiles_at = lds_offset(sTile);
+    auto fetch = [&](int buf, int t) __attribute__((always_inline)) {
+        loads.start(tiles_at + buf, wave * kRows);
         if (lane == 0)
             sValid[t & 1][wave] = (uint8_t)(valid & ((1 << kRows) - 1));
-        TL::template load<kRows>(lds_offset(tile(t)), wave * kRows, row ? row : zero_row);
     };
 
     const float to_log2 = a.c.scale * 1.44269504088896340736f;
     f32x4 s;         // t_j of the block this wave owns
     float sum = 0.f;  // and the sum of their probabilities
 
-    // This wave's part of tile t's scores, into LDS.
-    auto scores = [&](int t) {
-        const uint8_t *cur = tile(t);
+    // (buf: where a tile lies in sTile)
+    // This wave's part of a tile's scores, into LDS.
+    auto scores = [&](int buf) __attribute__((always_inline)) {
+        const uint8_t *cur = sTile + buf;
         const int swz = swizzle(col);  // of row 16 n + col
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb) {
@@ -451,7 +480,7 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
     };
 
     // Probabilities of the block this wave owns, of tile t, into LDS.
-    auto write_p = [&](int t) {
+    auto write_p = [&](int buf, int t) __attribute__((always_inline)) {
         const float ref = mq == -__builtin_inff() ? 0.f : mq;
         float p[4];
 #pragma unroll
@@ -462,7 +491,7 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
         const int at = ((orow * 2 + (grp >> 1)) ^ ((col >> 1) & 3)) * 8 + (grp & 1) * 4;
         if constexpr (kFp8) {
             constexpr int G = kGroups / kOwners > 0 ? kGroups / kOwners : 1;
-            const uint8_t *sc = tile(t) + TL::kScalesAt + (orow * 16 + grp * 4) * 16;
+            const uint8_t *sc = sTile + buf + TL::kScalesAt + (orow * 16 + grp * 4) * 16;
             f32x4 w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -488,26 +517,26 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
         }
     };
 
-    auto softmax = [&](int t) {
+    auto softmax = [&](int buf, int t) __attribute__((always_inline)) {
         const f32x4(*part)[64] = sScore[orow * MB + oblk];
         s = ((part[0][lane] + part[1][lane]) + part[2][lane]) + part[3][lane];
         const int first = orow * 16 + grp * 4;
-        const uint32_t valid = sValid[t & 1][first / kRows] >> (first % kRows);
+        const uint32_t counts = sValid[t & 1][first / kRows] >> (first % kRows);
         bool exceeds = false;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            s[k] = (valid >> k) & 1 ? s[k] * to_log2 : -__builtin_inff();
+            s[k] = (counts >> k) & 1 ? s[k] * to_log2 : -__builtin_inff();
             exceeds |= s[k] > mq + kSlack;
         }
         if (__any(exceeds) && lane == 0)
             sExceeds[t & 1] = 1;
-        write_p(t);
+        write_p(buf, t);
     };
 
     // Once tile t's probabilities are in LDS: if one exceeded its reference,
     // the maximum becomes the reference, the sums so far are scaled down and
     // the tile's probabilities written again.
-    auto settle = [&](int t) {
+    auto settle = [&](int buf, int t) __attribute__((always_inline)) {
         if (sExceeds[t & 1]) {
             float top = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
             top = fmaxf(top, __shfl_xor(top, 16));
@@ -529,15 +558,15 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
                 for (int c = 0; c < NC; ++c)
                     o[c][mb] *= alpha;
             }
-            write_p(t);
+            write_p(buf, t);
             barrier_lds();
         }
         l += sum;
     };
 
     // o[column][query row] += latent[row][column] * p[query row][row] of tile t
-    auto values = [&](int t) {
-        const uint8_t *cur = tile(t);
+    auto values = [&](int buf, int t) __attribute__((always_inline)) {
+        const uint8_t *cur = sTile + buf;
         const int gi = kFp8 ? wave * (DV / NW) / kScaleGroup : 0;
         frag pf[MB];
 #pragma unroll
@@ -584,18 +613,19 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
             sEntry[(t0 + 3) & 1][mine] = map[at(t0 + 3)];
         if (lane < kRows)
             sWord[t0 & 1][mine] = word(e);
-        const uint8_t *row = address(e0, word(e0));
-        fetch(t0, row);
-        row = address(e1, word(e1));
+        int prev = 2 * TL::kBytes, cur = 0, next = TL::kBytes;  // the buffers' roles
+        prepare(e0, word(e0));
+        fetch(cur, t0);
+        prepare(e1, word(e1));
         for (int t = t0; t < t1; ++t) {
             // tile t has arrived, and the probabilities of tile t - 1 are in LDS
             barrier_all();
             if (t > t0)
-                settle(t - 1);
+                settle(prev, t - 1);
             // on their way from here: the rows of tile t + 1, the words of
             // tile t + 3, the map's entries of tile t + 4
             if (t + 1 < t1)
-                fetch(t + 1, row);
+                fetch(next, t + 1);
             const int e3 = entry(t + 3, map ? sEntry[(t + 3) & 1][mine] : 0);
             if (t + 3 < t1 && lane < kRows) {
                 if (list.loc)
@@ -604,19 +634,21 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
                 if (map)
                     load_lds4(lds_offset(&sEntry[t & 1][wave * kRows]), map + at(t + 4));
             }
-            scores(t);
+            scores(cur);
             barrier_lds();
             if (threadIdx.x == 0)
                 sExceeds[(t + 1) & 1] = 0;  // read by everyone, set again after the next barrier
             if (t > t0)
-                values(t - 1);
-            softmax(t);
-            row = address(e, list.loc ? sWord[t & 1][mine] : 0);
+                values(prev, t - 1);
+            softmax(cur, t);
+            prepare(e, list.loc ? sWord[t & 1][mine] : 0);
             e = e3;
+            const int free = prev;
+            prev = cur, cur = next, next = free;
         }
         barrier_lds();
-        settle(t1 - 1);
-        values(t1 - 1);
+        settle(prev, t1 - 1);
+        values(prev, t1 - 1);
     }
 
     // the sums of the waves and lane groups that share a query row
