@@ -13,17 +13,17 @@
 // and the sums are scaled down.
 //
 // A workgroup of NW waves owns MB blocks of 16 query rows and a share of the
-// selection, which it walks in tiles of 32 rows.  Three tiles are in LDS: the
-// values of one are summed while the scores of the next are computed and the
-// one after is on its way (16-byte direct loads to LDS, addresses from the
-// location words, which are read two tiles earlier still).
-//   scores   the d_v + d_rope products of a score are split over four waves,
-//            each with its quarter of the queries in registers and reading its
-//            quarter of the keys once (16x16x32 MFMA); the partial sums pass
-//            through LDS;
+// selection, which it walks in tiles of TILE rows, kept in LDS.  Tiles arrive
+// by 16-byte direct loads to LDS, addresses from the location words, which are
+// read two tiles earlier still.
+//   scores   a wave computes 16 of the tile's rows for one block of query rows
+//            by 16x16x32 MFMA, the keys from LDS and the queries in registers;
 //   values   every wave takes d_v / NW columns of all query rows; the
 //            probabilities pass through LDS, the latents are read transposed
 //            (ds_read_tr), so the product needs no copy of the tile.
+// With three tiles in LDS the values of one are summed beside the scores of
+// the next, while the one after is on its way, and a tile costs one barrier;
+// with two (where three do not fit), its values follow its own scores.
 // Both products leave a query row in one lane (mod 16), so the running
 // maximum, the sums and their corrections stay in registers.
 //
@@ -44,7 +44,6 @@
 namespace kvr {
 namespace {
 
-constexpr int kTile = 32;     // rows per tile
 constexpr float kSlack = 8.f; // log2 of the largest probability kept
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -186,16 +185,16 @@ __device__ __forceinline__ const uint8_t *row_address(const Shape &sh, const Row
 }
 
 // A tile in LDS: latents, rope parts and (8-bit rows) scales, each part
-// [kTile rows][its bytes].
-template <int FMT, int DV, int DR>
+// [TILE rows][its bytes].
+template <int FMT, int DV, int DR, int TILE>
 struct Tile {
     static constexpr bool kFp8 = FMT == KVR_ROW_FP8;
     static constexpr int kLatent = kFp8 ? DV : 2 * DV;  // bytes of a row's parts
     static constexpr int kRope = 2 * DR;
     static constexpr int kScales = kFp8 ? scale_bytes(DV) : 0;
-    static constexpr int kRopeAt = kTile * kLatent;
-    static constexpr int kScalesAt = kRopeAt + kTile * kRope;
-    static constexpr int kBytes = kScalesAt + kTile * kScales;
+    static constexpr int kRopeAt = TILE * kLatent;
+    static constexpr int kScalesAt = kRopeAt + TILE * kRope;
+    static constexpr int kBytes = kScalesAt + TILE * kScales;
 
     // The direct loads of ROWS rows, each of up to 1024 consecutive bytes of a
     // part in LDS.
@@ -249,44 +248,34 @@ struct Tile {
     };
 };
 
-template <int FMT, int DV, int DR, int MB, int NW>
-__global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
+template <int FMT, int DV, int DR, int MB, int TILE, int BUFS>
+__global__ __launch_bounds__(MB *TILE / 16 * 64) void attend_kernel(AttendArgs a)
 {
     typedef typename Elem<FMT>::type E;
     typedef Mfma<E> M;
     typedef typename M::frag frag;
     typedef E e4 __attribute__((ext_vector_type(4)));
-    typedef Tile<FMT, DV, DR> TL;
+    typedef Tile<FMT, DV, DR, TILE> TL;
     constexpr bool kFp8 = FMT == KVR_ROW_FP8;
-    constexpr int DQ = 4;                      // parts of a score
-    constexpr int kSteps = DV / DQ / 32;       // MFMA steps of a part of the latent
-    constexpr int RG = NW / DQ;                // row groups of the scores
-    constexpr int RB = kTile / 16 / RG;        // row blocks of a wave's scores
-    constexpr int kBlocks = kTile / 16 * MB;   // 16x16 blocks of scores
-    constexpr int kOwners = NW / kBlocks;      // waves that own one of them
-    constexpr int NC = DV / NW / 16;           // value column blocks of a wave
+    constexpr int kSteps = (DV + DR) / 32;    // MFMA steps of a score
+    constexpr int RG = TILE / 16;             // row blocks of a tile
+    constexpr int NW = MB * RG;               // waves: one block of scores each
+    constexpr int NC = DV / NW / 16;          // value column blocks of a wave
     constexpr int kGroups = kFp8 ? DV / kScaleGroup : 1;
-    constexpr int kRows = kTile / NW;          // rows a wave loads
-    static_assert(NW % DQ == 0 && NW % kBlocks == 0 && DV % (NW * 16) == 0, "");
-    static_assert(kOwners == 1 || kOwners == 2, "");
+    constexpr int kRows = TILE / NW;          // rows a wave loads
+    static_assert(DV % (NW * 16) == 0 && kRows >= 4 && kRows <= 16, "");
 
-    __shared__ __attribute__((aligned(1024))) uint8_t sTile[3 * TL::kBytes];
-    __shared__ f32x4 sScore[kBlocks][DQ][64];
-    __shared__ __attribute__((aligned(16))) E sP[2][kGroups][MB * 16][kTile];
-    __shared__ float sMax[kTile / 16][MB * 16];
-    __shared__ uint8_t sValid[2][NW];
-    __shared__ int sExceeds[2];
-    __shared__ uint32_t sWord[2][kTile];  // location words, and with a map the
-    __shared__ int32_t sEntry[2][kTile];  // entries, of tiles to come
+    __shared__ __attribute__((aligned(1024))) uint8_t sTile[BUFS * TL::kBytes];
+    __shared__ __attribute__((aligned(16))) E sP[BUFS - 1][kGroups][MB * 16][TILE];
+    __shared__ float sMax[RG][MB * 16];
+    __shared__ uint16_t sValid[2][NW];
+    __shared__ int sExceeds[3];  // whether a tile's probabilities must be written again
+    __shared__ uint32_t sWord[2][TILE];  // location words, and with a map the
+    __shared__ int32_t sEntry[2][TILE];  // entries, of tiles to come
 
     const int lane = lane_id(), col = lane & 15, grp = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(wave_id());
-    const int dq = wave % DQ, rg = wave / DQ;
-    // the block of scores this wave owns: row block, query block, and which of
-    // its owners the wave is
-    const int orow = RG == 2 ? rg : dq & 1;
-    const int oblk = MB == 4 ? dq : MB == 2 ? dq & 1 : 0;
-    const int onum = kOwners == 2 ? dq >> 1 : 0;
+    const int rg = wave % RG, hg = wave / RG;  // the wave's block of scores
 
     // workgroups of one selection and share are 8 apart: the same XCD's L2
     // serves their rows
@@ -319,7 +308,7 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
         list.hot = lp.hot + (int64_t)r * a.sh.B * a.sh.R;
     }
 
-    const int tiles = (list.len + kTile - 1) / kTile;
+    const int tiles = (list.len + TILE - 1) / TILE;
     const int per = (tiles + a.shares - 1) / a.shares;
     const int t0 = share * per;
     const int t1 = t0 + per < tiles ? t0 + per : tiles;
@@ -328,25 +317,21 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
     // unit is one query)
     const E *q = static_cast<const E *>(a.c.q) + (int64_t)i * a.c.q_stride_entry;
     const int x0 = g * (MB * 16);
-    frag qf[MB][kSteps], qr[MB];  // the wave's part of the queries
+    frag qf[kSteps];  // of the wave's block
     auto load_q = [&](auto read) {
+        const int x = x0 + hg * 16 + col;
+        const bool in = x < a.unit_rows && t0 < t1;
+        const int xc = in ? x : 0;
+        const int qi = a.c.map ? unit % a.c.nq : xc / a.c.heads;
+        const int h = a.c.map ? xc : xc % a.c.heads;
+        const E *p = q + (int64_t)qi * a.c.q_stride_query + (int64_t)h * a.c.q_stride_head;
+        const frag zero = {};
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb) {
-            const int x = x0 + mb * 16 + col;
-            const bool in = x < a.unit_rows && t0 < t1;
-            const int xc = in ? x : 0;
-            const int qi = a.c.map ? unit % a.c.nq : xc / a.c.heads;
-            const int h = a.c.map ? xc : xc % a.c.heads;
-            const E *p = q + (int64_t)qi * a.c.q_stride_query + (int64_t)h * a.c.q_stride_head;
-            const frag zero = {};
-#pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
-                // an 8-bit key fragment holds 8 of the 16 codes of one LDS read
-                const int d = dq * (DV / DQ) + (kFp8 ? s / 2 * 64 + grp * 16 + (s & 1) * 8
-                                                     : s * 32 + grp * 8);
-                qf[mb][s] = in ? read(p + d) : zero;
-            }
-            qr[mb] = in && dq < DR / 32 ? read(p + DV + dq * 32 + grp * 8) : zero;
+        for (int s = 0; s < kSteps; ++s) {
+            // an 8-bit key fragment holds 8 of the 16 codes of one LDS read
+            const int d = kFp8 && s < DV / 32 ? s / 2 * 64 + grp * 16 + (s & 1) * 8
+                                              : s * 32 + grp * 8;
+            qf[s] = in ? read(p + d) : zero;
         }
     };
     if (a.wide)
@@ -360,9 +345,9 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
             return f;
         });
 
-    // m: the reference of this lane's query row in each block; mq, l: the one
-    // of the block the wave owns scores of and this lane's share of its sum
-    float m[MB], mq = -__builtin_inff(), l = 0.f;
+    // m: the reference of this lane's query row in each block; m_own, l: the
+    // one of the wave's block and this lane's share of its sum
+    float m[MB], m_own = -__builtin_inff(), l = 0.f;
     f32x4 o[NC][MB];
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
@@ -371,7 +356,7 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
         for (int c = 0; c < NC; ++c)
             o[c][mb] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-    if (threadIdx.x < 2)
+    if (threadIdx.x < 3)
         sExceeds[threadIdx.x] = 0;
 
     // This lane's row of a tile (a wave's first kRows lanes; the others repeat
@@ -379,12 +364,12 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
     // address; a row past the list's end reads the last entry's.
     const int mine = wave * kRows + (lane & (kRows - 1));
     auto at = [&](int t) {
-        const int j = t * kTile + mine;
+        const int j = t * TILE + mine;
         return j < list.len ? j : list.len - 1;
     };
     auto entry = [&](int t, int mapped) {
-        const int e = list.map ? mapped : t * kTile + mine;
-        return t < t1 && t * kTile + mine < list.len && e >= 0 && e < list.count ? e : -1;
+        const int e = list.map ? mapped : t * TILE + mine;
+        return t < t1 && t * TILE + mine < list.len && e >= 0 && e < list.count ? e : -1;
     };
     const uint8_t *zeros = zero_row;
     asm volatile("" : "+s"(zeros));  // kept, not looked up for each tile
@@ -402,158 +387,130 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
     auto fetch = [&](int buf, int t) __attribute__((always_inline)) {
         loads.start(tiles_at + buf, wave * kRows);
         if (lane == 0)
-            sValid[t & 1][wave] = (uint8_t)(valid & ((1 << kRows) - 1));
+            sValid[t & 1][wave] = (uint16_t)(valid & ((1 << kRows) - 1));
     };
 
     const float to_log2 = a.c.scale * 1.44269504088896340736f;
-    f32x4 s;         // t_j of the block this wave owns
+    f32x4 s;          // t_j of the wave's block
     float sum = 0.f;  // and the sum of their probabilities
 
     // (buf: where a tile lies in sTile)
-    // This wave's part of a tile's scores, into LDS.
+    // Scores of the wave's block of a tile.
     auto scores = [&](int buf) __attribute__((always_inline)) {
         const uint8_t *cur = sTile + buf;
-        const int swz = swizzle(col);  // of row 16 n + col
+        const int row = rg * 16 + col;
+        const int swz = swizzle(col);
+        const int kchunk[2] = {(grp ^ swz) * 16, ((4 + grp) ^ swz) * 16};
+        const uint8_t *base = cur + row * TL::kLatent;
+        s = f32x4{0.f, 0.f, 0.f, 0.f};
+        if constexpr (DR > 0) {
+            const uint8_t *rope = cur + TL::kRopeAt + row * TL::kRope;
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
-            const int row = (rg * RB + rb) * 16;
-            const uint8_t *base = cur + (row + col) * TL::kLatent + dq * (TL::kLatent / DQ);
-            f32x4 acc[MB];
+            for (int st = 0; st < DR / 32; ++st)
+                s = M::mul(*reinterpret_cast<const frag *>(rope + kchunk[st & 1] + st / 2 * 128),
+                           qf[DV / 32 + st], s);
+        }
+        if constexpr (kFp8) {
+            const uint8_t *sc = cur + TL::kScalesAt + (rg * 16 + grp * 4) * 16;
 #pragma unroll
-            for (int mb = 0; mb < MB; ++mb)
-                acc[mb] = f32x4{0.f, 0.f, 0.f, 0.f};
-            if constexpr (kFp8) {
-                u32x4 v[kSteps / 2];
-                float sc[4];
-                // a quarter is 128 bytes (8 chunks) or, with d_v 256, half of that
+            for (int gi = 0; gi < kGroups; ++gi) {
+                f32x4 part{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int h = 0; h < kSteps / 2; ++h) {
-                    const int chunk = ((dq * (kSteps * 2) + h * 4 + grp) & 7) ^ swz;
-                    const int line = (dq * (kSteps * 2) + h * 4) / 8;
-                    v[h] = *reinterpret_cast<const u32x4 *>(cur + (row + col) * TL::kLatent +
-                                                            line * 128 + chunk * 16);
+                for (int h = 0; h < 2; ++h) {
+                    const u32x4 v = *reinterpret_cast<const u32x4 *>(base + kchunk[h] + gi * 128);
+                    part = M::mul(widen(v[0], v[1]), qf[gi * 4 + h * 2], part);
+                    part = M::mul(widen(v[2], v[3]), qf[gi * 4 + h * 2 + 1], part);
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    sc[k] = reinterpret_cast<const float *>(
-                        cur + TL::kScalesAt + (row + grp * 4 + k) * 16)[dq * (DV / DQ) / kScaleGroup];
-#pragma unroll
-                for (int h = 0; h < kSteps / 2; ++h) {
-                    const frag k0 = widen(v[h][0], v[h][1]), k1 = widen(v[h][2], v[h][3]);
-#pragma unroll
-                    for (int mb = 0; mb < MB; ++mb)
-                        acc[mb] = M::mul(k0, qf[mb][2 * h], acc[mb]);
-#pragma unroll
-                    for (int mb = 0; mb < MB; ++mb)
-                        acc[mb] = M::mul(k1, qf[mb][2 * h + 1], acc[mb]);
-                }
-#pragma unroll
-                for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        acc[mb][k] *= sc[k];
-            } else {
-                frag kf[kSteps];
-#pragma unroll
-                for (int st = 0; st < kSteps; ++st) {
-                    const int chunk = ((st * 4 + grp) & 7) ^ swz;
-                    kf[st] = *reinterpret_cast<const frag *>(base + st / 2 * 128 + chunk * 16);
-                }
-#pragma unroll
-                for (int st = 0; st < kSteps; ++st)
-#pragma unroll
-                    for (int mb = 0; mb < MB; ++mb)
-                        acc[mb] = M::mul(kf[st], qf[mb][st], acc[mb]);
+                    s[k] = fmaf(part[k], reinterpret_cast<const float *>(sc + k * 16)[gi], s[k]);
             }
-            if (dq < DR / 32) {
-                const int chunk = (dq * 4 + grp) ^ swz;
-                const frag kf = *reinterpret_cast<const frag *>(
-                    cur + TL::kRopeAt + (row + col) * TL::kRope + chunk * 16);
+        } else {
+            f32x4 odd{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int mb = 0; mb < MB; ++mb)
-                    acc[mb] = M::mul(kf, qr[mb], acc[mb]);
+            for (int st = 0; st < DV / 32; ++st) {
+                const frag kf = *reinterpret_cast<const frag *>(base + kchunk[st & 1] + st / 2 * 128);
+                if (st & 1)
+                    odd = M::mul(kf, qf[st], odd);
+                else
+                    s = M::mul(kf, qf[st], s);
             }
-#pragma unroll
-            for (int mb = 0; mb < MB; ++mb)
-                sScore[(rg * RB + rb) * MB + mb][dq][lane] = acc[mb];
+            s += odd;
         }
     };
 
-    // Probabilities of the block this wave owns, of tile t, into LDS.
+    // Probabilities of the wave's block of tile t, into LDS.
+    auto pchunk = [&](int head, int chunk) {  // 8 rows of a query row, swizzled
+        return (chunk ^ (TILE == 64 ? head & 7 : (head >> 1) & 3)) * 8;
+    };
     auto write_p = [&](int buf, int t) __attribute__((always_inline)) {
-        const float ref = mq == -__builtin_inff() ? 0.f : mq;
+        const float ref = m_own == -__builtin_inff() ? 0.f : m_own;
         float p[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             p[k] = exp2_hw(s[k] - ref);
         sum = (p[0] + p[1]) + (p[2] + p[3]);
-        const int head = oblk * 16 + col;
-        const int at = ((orow * 2 + (grp >> 1)) ^ ((col >> 1) & 3)) * 8 + (grp & 1) * 4;
+        const int head = hg * 16 + col;
+        const int at = pchunk(head, rg * 2 + (grp >> 1)) + (grp & 1) * 4;
+        const int pb = BUFS == 3 ? t & 1 : 0;
         if constexpr (kFp8) {
-            constexpr int G = kGroups / kOwners > 0 ? kGroups / kOwners : 1;
-            const uint8_t *sc = sTile + buf + TL::kScalesAt + (orow * 16 + grp * 4) * 16;
+            const uint8_t *sc = sTile + buf + TL::kScalesAt + (rg * 16 + grp * 4) * 16;
             f32x4 w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 w[k] = *reinterpret_cast<const f32x4 *>(sc + k * 16);
 #pragma unroll
-            for (int gi = 0; gi < G; ++gi) {
+            for (int gi = 0; gi < kGroups; ++gi) {
                 e4 v;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float f = w[k][gi];
-                    if constexpr (kOwners == 2)
-                        f = onum ? w[k][G + gi] : f;
-                    v[k] = (E)(p[k] * f);
-                }
-                *reinterpret_cast<e4 *>(&sP[t & 1][onum * G + gi][head][at]) = v;
+                for (int k = 0; k < 4; ++k)
+                    v[k] = (E)(p[k] * w[k][gi]);
+                *reinterpret_cast<e4 *>(&sP[pb][gi][head][at]) = v;
             }
-        } else if (onum == 0) {
+        } else {
             e4 v;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 v[k] = (E)p[k];
-            *reinterpret_cast<e4 *>(&sP[t & 1][0][head][at]) = v;
+            *reinterpret_cast<e4 *>(&sP[pb][0][head][at]) = v;
         }
     };
 
-    auto softmax = [&](int buf, int t) __attribute__((always_inline)) {
-        const f32x4(*part)[64] = sScore[orow * MB + oblk];
-        s = ((part[0][lane] + part[1][lane]) + part[2][lane]) + part[3][lane];
-        const int first = orow * 16 + grp * 4;
+    auto softmax = [&](int buf, int t, int flag) __attribute__((always_inline)) {
+        const int first = rg * 16 + grp * 4;
         const uint32_t counts = sValid[t & 1][first / kRows] >> (first % kRows);
         bool exceeds = false;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             s[k] = (counts >> k) & 1 ? s[k] * to_log2 : -__builtin_inff();
-            exceeds |= s[k] > mq + kSlack;
+            exceeds |= s[k] > m_own + kSlack;
         }
         if (__any(exceeds) && lane == 0)
-            sExceeds[t & 1] = 1;
+            sExceeds[flag] = 1;
         write_p(buf, t);
     };
 
     // Once tile t's probabilities are in LDS: if one exceeded its reference,
     // the maximum becomes the reference, the sums so far are scaled down and
     // the tile's probabilities written again.
-    auto settle = [&](int buf, int t) __attribute__((always_inline)) {
-        if (sExceeds[t & 1]) {
+    auto settle = [&](int buf, int t, int flag) __attribute__((always_inline)) {
+        if (sExceeds[flag]) {
             float top = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
             top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
             if (grp == 0)
-                sMax[orow][oblk * 16 + col] = top;
+                sMax[rg][hg * 16 + col] = top;
             barrier_lds();
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb) {
                 float to = m[mb];
 #pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)
+                for (int k = 0; k < RG; ++k)
                     to = fmaxf(to, sMax[k][mb * 16 + col]);
                 const float alpha = to == -__builtin_inff() ? 1.f : exp2_hw(m[mb] - to);
                 m[mb] = to;
-                mq = oblk == mb ? to : mq;
-                l = oblk == mb ? l * alpha : l;
+                m_own = hg == mb ? to : m_own;
+                l = hg == mb ? l * alpha : l;
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
                     o[c][mb] *= alpha;
@@ -568,37 +525,41 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
     auto values = [&](int buf, int t) __attribute__((always_inline)) {
         const uint8_t *cur = sTile + buf;
         const int gi = kFp8 ? wave * (DV / NW) / kScaleGroup : 0;
-        frag pf[MB];
+        const int pb = BUFS == 3 ? t & 1 : 0;
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb)
-            pf[mb] = *reinterpret_cast<const frag *>(
-                &sP[t & 1][gi][mb * 16 + col][(grp ^ ((col >> 1) & 3)) * 8]);
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const int cb = wave * NC + c;  // block of 16 columns
-            frag vf;
-            if constexpr (kFp8) {
-                const int row = grp * 8 + (col >> 1);
-                const i32x2 v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(LDS_PTR(
-                    i32x2, cur + row * TL::kLatent + (cb ^ swizzle(row)) * 16 + (col & 1) * 8));
-                vf = widen((uint32_t)v[0], (uint32_t)v[1]);
-            } else {
-                union {
-                    s16x4 half[2];
-                    frag f;
-                } u;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int row = grp * 8 + h * 4 + (col >> 2);
-                    const int chunk = (cb * 2 + ((col >> 1) & 1)) ^ swizzle(row);
-                    u.half[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                        LDS_PTR(s16x4, cur + row * TL::kLatent + chunk * 16 + (col & 1) * 8));
-                }
-                vf = u.f;
-            }
+        for (int st = 0; st < TILE / 32; ++st) {
+            frag pf[MB];
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb)
-                o[c][mb] = M::mul(vf, pf[mb], o[c][mb]);
+                pf[mb] = *reinterpret_cast<const frag *>(
+                    &sP[pb][gi][mb * 16 + col][pchunk(mb * 16 + col, st * 4 + grp)]);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const int cb = wave * NC + c;  // block of 16 columns
+                frag vf;
+                if constexpr (kFp8) {
+                    const int row = st * 32 + grp * 8 + (col >> 1);
+                    const i32x2 v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(LDS_PTR(
+                        i32x2, cur + row * TL::kLatent + (cb ^ swizzle(row)) * 16 + (col & 1) * 8));
+                    vf = widen((uint32_t)v[0], (uint32_t)v[1]);
+                } else {
+                    union {
+                        s16x4 half[2];
+                        frag f;
+                    } u;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int row = st * 32 + grp * 8 + h * 4 + (col >> 2);
+                        const int chunk = (cb * 2 + ((col >> 1) & 1)) ^ swizzle(row);
+                        u.half[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                            LDS_PTR(s16x4, cur + row * TL::kLatent + chunk * 16 + (col & 1) * 8));
+                    }
+                    vf = u.f;
+                }
+#pragma unroll
+                for (int mb = 0; mb < MB; ++mb)
+                    o[c][mb] = M::mul(vf, pf[mb], o[c][mb]);
+            }
         }
     };
 
@@ -613,15 +574,20 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
             sEntry[(t0 + 3) & 1][mine] = map[at(t0 + 3)];
         if (lane < kRows)
             sWord[t0 & 1][mine] = word(e);
-        int prev = 2 * TL::kBytes, cur = 0, next = TL::kBytes;  // the buffers' roles
+        // the roles of the buffers and of the flags
+        int prev = (BUFS - 1) * TL::kBytes, cur = 0, next = TL::kBytes;
+        int f_prev = 2, f_cur = 0, f_next = 1;
         prepare(e0, word(e0));
         fetch(cur, t0);
         prepare(e1, word(e1));
         for (int t = t0; t < t1; ++t) {
-            // tile t has arrived, and the probabilities of tile t - 1 are in LDS
+            // tile t has arrived, and (BUFS 3) the probabilities of tile t - 1
+            // are in LDS
             barrier_all();
-            if (t > t0)
-                settle(prev, t - 1);
+            if (threadIdx.x == 0)
+                sExceeds[f_next] = 0;  // set after the next barrier, read before this one
+            if (BUFS == 3 && t > t0)
+                settle(prev, t - 1, f_prev);
             // on their way from here: the rows of tile t + 1, the words of
             // tile t + 3, the map's entries of tile t + 4
             if (t + 1 < t1)
@@ -635,28 +601,35 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
                     load_lds4(lds_offset(&sEntry[t & 1][wave * kRows]), map + at(t + 4));
             }
             scores(cur);
-            barrier_lds();
-            if (threadIdx.x == 0)
-                sExceeds[(t + 1) & 1] = 0;  // read by everyone, set again after the next barrier
-            if (t > t0)
-                values(prev, t - 1);
-            softmax(cur, t);
+            if (BUFS == 3) {
+                if (t > t0)
+                    values(prev, t - 1);
+                softmax(cur, t, f_cur);
+            } else {
+                softmax(cur, t, f_cur);
+                barrier_lds();
+                settle(cur, t, f_cur);
+                values(cur, t);
+            }
             prepare(e, list.loc ? sWord[t & 1][mine] : 0);
             e = e3;
-            const int free = prev;
-            prev = cur, cur = next, next = free;
+            const int free = prev, f_free = f_prev;
+            prev = cur, cur = next, next = BUFS == 3 ? free : prev;
+            f_prev = f_cur, f_cur = f_next, f_next = f_free;
         }
-        barrier_lds();
-        settle(prev, t1 - 1);
-        values(prev, t1 - 1);
+        if (BUFS == 3) {
+            barrier_lds();
+            settle(prev, t1 - 1, f_prev);
+            values(prev, t1 - 1);
+        }
     }
 
     // the sums of the waves and lane groups that share a query row
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
     barrier_lds();
-    if (grp == 0 && onum == 0)
-        sMax[orow][oblk * 16 + col] = l;
+    if (grp == 0)
+        sMax[rg][hg * 16 + col] = l;
     barrier_lds();
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
@@ -665,7 +638,7 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
             continue;
         float sum = 0.f;  // of the query row
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
+        for (int k = 0; k < RG; ++k)
             sum += sMax[k][mb * 16 + col];
         const int64_t at = (int64_t)unit * a.unit_rows + x;  // query row of the call
         const int c0 = wave * (DV / NW) + grp * 4;
@@ -730,11 +703,14 @@ __global__ __launch_bounds__(DV / 4) void join_kernel(AttendArgs a)
 template <int FMT, int DV, int DR>
 hipError_t launch_dims(const kvr_ctx *c, const AttendArgs &a, int block, dim3 grid, hipStream_t s)
 {
+    constexpr int kBufs16 = FMT == KVR_ROW_FP8 || DV == 256 ? 3 : 2;  // what LDS holds
     if (block == 16)
-        return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 1, 4>, grid, dim3(256), 0, s, a);
+        return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 1, 64, kBufs16>, grid,
+                      dim3(256), 0, s, a);
     if (block == 32)
-        return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 2, 8>, grid, dim3(512), 0, s, a);
-    return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 4, 8>, grid, dim3(512), 0, s, a);
+        return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 2, 32, 3>, grid, dim3(256), 0,
+                      s, a);
+    return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 4, 32, 3>, grid, dim3(512), 0, s, a);
 }
 
 template <int FMT>
@@ -763,7 +739,8 @@ AttendPlan attend_plan(int32_t n, int32_t nq, int32_t heads, int32_t d_v, int32_
     const int32_t unit_rows = mapped ? heads : nq * heads;
     p.block = unit_rows <= 16 ? 16 : unit_rows <= 32 ? 32 : 64;
     p.groups = (unit_rows + p.block - 1) / p.block;
-    const int64_t tiles = (rows + kTile - 1) / kTile;
+    const int tile = p.block == 16 ? 64 : 32;
+    const int64_t tiles = (rows + tile - 1) / tile;
     int64_t shares = kWorkgroups / (units * p.groups);
     shares = shares < tiles ? shares : tiles;
     p.shares = (int32_t)(shares < 1 ? 1 : shares);
@@ -775,7 +752,7 @@ AttendPlan attend_plan(int32_t n, int32_t nq, int32_t heads, int32_t d_v, int32_
 // rows times tiles, and at most a block of 64 for each workgroup.
 int64_t attend_workspace_bound(int32_t n, int32_t nq, int32_t heads, int32_t d_v, int32_t rows)
 {
-    const int64_t all = (int64_t)n * nq * heads, tiles = (rows + kTile - 1) / kTile;
+    const int64_t all = (int64_t)n * nq * heads, tiles = (rows + 31) / 32;
     const int64_t most = all * tiles;
     if (tiles < 2)
         return 0;
