@@ -79,7 +79,7 @@ __device__ __forceinline__ void load_lds16(uint32_t lds, const void *src)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                  :
-                 : "s"(lds), "v"(src)
+                 : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(src)
                  : "memory", "m0");
 }
 
@@ -87,7 +87,7 @@ __device__ __forceinline__ void load_lds4(uint32_t lds, const void *src)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
                  :
-                 : "s"(lds), "v"(src)
+                 : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(src)
                  : "memory", "m0");
 }
 
@@ -156,30 +156,29 @@ __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2
 struct RowList {
     const int32_t *map;   // this query's entries of the union, or null
     const uint32_t *loc;  // this entry's words, or null
-    const uint8_t *rows;  // this entry's gathered rows, or null
-    const uint8_t *tail, *pool, *hot;  // the request's places
+    const uint8_t *tail, *pool, *hot;  // the request's places, or all the gathered rows
+    bool gathered;
     int len;              // entries of the list
     int count;            // entries of the selection
 };
 
 // Address of the row of word w (entry e of the selection, -1: none), or null
-// when it is left out; bad: w lies outside its place.
+// when it is left out; bad: w lies outside its place.  Selects only, so that
+// it is scheduled among the products.
 __device__ __forceinline__ const uint8_t *row_address(const Shape &sh, const RowList &list, int e,
                                                       uint32_t w, bool &bad)
 {
     const bool in = e >= 0 && w != KVR_LOC_INVALID;
-    bad = false;
-    if (list.rows)
-        return in ? list.rows + (uint64_t)(uint32_t)e * (uint32_t)sh.R : nullptr;
     const uint32_t place = w >> kPlaceShift;
     const bool tail = place == KVR_PLACE_TAIL, page = place == KVR_PLACE_PAGE;
-    const uint32_t idx = w & (place == KVR_PLACE_HOT ? kSlotMask : kIndexMask);
+    const uint32_t at = w & (place == KVR_PLACE_HOT ? kSlotMask : kIndexMask);
     const uint32_t limit = tail ? (uint32_t)sh.T : page ? (uint32_t)sh.pool_rows : (uint32_t)sh.B;
     // (opaque, so that the choice is made between registers)
     const uint8_t *at_tail = list.tail, *at_page = list.pool, *at_hot = list.hot;
     asm("" : "+s"(at_tail), "+s"(at_page), "+s"(at_hot));
     const uint8_t *base = tail ? at_tail : page ? at_page : at_hot;
-    const bool ok = place != KVR_PLACE_INVALID && idx < limit;
+    const bool ok = list.gathered || (place != KVR_PLACE_INVALID && at < limit);
+    const uint32_t idx = list.gathered ? (uint32_t)e : at;
     bad = in && !ok;
     return in && ok ? base + (uint64_t)idx * (uint32_t)sh.R : nullptr;
 }
@@ -212,10 +211,12 @@ struct Tile {
             const int lane = lane_id();
             const uint32_t lo = (uint32_t)(uintptr_t)row, hi = (uint32_t)((uintptr_t)row >> 32);
             auto source = [&](int k, int chunks, int from) __attribute__((always_inline)) {
-                const uint64_t p = (uint64_t)(uint32_t)__shfl((int)hi, k) << 32 |
-                                   (uint32_t)__shfl((int)lo, k);
-                const int chunk = (lane % chunks) ^ swizzle(first + k);
-                return reinterpret_cast<const uint8_t *>(p) + from + chunk * 16;
+                // (a 32-bit offset and its carry: one register each for the
+                // offsets the compiler keeps)
+                const uint32_t off = from + ((lane % chunks) ^ swizzle(first + k)) * 16;
+                const uint32_t l = (uint32_t)__shfl((int)lo, k) + off;
+                const uint32_t h = (uint32_t)__shfl((int)hi, k) + (l < off);
+                return reinterpret_cast<const uint8_t *>((uint64_t)h << 32 | l);
             };
 #pragma unroll
             for (int i = 0; i < kLatentLoads; ++i)
@@ -228,28 +229,27 @@ struct Tile {
                 src[kLatentLoads + kRopeLoads] = row + kLatent;
         }
 
-        // Starts them, into the tile at LDS offset `lds`.
-        __device__ __forceinline__ void start(uint32_t lds, int first) const
+        static constexpr int kCount = kLatentLoads + kRopeLoads + (kFp8 ? 1 : 0);
+        // Starts load n, into the tile at LDS offset `lds`.
+        __device__ __forceinline__ void start(int n, uint32_t lds, int first) const
         {
             const int lane = lane_id();
-#pragma unroll
-            for (int i = 0; i < kLatentLoads; ++i)
+            if (n < kLatentLoads) {
                 if (kLatentRows * kLatent == 1024 || lane < kLatentRows * kLatent / 16)
-                    load_lds16(lds + (first + i * kLatentRows) * kLatent, src[i]);
-#pragma unroll
-            for (int i = 0; i < kRopeLoads; ++i)
+                    load_lds16(lds + (first + n * kLatentRows) * kLatent, src[n]);
+            } else if (n < kLatentLoads + kRopeLoads) {
+                const int i = n - kLatentLoads;
                 if (kRopeRows * kRope == 1024 || lane < kRopeRows * kRope / 16)
-                    load_lds16(lds + kRopeAt + (first + i * kRopeRows) * kRope,
-                               src[kLatentLoads + i]);
-            if constexpr (kFp8)
-                if (lane < ROWS)
-                    load_lds16(lds + kScalesAt + first * 16, src[kLatentLoads + kRopeLoads]);
+                    load_lds16(lds + kRopeAt + (first + i * kRopeRows) * kRope, src[n]);
+            } else if (lane < ROWS) {
+                load_lds16(lds + kScalesAt + first * 16, src[n]);
+            }
         }
     };
 };
 
-template <int FMT, int DV, int DR, int MB, int TILE, int BUFS>
-__global__ __launch_bounds__(MB *TILE / 16 * 64) void attend_kernel(AttendArgs a)
+template <int FMT, int DV, int DR, int MB, int MQ, int TILE, int BUFS>
+__global__ __launch_bounds__(MB / MQ * TILE / 16 * 64) void attend_kernel(AttendArgs a)
 {
     typedef typename Elem<FMT>::type E;
     typedef Mfma<E> M;
@@ -259,7 +259,7 @@ __global__ __launch_bounds__(MB *TILE / 16 * 64) void attend_kernel(AttendArgs a
     constexpr bool kFp8 = FMT == KVR_ROW_FP8;
     constexpr int kSteps = (DV + DR) / 32;    // MFMA steps of a score
     constexpr int RG = TILE / 16;             // row blocks of a tile
-    constexpr int NW = MB * RG;               // waves: one block of scores each
+    constexpr int NW = MB / MQ * RG;          // waves: MQ blocks of scores each
     constexpr int NC = DV / NW / 16;          // value column blocks of a wave
     constexpr int kGroups = kFp8 ? DV / kScaleGroup : 1;
     constexpr int kRows = TILE / NW;          // rows a wave loads
@@ -269,13 +269,13 @@ __global__ __launch_bounds__(MB *TILE / 16 * 64) void attend_kernel(AttendArgs a
     __shared__ __attribute__((aligned(16))) E sP[BUFS - 1][kGroups][MB * 16][TILE];
     __shared__ float sMax[RG][MB * 16];
     __shared__ uint16_t sValid[2][NW];
-    __shared__ int sExceeds[3];  // whether a tile's probabilities must be written again
+    __shared__ int sExceeds[4];  // whether a tile's probabilities must be written again
     __shared__ uint32_t sWord[2][TILE];  // location words, and with a map the
     __shared__ int32_t sEntry[2][TILE];  // entries, of tiles to come
 
     const int lane = lane_id(), col = lane & 15, grp = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(wave_id());
-    const int rg = wave % RG, hg = wave / RG;  // the wave's block of scores
+    const int rg = wave % RG, hg = wave / RG;  // the wave's blocks of scores
 
     // workgroups of one selection and share are 8 apart: the same XCD's L2
     // serves their rows
@@ -295,13 +295,13 @@ __global__ __launch_bounds__(MB *TILE / 16 * 64) void attend_kernel(AttendArgs a
     list.len = a.c.map && list.count > 0 ? a.c.k : list.count;
     list.map = a.c.map ? a.c.map + (int64_t)unit * a.c.k : nullptr;
     list.loc = a.c.loc ? a.c.loc + (int64_t)i * a.c.stride : nullptr;
-    list.rows = a.c.rows ? static_cast<const uint8_t *>(a.c.rows) +
-                               (int64_t)i * a.c.stride * a.sh.R
-                         : nullptr;
+    list.gathered = a.c.rows != nullptr;
     if (!known && a.c.status && threadIdx.x == 0)
         a.c.status[i] = KVR_E_ARG;
-    list.tail = list.pool = list.hot = nullptr;
-    if (!list.rows && list.len > 0) {
+    if (list.gathered) {
+        list.tail = list.pool = list.hot =
+            static_cast<const uint8_t *>(a.c.rows) + (int64_t)i * a.c.stride * a.sh.R;
+    } else if (list.len > 0) {
         const LayerPtrs lp = a.layers[a.c.layer];
         list.tail = lp.tail + (int64_t)r * a.sh.T * a.sh.R;
         list.pool = lp.pool;
@@ -317,21 +317,24 @@ __global__ __launch_bounds__(MB *TILE / 16 * 64) void attend_kernel(AttendArgs a
     // unit is one query)
     const E *q = static_cast<const E *>(a.c.q) + (int64_t)i * a.c.q_stride_entry;
     const int x0 = g * (MB * 16);
-    frag qf[kSteps];  // of the wave's block
+    frag qf[MQ][kSteps];  // of the wave's blocks
     auto load_q = [&](auto read) {
-        const int x = x0 + hg * 16 + col;
-        const bool in = x < a.unit_rows && t0 < t1;
-        const int xc = in ? x : 0;
-        const int qi = a.c.map ? unit % a.c.nq : xc / a.c.heads;
-        const int h = a.c.map ? xc : xc % a.c.heads;
-        const E *p = q + (int64_t)qi * a.c.q_stride_query + (int64_t)h * a.c.q_stride_head;
-        const frag zero = {};
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            // an 8-bit key fragment holds 8 of the 16 codes of one LDS read
-            const int d = kFp8 && s < DV / 32 ? s / 2 * 64 + grp * 16 + (s & 1) * 8
-                                              : s * 32 + grp * 8;
-            qf[s] = in ? read(p + d) : zero;
+        for (int mq = 0; mq < MQ; ++mq) {
+            const int x = x0 + (hg * MQ + mq) * 16 + col;
+            const bool in = x < a.unit_rows && t0 < t1;
+            const int xc = in ? x : 0;
+            const int qi = a.c.map ? unit % a.c.nq : xc / a.c.heads;
+            const int h = a.c.map ? xc : xc % a.c.heads;
+            const E *p = q + (int64_t)qi * a.c.q_stride_query + (int64_t)h * a.c.q_stride_head;
+            const frag zero = {};
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                // an 8-bit key fragment holds 8 of the 16 codes of one LDS read
+                const int d = kFp8 && s < DV / 32 ? s / 2 * 64 + grp * 16 + (s & 1) * 8
+                                                  : s * 32 + grp * 8;
+                qf[mq][s] = in ? read(p + d) : zero;
+            }
         }
     };
     if (a.wide)
@@ -345,9 +348,9 @@ __global__ __launch_bounds__(MB *TILE / 16 * 64) void attend_kernel(AttendArgs a
             return f;
         });
 
-    // m: the reference of this lane's query row in each block; m_own, l: the
-    // one of the wave's block and this lane's share of its sum
-    float m[MB], m_own = -__builtin_inff(), l = 0.f;
+    // m: the reference of this lane's query row in each block; m_own, l: those
+    // of the wave's blocks and this lane's shares of their sums
+    float m[MB], m_own[MQ], l[MQ];
     f32x4 o[NC][MB];
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
@@ -355,6 +358,11 @@ __global__ __launch_bounds__(MB *TILE / 16 * 64) void attend_kernel(AttendArgs a
 #pragma unroll
         for (int c = 0; c < NC; ++c)
             o[c][mb] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+#pragma unroll
+    for (int mq = 0; mq < MQ; ++mq) {
+        m_own[mq] = -__builtin_inff();
+        l[mq] = 0.f;
     }
     if (threadIdx.x < 3)
         sExceeds[threadIdx.x] = 0;
@@ -375,131 +383,183 @@ __global__ __launch_bounds__(MB *TILE / 16 * 64) void attend_kernel(AttendArgs a
     asm volatile("" : "+s"(zeros));  // kept, not looked up for each tile
     typename TL::template Loads<kRows> loads;  // of the tile fetched next
     uint64_t valid = 0;                        // and which of its rows count
+    bool any_bad = false;
     auto prepare = [&](int e, uint32_t w) __attribute__((always_inline)) {
         bool bad;
         const uint8_t *p = row_address(a.sh, list, e, w, bad);
-        if (__any(bad) && bad && a.c.status)
-            a.c.status[i] = KVR_E_RANGE;
+        any_bad |= bad;
         valid = __ballot(p != nullptr);
         loads.prepare(wave * kRows, p ? p : zeros);
     };
+    // Words and entries that are not given are read as 0.
+    const uint32_t *loc = list.loc ? list.loc : reinterpret_cast<const uint32_t *>(zeros);
+    const int32_t *map = list.map ? list.map : reinterpret_cast<const int32_t *>(zeros);
+    auto word_at = [&](int e) { return loc + (list.loc && e >= 0 ? e : 0); };
+    auto entry_at = [&](int t) { return map + (list.map ? at(t) : 0); };
+    // Starts part `part` of `parts` of a tile's loads into a buffer.
     const uint32_t tiles_at = lds_offset(sTile);
-    auto fetch = [&](int buf, int t) __attribute__((always_inline)) {
-        loads.start(tiles_at + buf, wave * kRows);
-        if (lane == 0)
+    auto fetch = [&](int buf, int t, int part, int parts) __attribute__((always_inline)) {
+        constexpr int N = TL::template Loads<kRows>::kCount;
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            if (n * parts / N == part)
+                loads.start(n, tiles_at + buf, wave * kRows);
+        if (part == 0)
             sValid[t & 1][wave] = (uint16_t)(valid & ((1 << kRows) - 1));
     };
 
     const float to_log2 = a.c.scale * 1.44269504088896340736f;
-    f32x4 s;          // t_j of the wave's block
-    float sum = 0.f;  // and the sum of their probabilities
+    f32x4 s[MQ];    // t_j of the wave's blocks
+    float sum[MQ];  // and the sums of their probabilities
 
     // (buf: where a tile lies in sTile)
-    // Scores of the wave's block of a tile.
-    auto scores = [&](int buf) __attribute__((always_inline)) {
+    // LDS reads are issued in batches ahead of the products that use them
+    // (sched_barrier keeps them there: left alone, each read is moved next to
+    // its use and waited for).
+    f32x4 w[kFp8 ? 4 : 1];  // scales of this lane's 4 rows of the block
+    constexpr int kReads = TL::kLatent / 64;  // 16-byte reads of a key's latent
+    constexpr int kBatch = kFp8 ? 2 : 4;      // of them at once: a scale group, or 4 steps
+    constexpr int kBatches = kReads / kBatch;
+    struct Keys {
+        frag rope[DR > 0 ? DR / 32 : 1];
+        u32x4 latent[2][kBatch];
+    };
+    const int kchunk[2] = {(grp ^ swizzle(col)) * 16, ((4 + grp) ^ swizzle(col)) * 16};
+    auto read_keys = [&](Keys &key, int buf, int b) __attribute__((always_inline)) {
         const uint8_t *cur = sTile + buf;
         const int row = rg * 16 + col;
-        const int swz = swizzle(col);
-        const int kchunk[2] = {(grp ^ swz) * 16, ((4 + grp) ^ swz) * 16};
-        const uint8_t *base = cur + row * TL::kLatent;
-        s = f32x4{0.f, 0.f, 0.f, 0.f};
-        if constexpr (DR > 0) {
-            const uint8_t *rope = cur + TL::kRopeAt + row * TL::kRope;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int n = b * kBatch + j;
+            key.latent[b & 1][j] = *reinterpret_cast<const u32x4 *>(cur + row * TL::kLatent +
+                                                                    kchunk[n & 1] + n / 2 * 128);
+        }
+        if (b > 0)
+            return;
+        if constexpr (DR > 0)
 #pragma unroll
             for (int st = 0; st < DR / 32; ++st)
-                s = M::mul(*reinterpret_cast<const frag *>(rope + kchunk[st & 1] + st / 2 * 128),
-                           qf[DV / 32 + st], s);
-        }
-        if constexpr (kFp8) {
-            const uint8_t *sc = cur + TL::kScalesAt + (rg * 16 + grp * 4) * 16;
+                key.rope[st] = *reinterpret_cast<const frag *>(
+                    cur + TL::kRopeAt + row * TL::kRope + kchunk[st & 1] + st / 2 * 128);
+        if constexpr (kFp8)
 #pragma unroll
-            for (int gi = 0; gi < kGroups; ++gi) {
-                f32x4 part{0.f, 0.f, 0.f, 0.f};
+            for (int k = 0; k < 4; ++k)
+                w[k] = *reinterpret_cast<const f32x4 *>(cur + TL::kScalesAt +
+                                                        (rg * 16 + grp * 4 + k) * 16);
+    };
+    // Scores of the wave's block of a tile whose first keys are being read;
+    // then(b) starts what else is read or loaded beside batch b.
+    auto scores = [&](Keys &key, int buf, auto then) __attribute__((always_inline)) {
+        f32x4 even[MQ] = {}, odd[MQ] = {};
+#pragma unroll
+        for (int b = 0; b < kBatches; ++b) {
+            if (b + 1 < kBatches)
+                read_keys(key, buf, b + 1);
+            then(b);
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (kFp8) {
+                f32x4 part[2][MQ] = {};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const u32x4 v = *reinterpret_cast<const u32x4 *>(base + kchunk[h] + gi * 128);
-                    part = M::mul(widen(v[0], v[1]), qf[gi * 4 + h * 2], part);
-                    part = M::mul(widen(v[2], v[3]), qf[gi * 4 + h * 2 + 1], part);
+                    const u32x4 v = key.latent[b & 1][h];
+                    const frag k0 = widen(v[0], v[1]), k1 = widen(v[2], v[3]);
+#pragma unroll
+                    for (int mq = 0; mq < MQ; ++mq)
+                        part[h][mq] = M::mul(k0, qf[mq][b * 4 + h * 2], part[h][mq]);
+#pragma unroll
+                    for (int mq = 0; mq < MQ; ++mq)
+                        part[h][mq] = M::mul(k1, qf[mq][b * 4 + h * 2 + 1], part[h][mq]);
                 }
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    s[k] = fmaf(part[k], reinterpret_cast<const float *>(sc + k * 16)[gi], s[k]);
-            }
-        } else {
-            f32x4 odd{0.f, 0.f, 0.f, 0.f};
+                for (int mq = 0; mq < MQ; ++mq)
 #pragma unroll
-            for (int st = 0; st < DV / 32; ++st) {
-                const frag kf = *reinterpret_cast<const frag *>(base + kchunk[st & 1] + st / 2 * 128);
-                if (st & 1)
-                    odd = M::mul(kf, qf[st], odd);
-                else
-                    s = M::mul(kf, qf[st], s);
+                    for (int k = 0; k < 4; ++k)
+                        even[mq][k] = fmaf(part[0][mq][k] + part[1][mq][k], w[k][b], even[mq][k]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < kBatch; j += 2) {
+#pragma unroll
+                    for (int mq = 0; mq < MQ; ++mq)
+                        even[mq] = M::mul(__builtin_bit_cast(frag, key.latent[b & 1][j]),
+                                          qf[mq][b * kBatch + j], even[mq]);
+#pragma unroll
+                    for (int mq = 0; mq < MQ; ++mq)
+                        odd[mq] = M::mul(__builtin_bit_cast(frag, key.latent[b & 1][j + 1]),
+                                         qf[mq][b * kBatch + j + 1], odd[mq]);
+                }
             }
-            s += odd;
+            if (b == 0 && DR > 0)
+#pragma unroll
+                for (int st = 0; st < DR / 32; ++st)
+#pragma unroll
+                    for (int mq = 0; mq < MQ; ++mq)
+                        odd[mq] = M::mul(key.rope[st], qf[mq][DV / 32 + st], odd[mq]);
         }
+#pragma unroll
+        for (int mq = 0; mq < MQ; ++mq)
+            s[mq] = even[mq] + odd[mq];
     };
 
     // Probabilities of the wave's block of tile t, into LDS.
     auto pchunk = [&](int head, int chunk) {  // 8 rows of a query row, swizzled
         return (chunk ^ (TILE == 64 ? head & 7 : (head >> 1) & 3)) * 8;
     };
-    auto write_p = [&](int buf, int t) __attribute__((always_inline)) {
-        const float ref = m_own == -__builtin_inff() ? 0.f : m_own;
-        float p[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            p[k] = exp2_hw(s[k] - ref);
-        sum = (p[0] + p[1]) + (p[2] + p[3]);
-        const int head = hg * 16 + col;
-        const int at = pchunk(head, rg * 2 + (grp >> 1)) + (grp & 1) * 4;
+    auto write_p = [&](int t, const f32x4 *w) __attribute__((always_inline)) {
         const int pb = BUFS == 3 ? t & 1 : 0;
-        if constexpr (kFp8) {
-            const uint8_t *sc = sTile + buf + TL::kScalesAt + (rg * 16 + grp * 4) * 16;
-            f32x4 w[4];
+#pragma unroll
+        for (int mq = 0; mq < MQ; ++mq) {
+            const float ref = m_own[mq] == -__builtin_inff() ? 0.f : m_own[mq];
+            float p[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                w[k] = *reinterpret_cast<const f32x4 *>(sc + k * 16);
+                p[k] = exp2_hw(s[mq][k] - ref);
+            sum[mq] = (p[0] + p[1]) + (p[2] + p[3]);
+            const int head = (hg * MQ + mq) * 16 + col;
+            const int at = pchunk(head, rg * 2 + (grp >> 1)) + (grp & 1) * 4;
 #pragma unroll
             for (int gi = 0; gi < kGroups; ++gi) {
                 e4 v;
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    v[k] = (E)(p[k] * w[k][gi]);
+                for (int k = 0; k < 4; ++k) {
+                    if constexpr (kFp8)
+                        v[k] = (E)(p[k] * w[k][gi]);
+                    else
+                        v[k] = (E)p[k];
+                }
                 *reinterpret_cast<e4 *>(&sP[pb][gi][head][at]) = v;
             }
-        } else {
-            e4 v;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                v[k] = (E)p[k];
-            *reinterpret_cast<e4 *>(&sP[pb][0][head][at]) = v;
         }
     };
 
-    auto softmax = [&](int buf, int t, int flag) __attribute__((always_inline)) {
+    auto softmax = [&](int t, int flag) __attribute__((always_inline)) {
         const int first = rg * 16 + grp * 4;
         const uint32_t counts = sValid[t & 1][first / kRows] >> (first % kRows);
         bool exceeds = false;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            s[k] = (counts >> k) & 1 ? s[k] * to_log2 : -__builtin_inff();
-            exceeds |= s[k] > m_own + kSlack;
+        for (int mq = 0; mq < MQ; ++mq) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                s[mq][k] = (counts >> k) & 1 ? s[mq][k] * to_log2 : -__builtin_inff();
+                exceeds |= s[mq][k] > m_own[mq] + kSlack;
+            }
         }
-        if (__any(exceeds) && lane == 0)
-            sExceeds[flag] = 1;
-        write_p(buf, t);
+        sExceeds[__any(exceeds) ? flag : 3] = 1;
+        write_p(t, w);
     };
 
-    // Once tile t's probabilities are in LDS: if one exceeded its reference,
-    // the maximum becomes the reference, the sums so far are scaled down and
-    // the tile's probabilities written again.
-    auto settle = [&](int buf, int t, int flag) __attribute__((always_inline)) {
-        if (sExceeds[flag]) {
-            float top = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            if (grp == 0)
-                sMax[rg][hg * 16 + col] = top;
+    // Tile t's probabilities are in LDS and one exceeded its reference: the
+    // maximum becomes the reference, the sums so far are scaled down and the
+    // tile's probabilities written again.
+    auto settle = [&](int buf, int t) __attribute__((always_inline)) {
+        {
+#pragma unroll
+            for (int mq = 0; mq < MQ; ++mq) {
+                float top = fmaxf(fmaxf(s[mq][0], s[mq][1]), fmaxf(s[mq][2], s[mq][3]));
+                top = fmaxf(top, __shfl_xor(top, 16));
+                top = fmaxf(top, __shfl_xor(top, 32));
+                if (grp == 0)
+                    sMax[rg][(hg * MQ + mq) * 16 + col] = top;
+            }
             barrier_lds();
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb) {
@@ -509,127 +569,212 @@ __global__ __launch_bounds__(MB *TILE / 16 * 64) void attend_kernel(AttendArgs a
                     to = fmaxf(to, sMax[k][mb * 16 + col]);
                 const float alpha = to == -__builtin_inff() ? 1.f : exp2_hw(m[mb] - to);
                 m[mb] = to;
-                m_own = hg == mb ? to : m_own;
-                l = hg == mb ? l * alpha : l;
+                m_own[mb % MQ] = hg == mb / MQ ? to : m_own[mb % MQ];
+                l[mb % MQ] = hg == mb / MQ ? l[mb % MQ] * alpha : l[mb % MQ];
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
                     o[c][mb] *= alpha;
             }
-            write_p(buf, t);
+            f32x4 sc[kFp8 ? 4 : 1];  // the tile's scales once more
+            if constexpr (kFp8)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    sc[k] = *reinterpret_cast<const f32x4 *>(sTile + buf + TL::kScalesAt +
+                                                             (rg * 16 + grp * 4 + k) * 16);
+            write_p(t, sc);
             barrier_lds();
         }
-        l += sum;
+    };
+    auto count = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int mq = 0; mq < MQ; ++mq)
+            l[mq] += sum[mq];
     };
 
-    // o[column][query row] += latent[row][column] * p[query row][row] of tile t
-    auto values = [&](int buf, int t) __attribute__((always_inline)) {
-        const uint8_t *cur = sTile + buf;
-        const int gi = kFp8 ? wave * (DV / NW) / kScaleGroup : 0;
+    // o[column][query row] += latent[row][column] * p[query row][row] of tile t:
+    // its operands, then the products.
+    struct Operands {
+        frag p[TILE / 32][MB];
+        i32x2 v[TILE / 32][NC][kFp8 ? 1 : 2];
+    };
+    const int gi_own = kFp8 ? wave * (DV / NW) / kScaleGroup : 0;
+    auto read_p = [&](Operands &op, int t) __attribute__((always_inline)) {
         const int pb = BUFS == 3 ? t & 1 : 0;
 #pragma unroll
-        for (int st = 0; st < TILE / 32; ++st) {
-            frag pf[MB];
+        for (int st = 0; st < TILE / 32; ++st)
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb)
-                pf[mb] = *reinterpret_cast<const frag *>(
-                    &sP[pb][gi][mb * 16 + col][pchunk(mb * 16 + col, st * 4 + grp)]);
+                op.p[st][mb] = *reinterpret_cast<const frag *>(
+                    &sP[pb][gi_own][mb * 16 + col][pchunk(mb * 16 + col, st * 4 + grp)]);
+    };
+    auto read_v = [&](Operands &op, int buf) __attribute__((always_inline)) {
+        const uint8_t *cur = sTile + buf;
+#pragma unroll
+        for (int st = 0; st < TILE / 32; ++st) {
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 const int cb = wave * NC + c;  // block of 16 columns
-                frag vf;
                 if constexpr (kFp8) {
                     const int row = st * 32 + grp * 8 + (col >> 1);
-                    const i32x2 v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(LDS_PTR(
+                    op.v[st][c][0] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(LDS_PTR(
                         i32x2, cur + row * TL::kLatent + (cb ^ swizzle(row)) * 16 + (col & 1) * 8));
-                    vf = widen((uint32_t)v[0], (uint32_t)v[1]);
                 } else {
-                    union {
-                        s16x4 half[2];
-                        frag f;
-                    } u;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int row = st * 32 + grp * 8 + h * 4 + (col >> 2);
                         const int chunk = (cb * 2 + ((col >> 1) & 1)) ^ swizzle(row);
-                        u.half[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                            LDS_PTR(s16x4, cur + row * TL::kLatent + chunk * 16 + (col & 1) * 8));
+                        op.v[st][c][h] = __builtin_bit_cast(
+                            i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(
+                                       s16x4, cur + row * TL::kLatent + chunk * 16 + (col & 1) * 8)));
                     }
-                    vf = u.f;
                 }
+            }
+        }
+    };
+    auto values = [&](const Operands &op) __attribute__((always_inline)) {
+#pragma unroll
+        for (int st = 0; st < TILE / 32; ++st) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                frag vf;
+                if constexpr (kFp8)
+                    vf = widen((uint32_t)op.v[st][c][0][0], (uint32_t)op.v[st][c][0][1]);
+                else
+                    vf = __builtin_bit_cast(frag, __builtin_shufflevector(op.v[st][c][0],
+                                                                          op.v[st][c][kFp8 ? 0 : 1],
+                                                                          0, 1, 2, 3));
 #pragma unroll
                 for (int mb = 0; mb < MB; ++mb)
-                    o[c][mb] = M::mul(vf, pf[mb], o[c][mb]);
+                    o[c][mb] = M::mul(vf, op.p[st][mb], o[c][mb]);
             }
+        }
+    };
+    // In the region it ends, the products and the vector instructions beside
+    // them take turns.
+    auto interleave = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int n = 0; n < TILE / 32 * NC * MB; ++n) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // a product
+            __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);   // vector instructions
         }
     };
 
     if (t0 < t1) {
         // the entries, words and addresses of the first tiles
-        const int32_t *map = list.map;
-        const int e0 = entry(t0, map ? map[at(t0)] : 0);
-        const int e1 = entry(t0 + 1, map ? map[at(t0 + 1)] : 0);
-        int e = entry(t0 + 2, map ? map[at(t0 + 2)] : 0);
-        auto word = [&](int k) { return list.loc ? list.loc[k >= 0 ? k : 0] : 0u; };
-        if (map && lane < kRows)
-            sEntry[(t0 + 3) & 1][mine] = map[at(t0 + 3)];
-        if (lane < kRows)
-            sWord[t0 & 1][mine] = word(e);
+        const int e0 = entry(t0, *entry_at(t0)), e1 = entry(t0 + 1, *entry_at(t0 + 1));
+        int e = entry(t0 + 2, *entry_at(t0 + 2));
+        if (lane < kRows) {
+            sEntry[(t0 + 3) & 1][mine] = *entry_at(t0 + 3);
+            sWord[t0 & 1][mine] = *word_at(e);
+        }
         // the roles of the buffers and of the flags
         int prev = (BUFS - 1) * TL::kBytes, cur = 0, next = TL::kBytes;
         int f_prev = 2, f_cur = 0, f_next = 1;
-        prepare(e0, word(e0));
-        fetch(cur, t0);
-        prepare(e1, word(e1));
-        for (int t = t0; t < t1; ++t) {
-            // tile t has arrived, and (BUFS 3) the probabilities of tile t - 1
-            // are in LDS
-            barrier_all();
-            if (threadIdx.x == 0)
-                sExceeds[f_next] = 0;  // set after the next barrier, read before this one
-            if (BUFS == 3 && t > t0)
-                settle(prev, t - 1, f_prev);
-            // on their way from here: the rows of tile t + 1, the words of
-            // tile t + 3, the map's entries of tile t + 4
-            if (t + 1 < t1)
-                fetch(next, t + 1);
-            const int e3 = entry(t + 3, map ? sEntry[(t + 3) & 1][mine] : 0);
-            if (t + 3 < t1 && lane < kRows) {
-                if (list.loc)
-                    load_lds4(lds_offset(&sWord[(t + 3) & 1][wave * kRows]),
-                              list.loc + (e3 >= 0 ? e3 : 0));
-                if (map)
-                    load_lds4(lds_offset(&sEntry[t & 1][wave * kRows]), map + at(t + 4));
+        prepare(e0, *word_at(e0));
+        fetch(cur, t0, 0, 1);
+        prepare(e1, *word_at(e1));
+        // On their way from tile t's turn: the rows of tile t + 1, the words of
+        // tile t + 3, the map's entries of tile t + 4.  (Past the last tile they
+        // are rows of zeros and repeated words.)
+        int e3 = -1;
+        auto ahead = [&](int t) __attribute__((always_inline)) {
+            e3 = entry(t + 3, sEntry[(t + 3) & 1][mine]);
+            if (lane < kRows) {
+                load_lds4(lds_offset(&sWord[(t + 3) & 1][wave * kRows]), word_at(e3));
+                load_lds4(lds_offset(&sEntry[t & 1][wave * kRows]), entry_at(t + 4));
             }
-            scores(cur);
-            if (BUFS == 3) {
-                if (t > t0)
-                    values(prev, t - 1);
-                softmax(cur, t, f_cur);
-            } else {
-                softmax(cur, t, f_cur);
-                barrier_lds();
-                settle(cur, t, f_cur);
-                values(cur, t);
-            }
-            prepare(e, list.loc ? sWord[t & 1][mine] : 0);
+        };
+        constexpr int kParts = kBatches < 2 ? 1 : 2;  // batches that loads are started beside
+        auto turn = [&]() __attribute__((always_inline)) {
             e = e3;
             const int free = prev, f_free = f_prev;
             prev = cur, cur = next, next = BUFS == 3 ? free : prev;
             f_prev = f_cur, f_cur = f_next, f_next = f_free;
+        };
+        Keys key;
+        Operands op;
+        int t = t0;
+        uint32_t w2;
+        // A tile up to its probabilities; three buffers: beside the values of
+        // the tile before (but for the first).
+        auto step = [&](auto first) __attribute__((always_inline)) {
+            read_keys(key, cur, 0);
+            w2 = sWord[t & 1][mine];
+            __builtin_amdgcn_sched_barrier(0);
+            sExceeds[f_next] = 0;  // set after the next barrier, read before this one
+            ahead(t);
+            scores(key, cur, [&](int b) __attribute__((always_inline)) {
+                if (b < kParts)
+                    fetch(next, t + 1, b, kParts);
+                if (BUFS == 3 && !decltype(first)::value && b == kBatches - 1) {
+                    read_p(op, t - 1);
+                    read_v(op, prev);
+                }
+            });
+            if (BUFS == 3 && !decltype(first)::value)
+                values(op);
+            softmax(t, f_cur);
+            if (BUFS == 3) {
+                prepare(e, w2);
+                if (!decltype(first)::value)
+                    interleave();
+                turn();
+                ++t;
+                barrier_all();
+            } else {
+                read_v(op, cur);
+                barrier_lds();
+            }
+            return __builtin_amdgcn_readfirstlane(sExceeds[BUFS == 3 ? f_prev : f_cur]);
+        };
+        // Three buffers: after a step, t is the tile that has arrived, and tile
+        // t - 1 has its probabilities in LDS.  Two: tile t has them.
+        barrier_all();
+        step(std::true_type());
+        // The sums are scaled down (as they always are after the first tile)
+        // between runs of tiles that stay below their references, not on a
+        // branch inside the loop: there the compiler would keep two copies of
+        // them (512 registers did not hold 128 of them twice).
+        for (bool again = true; again;) {
+            settle(BUFS == 3 ? prev : cur, BUFS == 3 ? t - 1 : t);
+            again = false;
+            for (;;) {
+                count();
+                if (BUFS == 2) {
+                    read_p(op, t);
+                    values(op);
+                    prepare(e, w2);
+                    turn();
+                    ++t;
+                }
+                if (t >= t1)
+                    break;
+                if (BUFS == 2)
+                    barrier_all();
+                if (step(std::false_type())) {
+                    again = true;
+                    break;
+                }
+            }
         }
         if (BUFS == 3) {
-            barrier_lds();
-            settle(prev, t1 - 1, f_prev);
-            values(prev, t1 - 1);
+            read_p(op, t1 - 1);
+            read_v(op, prev);
+            values(op);
         }
     }
+    if (any_bad && a.c.status)
+        a.c.status[i] = KVR_E_RANGE;
 
     // the sums of the waves and lane groups that share a query row
-    l += __shfl_xor(l, 16);
-    l += __shfl_xor(l, 32);
-    barrier_lds();
-    if (grp == 0)
-        sMax[rg][hg * 16 + col] = l;
+    barrier_all();  // also: no load is on its way to LDS when the wave ends
+#pragma unroll
+    for (int mq = 0; mq < MQ; ++mq) {
+        l[mq] += __shfl_xor(l[mq], 16);
+        l[mq] += __shfl_xor(l[mq], 32);
+        if (grp == 0)
+            sMax[rg][(hg * MQ + mq) * 16 + col] = l[mq];
+    }
     barrier_lds();
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
@@ -703,14 +848,15 @@ __global__ __launch_bounds__(DV / 4) void join_kernel(AttendArgs a)
 template <int FMT, int DV, int DR>
 hipError_t launch_dims(const kvr_ctx *c, const AttendArgs &a, int block, dim3 grid, hipStream_t s)
 {
-    constexpr int kBufs16 = FMT == KVR_ROW_FP8 || DV == 256 ? 3 : 2;  // what LDS holds
+    constexpr int kBufs = FMT == KVR_ROW_FP8 || DV == 256 ? 3 : 2;  // what LDS holds
     if (block == 16)
-        return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 1, 64, kBufs16>, grid,
+        return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 1, 1, 64, kBufs>, grid,
                       dim3(256), 0, s, a);
     if (block == 32)
-        return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 2, 32, 3>, grid, dim3(256), 0,
-                      s, a);
-    return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 4, 32, 3>, grid, dim3(512), 0, s, a);
+        return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 2, 1, 64, kBufs>, grid,
+                      dim3(512), 0, s, a);
+    return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 4, 2, 32, 3>, grid, dim3(256), 0, s,
+                  a);
 }
 
 template <int FMT>
@@ -739,7 +885,7 @@ AttendPlan attend_plan(int32_t n, int32_t nq, int32_t heads, int32_t d_v, int32_
     const int32_t unit_rows = mapped ? heads : nq * heads;
     p.block = unit_rows <= 16 ? 16 : unit_rows <= 32 ? 32 : 64;
     p.groups = (unit_rows + p.block - 1) / p.block;
-    const int tile = p.block == 16 ? 64 : 32;
+    const int tile = p.block == 64 ? 32 : 64;
     const int64_t tiles = (rows + tile - 1) / tile;
     int64_t shares = kWorkgroups / (units * p.groups);
     shares = shares < tiles ? shares : tiles;
