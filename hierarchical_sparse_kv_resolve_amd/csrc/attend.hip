@@ -44,6 +44,7 @@
 namespace kvr {
 namespace {
 
+constexpr int kTile = 64;     // rows per tile
 constexpr float kSlack = 8.f; // log2 of the largest probability kept
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -337,17 +338,6 @@ __global__ __launch_bounds__(MB / MQ * TILE / 16 * 64) void attend_kernel(Attend
             }
         }
     };
-    if (a.wide)
-        load_q([](const E *p) { return *reinterpret_cast<const frag *>(p); });
-    else
-        load_q([](const E *p) {
-            frag f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                f[e] = p[e];
-            return f;
-        });
-
     // m: the reference of this lane's query row in each block; m_own, l: those
     // of the wave's blocks and this lane's shares of their sums
     float m[MB], m_own[MQ], l[MQ];
@@ -458,23 +448,23 @@ __global__ __launch_bounds__(MB / MQ * TILE / 16 * 64) void attend_kernel(Attend
             then(b);
             __builtin_amdgcn_sched_barrier(0);
             if constexpr (kFp8) {
-                f32x4 part[2][MQ] = {};
+                f32x4 part[MQ] = {};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const u32x4 v = key.latent[b & 1][h];
                     const frag k0 = widen(v[0], v[1]), k1 = widen(v[2], v[3]);
 #pragma unroll
                     for (int mq = 0; mq < MQ; ++mq)
-                        part[h][mq] = M::mul(k0, qf[mq][b * 4 + h * 2], part[h][mq]);
+                        part[mq] = M::mul(k0, qf[mq][b * 4 + h * 2], part[mq]);
 #pragma unroll
                     for (int mq = 0; mq < MQ; ++mq)
-                        part[h][mq] = M::mul(k1, qf[mq][b * 4 + h * 2 + 1], part[h][mq]);
+                        part[mq] = M::mul(k1, qf[mq][b * 4 + h * 2 + 1], part[mq]);
                 }
 #pragma unroll
                 for (int mq = 0; mq < MQ; ++mq)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        even[mq][k] = fmaf(part[0][mq][k] + part[1][mq][k], w[k][b], even[mq][k]);
+                        even[mq][k] = fmaf(part[mq][k], w[k][b], even[mq][k]);
             } else {
 #pragma unroll
                 for (int j = 0; j < kBatch; j += 2) {
@@ -672,6 +662,16 @@ __global__ __launch_bounds__(MB / MQ * TILE / 16 * 64) void attend_kernel(Attend
         int f_prev = 2, f_cur = 0, f_next = 1;
         prepare(e0, *word_at(e0));
         fetch(cur, t0, 0, 1);
+        if (a.wide)
+            load_q([](const E *p) { return *reinterpret_cast<const frag *>(p); });
+        else
+            load_q([](const E *p) {
+                frag f;
+    #pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    f[e] = p[e];
+                return f;
+            });
         prepare(e1, *word_at(e1));
         // On their way from tile t's turn: the rows of tile t + 1, the words of
         // tile t + 3, the map's entries of tile t + 4.  (Past the last tile they
@@ -684,7 +684,6 @@ __global__ __launch_bounds__(MB / MQ * TILE / 16 * 64) void attend_kernel(Attend
                 load_lds4(lds_offset(&sEntry[t & 1][wave * kRows]), entry_at(t + 4));
             }
         };
-        constexpr int kParts = kBatches < 2 ? 1 : 2;  // batches that loads are started beside
         auto turn = [&]() __attribute__((always_inline)) {
             e = e3;
             const int free = prev, f_free = f_prev;
@@ -704,8 +703,7 @@ __global__ __launch_bounds__(MB / MQ * TILE / 16 * 64) void attend_kernel(Attend
             sExceeds[f_next] = 0;  // set after the next barrier, read before this one
             ahead(t);
             scores(key, cur, [&](int b) __attribute__((always_inline)) {
-                if (b < kParts)
-                    fetch(next, t + 1, b, kParts);
+                fetch(next, t + 1, b, kBatches);
                 if (BUFS == 3 && !decltype(first)::value && b == kBatches - 1) {
                     read_p(op, t - 1);
                     read_v(op, prev);
@@ -813,35 +811,78 @@ __global__ __launch_bounds__(MB / MQ * TILE / 16 * 64) void attend_kernel(Attend
     }
 }
 
-// Joins the shares of each query row, in their order: a workgroup per row.
+// Joins the shares of each query row: a workgroup per row, its waves taking
+// every fourth share with several in flight, their sums added in wave order.
+// Bound by reading the shares (one after the other, a wave for all, took 19 us
+// for 32 shares of 512 rows).
+constexpr int kJoinWaves = 4;
 template <typename E, int DV>
-__global__ __launch_bounds__(DV / 4) void join_kernel(AttendArgs a)
+__global__ __launch_bounds__(kJoinWaves * 64) void join_kernel(AttendArgs a)
 {
+    constexpr int N = DV / 64;   // columns of a lane
+    constexpr int kFlight = 4;   // shares in flight
+    typedef float vec __attribute__((ext_vector_type(N)));
+    __shared__ float sL[kJoinWaves];
+    __shared__ vec sO[kJoinWaves][64];
+    const int lane = lane_id(), wave = wave_id();
     const int64_t at = blockIdx.x;
     const int unit = (int)(at / a.unit_rows), x = (int)(at % a.unit_rows);
     const int64_t first = (int64_t)unit * a.shares * a.unit_rows + x;
+    auto stat = [&](int s) {
+        return *reinterpret_cast<const float2 *>(a.stat + 2 * (first + (int64_t)s * a.unit_rows));
+    };
     float m = -__builtin_inff();
-    for (int s = 0; s < a.shares; ++s)
-        m = fmaxf(m, a.stat[2 * (first + (int64_t)s * a.unit_rows)]);
+    for (int s = lane; s < a.shares; s += 64)
+        m = fmaxf(m, stat(s).x);
+#pragma unroll
+    for (int k = 32; k >= 1; k >>= 1)
+        m = fmaxf(m, __shfl_xor(m, k));
     float l = 0.f;
-    f32x4 o{0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < a.shares; ++s) {
-        const int64_t ps = first + (int64_t)s * a.unit_rows;
-        const float2 st = *reinterpret_cast<const float2 *>(a.stat + 2 * ps);
-        if (st.x == -__builtin_inff() && st.y == 0.f)
-            continue;
-        const float w = st.x == -__builtin_inff() ? 1.f : exp2_hw(st.x - m);
-        l += w * st.y;
-        o += w * *reinterpret_cast<const f32x4 *>(a.partial + ps * DV + threadIdx.x * 4);
+    vec o = {};
+    for (int s0 = wave; s0 < a.shares; s0 += kJoinWaves * kFlight) {
+        vec part[kFlight];
+        float w[kFlight], ls[kFlight];
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) {
+            const int s = s0 + f * kJoinWaves;
+            w[f] = 0.f;
+            ls[f] = 0.f;
+            part[f] = vec{};
+            if (s >= a.shares)
+                continue;
+            const float2 st = stat(s);
+            if (st.x == -__builtin_inff() && st.y == 0.f)
+                continue;  // an empty share: its sums were not written
+            w[f] = st.x == -__builtin_inff() ? 1.f : exp2_hw(st.x - m);
+            ls[f] = st.y;
+            part[f] = *reinterpret_cast<const vec *>(
+                a.partial + (first + (int64_t)s * a.unit_rows) * DV + lane * N);
+        }
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) {
+            l += w[f] * ls[f];
+            o += w[f] * part[f];
+        }
+    }
+    sO[wave][lane] = o;
+    if (lane == 0)
+        sL[wave] = l;
+    __syncthreads();
+    if (wave != 0)
+        return;
+#pragma unroll
+    for (int k = 1; k < kJoinWaves; ++k) {
+        l += sL[k];
+        o += sO[k][lane];
     }
     const float inv = m == -__builtin_inff() && l == 0.f ? 0.f : 1.f / l;
-    typedef E e4 __attribute__((ext_vector_type(4)));
-    e4 v;
+    typedef E out __attribute__((ext_vector_type(N)));
+    out v;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < N; ++k)
         v[k] = (E)(o[k] * inv);
-    *reinterpret_cast<e4 *>(static_cast<E *>(a.c.out) + at * DV + threadIdx.x * 4) = v;
-    if (threadIdx.x == 0 && a.c.lse)
+    *reinterpret_cast<out *>(static_cast<E *>(a.c.out) + at * DV + lane * N) = v;
+    if (lane == 0 && a.c.lse)
         a.c.lse[at] = 0.69314718055994530942f * (m + __log2f(l));
 }
 
@@ -852,11 +893,8 @@ hipError_t launch_dims(const kvr_ctx *c, const AttendArgs &a, int block, dim3 gr
     if (block == 16)
         return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 1, 1, 64, kBufs>, grid,
                       dim3(256), 0, s, a);
-    if (block == 32)
-        return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 2, 1, 64, kBufs>, grid,
-                      dim3(512), 0, s, a);
-    return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 4, 2, 32, 3>, grid, dim3(256), 0, s,
-                  a);
+    return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 2, 1, 64, kBufs>, grid, dim3(512), 0,
+                  s, a);
 }
 
 template <int FMT>
@@ -883,10 +921,9 @@ AttendPlan attend_plan(int32_t n, int32_t nq, int32_t heads, int32_t d_v, int32_
     AttendPlan p{};
     const int64_t units = mapped ? (int64_t)n * nq : n;
     const int32_t unit_rows = mapped ? heads : nq * heads;
-    p.block = unit_rows <= 16 ? 16 : unit_rows <= 32 ? 32 : 64;
+    p.block = unit_rows <= 16 ? 16 : 32;
     p.groups = (unit_rows + p.block - 1) / p.block;
-    const int tile = p.block == 64 ? 32 : 64;
-    const int64_t tiles = (rows + tile - 1) / tile;
+    const int64_t tiles = (rows + kTile - 1) / kTile;
     int64_t shares = kWorkgroups / (units * p.groups);
     shares = shares < tiles ? shares : tiles;
     p.shares = (int32_t)(shares < 1 ? 1 : shares);
@@ -898,7 +935,7 @@ AttendPlan attend_plan(int32_t n, int32_t nq, int32_t heads, int32_t d_v, int32_
 // rows times tiles, and at most a block of 64 for each workgroup.
 int64_t attend_workspace_bound(int32_t n, int32_t nq, int32_t heads, int32_t d_v, int32_t rows)
 {
-    const int64_t all = (int64_t)n * nq * heads, tiles = (rows + 31) / 32;
+    const int64_t all = (int64_t)n * nq * heads, tiles = (rows + kTile - 1) / kTile;
     const int64_t most = all * tiles;
     if (tiles < 2)
         return 0;
@@ -930,11 +967,15 @@ hipError_t launch_attend(const kvr_ctx *c, const kvr_attend_call &call, const At
     const dim3 rows((unsigned)((int64_t)a.units * a.unit_rows));
     if (call.format == KVR_ROW_F16)
         return call.d_v == 512
-                   ? launch(c, KVR_KERNEL_ATTEND, join_kernel<_Float16, 512>, rows, dim3(128), 0, s, a)
-                   : launch(c, KVR_KERNEL_ATTEND, join_kernel<_Float16, 256>, rows, dim3(64), 0, s, a);
+                   ? launch(c, KVR_KERNEL_ATTEND, join_kernel<_Float16, 512>, rows, dim3(kJoinWaves * 64), 0, s,
+                            a)
+                   : launch(c, KVR_KERNEL_ATTEND, join_kernel<_Float16, 256>, rows, dim3(kJoinWaves * 64), 0, s,
+                            a);
     return call.d_v == 512
-               ? launch(c, KVR_KERNEL_ATTEND, join_kernel<__bf16, 512>, rows, dim3(128), 0, s, a)
-               : launch(c, KVR_KERNEL_ATTEND, join_kernel<__bf16, 256>, rows, dim3(64), 0, s, a);
+               ? launch(c, KVR_KERNEL_ATTEND, join_kernel<__bf16, 512>, rows, dim3(kJoinWaves * 64), 0, s,
+                            a)
+               : launch(c, KVR_KERNEL_ATTEND, join_kernel<__bf16, 256>, rows, dim3(kJoinWaves * 64), 0, s,
+                            a);
 }
 
 }  // namespace kvr
