@@ -248,6 +248,9 @@ def _pinned(x, name: str, nbytes: int = 0) -> int | None:
 def _stream(stream) -> int | None:
     if stream is None:
         import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:  # without building a Stream object for each call
+            return raw(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -260,45 +263,56 @@ def _check(rc: int):
     return rc
 
 
-def _typed(x, name: str, dtypes, shape=None):
-    """A strided device tensor of one of the dtypes (names) whose last
-    dimension is contiguous, on the current device."""
+def _here() -> int:
+    """The current device (which the library requires to be the context's)."""
     import torch
-    if not isinstance(x, torch.Tensor):
-        raise TypeError(f"{name}: expected a GPU tensor, got {type(x)}")
-    if not x.is_cuda:
-        raise TypeError(f"{name}: expected a GPU tensor, got one on {x.device}")
-    if str(x.dtype)[6:] not in dtypes:
+    return torch.cuda.current_device()
+
+
+def _typed(x, name: str, dtypes, here: int | None = None, shape=None):
+    """A strided tensor on the current device (`here`), of one of the dtypes
+    (names), whose last dimension is contiguous; its dtype's name."""
+    if not getattr(x, "is_cuda", False):
+        what = f"one on {x.device}" if hasattr(x, "is_cuda") else type(x)
+        raise TypeError(f"{name}: expected a GPU tensor, got {what}")
+    kind = _DTYPE_NAMES.get(x.dtype)
+    if kind is None:
+        kind = _DTYPE_NAMES[x.dtype] = str(x.dtype)[6:]
+    if kind not in dtypes:
         raise TypeError(f"{name}: expected {' or '.join(dtypes)}, got {x.dtype}")
-    if shape is not None and tuple(x.shape) != tuple(shape):
+    if shape is not None and x.shape != shape:
         raise ValueError(f"{name}: shape {tuple(x.shape)}, the call needs {tuple(shape)}")
-    if x.numel() and x.shape[-1] > 1 and x.stride(-1) != 1:
+    if not x.is_contiguous() and x.numel() and x.shape[-1] > 1 and x.stride(-1) != 1:
         raise ValueError(f"{name}: the last dimension is not contiguous")
-    _same_device(x, name)
-    return x
+    _same_device(x, name, here)
+    return kind
 
 
-def _same_device(x, name: str):
-    """A tensor of another device than the current one (which the library
-    requires to be the context's) is refused; addresses pass."""
+_DTYPE_NAMES: dict = {}
+
+
+def _same_device(x, name: str, here: int | None = None):
+    """A tensor of another device than the current one is refused; addresses
+    pass."""
     if getattr(x, "is_cuda", False):
-        import torch
-        if x.device.index != torch.cuda.current_device():
-            raise ValueError(f"{name}: on {x.device}, the current device is "
-                             f"cuda:{torch.cuda.current_device()}")
+        here = _here() if here is None else here
+        if x.get_device() != here:
+            raise ValueError(f"{name}: on {x.device}, the current device is cuda:{here}")
     return x
 
 
-def _dev_here(x, name: str, nbytes: int = 0) -> int | None:
-    return _dev(_same_device(x, name), name, nbytes)
+def _dev_here(x, name: str, nbytes: int = 0, here: int | None = None) -> int | None:
+    if x is None or isinstance(x, int):
+        return x
+    return _dev(_same_device(x, name, here), name, nbytes)
 
 
-def _workspace(x):
+def _workspace(x, here: int | None = None):
     """(address, bytes) of a workspace tensor; an address is taken to hold what
     the call needs."""
     if x is None or isinstance(x, int):
         return x, (1 << 62 if x else 0)
-    return _dev_here(x, "workspace"), x.numel() * x.element_size()
+    return _dev_here(x, "workspace", 0, here), x.numel() * x.element_size()
 
 
 def row_layout(fmt: str, d_v: int, d_rope: int) -> int:
@@ -580,19 +594,19 @@ class Context:
         fp32, both of one type; rows may be strided slices), normalised where a
         float32 weight [d_v] is given, into rows (n * row_bytes bytes, on the
         device or pinned)."""
-        types = tuple(_VALUE_TYPES)
-        _typed(latent, "latent", types, (n, d_v))
-        kind = str(latent.dtype)[6:]
+        here = _here()
+        kind = _typed(latent, "latent", _VALUE_TYPES, here, (n, d_v))
         if d_rope:
-            _typed(rope, "rope", (kind,), (n, d_rope))
+            _typed(rope, "rope", (kind,), here, (n, d_rope))
         if weight is not None:
-            _typed(weight, "weight", ("float32",), (d_v,))
+            _typed(weight, "weight", ("float32",), here, (d_v,))
         need = max(n, 0) * self.cfg.row_bytes
         on_host = hasattr(rows, "is_cuda") and not rows.is_cuda
         call = PackCall(_row_format(fmt), _VALUE_TYPES[kind], n, d_v, d_rope, eps,
                         latent.data_ptr(), rope.data_ptr() if d_rope else None,
                         None if weight is None else weight.data_ptr(),
-                        _pinned(rows, "rows", need) if on_host else _dev_here(rows, "rows", need),
+                        _pinned(rows, "rows", need) if on_host else
+                        _dev_here(rows, "rows", need, here),
                         latent.stride(0), rope.stride(0) if d_rope else 0)
         _check(lib().kvr_pack_rows(self.handle, ctypes.byref(call), _stream(stream)))
 
@@ -610,34 +624,32 @@ class Context:
         names in `layer` (or over the gathered rows), into out [n, nq, heads,
         d_v] and lse [n, nq, heads]; with map_ [n, nq, k] query a of entry i
         attends to the entries map_[i, a] only.  See kvr_attend_rows."""
-        kind = (_ROW_TYPES.get(fmt, ""),)
-        code = _row_format(fmt)
+        code, kind, here = _row_format(fmt), (_ROW_TYPES[fmt],), _here()
         if getattr(q, "ndim", 4) != 4:
             raise ValueError(f"q: {q.ndim} dimensions, the call needs [n, nq, heads, d_v + d_rope]")
-        _typed(q, "q", kind)
-        nq, heads = int(q.shape[1]), int(q.shape[2])
-        _typed(q, "q", kind, (n, nq, heads, d_v + d_rope))
-        _typed(out, "out", kind, (n, nq, heads, d_v))
+        nq, heads = (int(q.shape[1]), int(q.shape[2])) if hasattr(q, "shape") else (1, 1)
+        _typed(q, "q", kind, here, (n, nq, heads, d_v + d_rope))
+        _typed(out, "out", kind, here, (n, nq, heads, d_v))
         if lse is not None:
-            _typed(lse, "lse", ("float32",), (n, nq, heads))
+            _typed(lse, "lse", ("float32",), here, (n, nq, heads))
         k = 0
         if map_ is not None:
             if getattr(map_, "ndim", 3) != 3:
                 raise ValueError(f"map: {map_.ndim} dimensions, the call needs [n, nq, k]")
-            _typed(map_, "map", ("int32",))
-            k = int(map_.shape[2])
-            _typed(map_, "map", ("int32",), (n, nq, k))
+            k = int(map_.shape[2]) if hasattr(map_, "shape") else 0
+            _typed(map_, "map", ("int32",), here, (n, nq, k))
         if count is not None and not isinstance(count, int):
-            _typed(count, "count", ("int32",))
+            _typed(count, "count", ("int32",), here)
         m = max(n, 0) * max(stride, 0)
-        ws, ws_bytes = _workspace(workspace)
+        ws, ws_bytes = _workspace(workspace, here)
+        strides = q.stride()
         call = AttendCall(layer, code, n, nq, heads, d_v, d_rope, stride, k, scale,
-                          _dev_here(req_ids, "req_ids", 4 * n), _dev_here(loc, "loc", 4 * m),
-                          _dev_here(rows, "rows", m * self.cfg.row_bytes),
-                          _dev_here(count, "count", 4 * n), _dev_here(map_, "map"),
-                          q.data_ptr(), q.stride(0), q.stride(1), q.stride(2),
-                          _dev_here(out, "out"), _dev_here(lse, "lse"),
-                          _dev_here(status, "status", 4 * n), ws, ws_bytes)
+                          _dev_here(req_ids, "req_ids", 4 * n, here),
+                          _dev_here(loc, "loc", 4 * m, here),
+                          _dev_here(rows, "rows", m * self.cfg.row_bytes, here),
+                          _dev_here(count, "count", 4 * n, here), _dev(map_, "map"),
+                          q.data_ptr(), strides[0], strides[1], strides[2], _dev(out, "out"),
+                          _dev(lse, "lse"), _dev_here(status, "status", 4 * n, here), ws, ws_bytes)
         _check(lib().kvr_attend_rows(self.handle, ctypes.byref(call), _stream(stream)))
 
     # ------------------------------------------- pages shared by requests
