@@ -475,7 +475,8 @@ typedef struct kvr_pack_call {
 /* Rows of n new (or imported) tokens in the cache's format, for
  * kvr_append_rows, a host store or the optional pool.  x is rounded once, to
  * nearest, to the row's 16-bit type; in fp8 rows each group of 128 values has
- * scale = max|x| / 448 (1 for a group of zeros) and codes e4m3(x / scale).
+ * scale = max|x| / 448 (1 for a group of zeros) and codes e4m3(x / scale)
+ * (the quotient to 32-bit accuracy).
  * The rope part is rounded to 16 bits as it is.  A NaN or an infinity makes
  * its own scale group (its own value, in 16-bit rows; the whole latent when
  * it is normalised) NaN or infinite, no other.  One kernel; n = 0 is a no-op. */
