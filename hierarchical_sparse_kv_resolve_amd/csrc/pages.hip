@@ -312,10 +312,12 @@ __global__ __launch_bounds__(NT) void copy_commit_kernel(CopyArgs a, int32_t n)
 //
 // Both need, for each page, the number of live pages below it.  The pool is
 // cut into at most kPoolBlocks blocks; a first launch counts each block's live
-// pages, and every block of the next adds up the counts before its own.
+// pages, and every block of the next adds up the counts before its own.  A
+// pool of one block (up to 2048 pages) needs no first launch.
 
 constexpr int kPoolBlocks = 1024;
-constexpr int kPoolBlockMin = 1024;  // pages per block, at least
+constexpr int kPoolChunk = 2048;  // pages a workgroup looks at in one step
+constexpr int kPoolItems = kPoolChunk / NT;
 
 struct PoolArgs {
     int64_t pages;
@@ -356,65 +358,93 @@ __global__ __launch_bounds__(NT) void count_live_kernel(PoolArgs a)
 template <bool PLAN>
 __global__ __launch_bounds__(NT) void rank_pages_kernel(PoolArgs a)
 {
-    __shared__ int sSum[2], sWave[NT / 64], sMoved;
+    __shared__ int sSum[2], sWave[kPoolItems][NT / 64], sMoved;
     if (threadIdx.x < 2)
         sSum[threadIdx.x] = 0;
     if (threadIdx.x == 0)
         sMoved = 0;
-    __syncthreads();
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t p0 = (int64_t)blockIdx.x * a.per_block;
+    const int64_t p1 = p0 + a.per_block < a.pages ? p0 + a.per_block : a.pages;
+    bool is[kPoolItems];
+    auto load = [&](int64_t c) {
+#pragma unroll
+        for (int k = 0; k < kPoolItems; ++k) {
+            const int64_t p = c + k * NT + threadIdx.x;
+            is[k] = p < p1 && a.refs[p] > 0;
+        }
+    };
+    load(p0);
     int before = 0, all = 0;
-    for (int b = threadIdx.x; b < a.blocks; b += NT) {
-        const int v = a.block_live[b];
-        all += v;
-        before += b < (int)blockIdx.x ? v : 0;
+    if (a.blocks == 1) {
+#pragma unroll
+        for (int k = 0; k < kPoolItems; ++k)
+            all += is[k];
+    } else {
+        for (int b = threadIdx.x; b < a.blocks; b += NT) {
+            const int v = a.block_live[b];
+            all += v;
+            before += b < (int)blockIdx.x ? v : 0;
+        }
     }
+    __syncthreads();
     atomicAdd(&sSum[0], before);
     atomicAdd(&sSum[1], all);
     __syncthreads();
     int base = sSum[0];
     const int live = sSum[1];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t p0 = (int64_t)blockIdx.x * a.per_block;
-    const int64_t p1 = p0 + a.per_block < a.pages ? p0 + a.per_block : a.pages;
     int moved = 0;
-    for (int64_t c = p0; c < p1; c += NT) {
-        const int64_t p = c + threadIdx.x;
-        const bool is = p < p1 && a.refs[p] > 0;
-        const uint64_t mask = __ballot(is);
-        if (lane == 0)
-            sWave[wave] = __popcll(mask);
+    for (int64_t c = p0; c < p1; c += kPoolChunk) {
+        if (c > p0)
+            load(c);
+        uint64_t mask[kPoolItems];
+#pragma unroll
+        for (int k = 0; k < kPoolItems; ++k) {
+            mask[k] = __ballot(is[k]);
+            if (lane == 0)
+                sWave[k][wave] = __popcll(mask[k]);
+        }
         __syncthreads();
-        int below = base + __popcll(mask & ((1ull << lane) - 1ull)), sum = 0;
-        for (int w = 0; w < NT / 64; ++w) {
-            below += w < wave ? sWave[w] : 0;
-            sum += sWave[w];
-        }
-        base += sum;
-        __syncthreads();  // sWave is rewritten by the next chunk
-        if (p >= p1)
-            continue;
-        if (!PLAN) {
-            if (!is)
-                a.free_list[p - below] = (int32_t)p;
-            continue;
-        }
-        if (p >= live) {
-            const int rank = live - 1 - below;
-            const bool goes = is && rank < a.max_moves;
-            a.rank[p] = goes ? rank : -1;
-            if (goes) {
-                a.moves[2 * (int64_t)rank] = (int32_t)p;
-                ++moved;
+#pragma unroll
+        for (int k = 0; k < kPoolItems; ++k) {
+            int below = base + __popcll(mask[k] & ((1ull << lane) - 1ull));
+            for (int w = 0; w < NT / 64; ++w) {
+                below += w < wave ? sWave[k][w] : 0;
+                base += sWave[k][w];
             }
-        } else if (!is && p - below < a.max_moves) {
-            a.moves[2 * (p - below) + 1] = (int32_t)p;
+            const int64_t p = c + k * NT + threadIdx.x;
+            if (p >= p1)
+                continue;
+            if (!PLAN) {
+                if (!is[k])
+                    a.free_list[p - below] = (int32_t)p;
+                continue;
+            }
+            if (p >= live) {
+                const int rank = live - 1 - below;
+                const bool goes = is[k] && rank < a.max_moves;
+                a.rank[p] = goes ? rank : -1;
+                if (goes) {
+                    a.moves[2 * (int64_t)rank] = (int32_t)p;
+                    ++moved;
+                }
+            } else if (!is[k] && p - below < a.max_moves) {
+                a.moves[2 * (p - below) + 1] = (int32_t)p;
+            }
         }
+        __syncthreads();  // sWave is rewritten by the next chunk
     }
     if (PLAN) {
         atomicAdd(&sMoved, moved);
         __syncthreads();
-        if (threadIdx.x == 0 && sMoved)
-            atomicAdd(a.move_count, sMoved);
+        if (threadIdx.x == 0) {
+            if (a.blocks == 1) {
+                *a.move_count = sMoved;
+                a.block_live[0] = live;
+            } else if (sMoved) {
+                atomicAdd(a.move_count, sMoved);
+            }
+        }
     } else if (blockIdx.x == 0 && threadIdx.x == 0) {
         *a.free_count = (int32_t)(a.pages - live);
     }
@@ -476,13 +506,20 @@ PoolArgs pool_args(const kvr_ctx *c, void *workspace)
 {
     PoolArgs a{};
     a.pages = pool_pages(c);
-    int64_t per = (a.pages + kPoolBlocks - 1) / kPoolBlocks;
-    a.per_block = (int32_t)(per < kPoolBlockMin ? kPoolBlockMin : per);
+    const int64_t per = (a.pages + kPoolBlocks - 1) / kPoolBlocks;
+    a.per_block = (int32_t)((per < 1 ? 1 : (per + kPoolChunk - 1) / kPoolChunk) * kPoolChunk);
     a.blocks = (int32_t)((a.pages + a.per_block - 1) / a.per_block);
     a.refs = c->page_refs;
     a.block_live = static_cast<int32_t *>(workspace);
     a.rank = a.block_live + kPoolBlocks;
     return a;
+}
+
+hipError_t launch_count_live(const kvr_ctx *c, const PoolArgs &a, hipStream_t s)
+{
+    if (a.blocks == 1)
+        return hipSuccess;
+    return launch(c, KVR_KERNEL_PAGES, count_live_kernel, dim3(a.blocks), dim3(NT), 0, s, a);
 }
 
 unsigned blocks_for(int64_t items, int64_t most)
@@ -567,7 +604,7 @@ hipError_t launch_list_free(const kvr_ctx *c, int32_t *free_list, int32_t *free_
     if (a.pages == 0)
         return launch(c, KVR_KERNEL_PAGES, zero_kernel, dim3(1), dim3(NT), 0, s, free_count,
                       (int64_t)1);
-    hipError_t e = launch(c, KVR_KERNEL_PAGES, count_live_kernel, dim3(a.blocks), dim3(NT), 0, s, a);
+    hipError_t e = launch_count_live(c, a, s);
     if (e != hipSuccess)
         return e;
     return launch(c, KVR_KERNEL_PAGES, rank_pages_kernel<false>, dim3(a.blocks), dim3(NT), 0, s, a);
@@ -583,7 +620,7 @@ hipError_t launch_compact(const kvr_ctx *c, int32_t max_moves, int32_t *moves, i
     if (a.pages == 0)
         return launch(c, KVR_KERNEL_PAGES, zero_kernel, dim3(1), dim3(NT), 0, s, move_count,
                       (int64_t)1);
-    hipError_t e = launch(c, KVR_KERNEL_PAGES, count_live_kernel, dim3(a.blocks), dim3(NT), 0, s, a);
+    hipError_t e = launch_count_live(c, a, s);
     if (e != hipSuccess)
         return e;
     e = launch(c, KVR_KERNEL_PAGES, rank_pages_kernel<true>, dim3(a.blocks), dim3(NT), 0, s, a);
