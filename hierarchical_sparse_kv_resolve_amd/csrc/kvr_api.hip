@@ -930,15 +930,16 @@ int kvr_pack_rows(kvr_ctx *ctx, const kvr_pack_call *call, void *stream)
     return err == hipSuccess ? ok() : hip_fail(err, "pack launch");
 }
 
-// Sizes of an attention call that its kernels' 32-bit indexing covers.
+// Sizes of an attention call that its kernels' 32-bit indexing and the grid
+// limit cover.
 static int check_attend_sizes(int32_t n, int32_t nq, int32_t heads, int32_t rows)
 {
     if (n < 0 || nq < 1 || heads < 1 || rows < 0)
         return fail(KVR_E_ARG, "n and rows must be >= 0, nq and heads >= 1");
     if (nq > 4096 || heads > 4096 || rows > (1 << 24))
         return fail(KVR_E_ARG, "at most 4096 queries, 4096 heads and 2^24 rows per query");
-    if ((int64_t)n * nq * heads > (1 << 24))
-        return fail(KVR_E_ARG, "n * nq * heads must be at most 2^24");
+    if ((int64_t)n * nq * heads > (1 << 22))
+        return fail(KVR_E_ARG, "n * nq * heads must be at most 2^22");
     return KVR_OK;
 }
 

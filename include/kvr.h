@@ -503,8 +503,9 @@ int kvr_pack_rows(kvr_ctx *ctx, const kvr_pack_call *call, void *stream);
  *   out (device) [n][nq][heads][d_v] contiguous, of q's type, aligned to 16
  *     bytes; lse (device) float [n][nq][heads] or NULL
  *   status (device) int32 [n] or NULL: KVR_E_RANGE for an entry with a
- *     location outside its place (which is left out), KVR_E_ARG for a request
- *     id out of range (which attends to nothing), otherwise not written
+ *     location outside its place (which is left out; rows NULL only),
+ *     KVR_E_ARG for a request id out of range (which attends to nothing),
+ *     otherwise not written
  *   workspace (device), aligned to 16 bytes: at least
  *     kvr_attend_workspace(n, nq, heads, d_v, rows per query) bytes; written
  *     by the call, so calls that may run at once (two streams, two graphs)
@@ -547,8 +548,10 @@ typedef struct kvr_attend_call {
  * e4m3 code is exact in bf16), sums, maxima and exponentials in 32 bits;
  * probabilities are rounded to 16 bits before their product with the values.
  * A selection may be cut into shares that are attended to apart and joined in
- * a fixed order: results do not vary from run to run.  One kernel, or two
- * with shares. */
+ * a fixed order: results do not vary from run to run (another n, nq or heads
+ * may cut it otherwise and round differently).  One kernel, or two with
+ * shares.  Limits: nq and heads at most 4096, n * nq * heads at most 2^22,
+ * stride and k at most 2^24. */
 int kvr_attend_rows(kvr_ctx *ctx, const kvr_attend_call *call, void *stream);
 
 /* Workspace bytes of kvr_attend_rows for calls of up to n entries, nq
@@ -568,16 +571,20 @@ int64_t kvr_attend_workspace(int32_t n, int32_t nq, int32_t heads, int32_t d_v, 
  *   releases (freed_phys[i] still names the page entry i let go of, which is
  *   free only once its count is 0) and kvr_restore_pages refuses a physical
  *   page whose count is not 0 with KVR_E_STATE and sets the count of each page
- *   it fills to 1.  kvr_residency_* expects each physical page in one map
- *   entry: give entries pages of their own (kvr_copy_pages) before a map is
- *   handed to it.
+ *   it fills to 1.  kvr_residency_* keeps lists of its own, which do not
+ *   follow the calls below, and expects each physical page in one map entry:
+ *   give entries pages of their own (kvr_copy_pages) before a map is handed to
+ *   it.
  * kvr_count_page_refs: set the counts from page_map.
  *
  * The calls below need the counts bound when pool_pages > 0.
  *
  * kvr_release_requests: each listed request gives up its rows: the counts of
  *   its pages go down, page_map becomes -1, host_valid 0, tags -1, stamps 0,
- *   clock 0 and L 0.  Payload stays as it is.
+ *   clock 0 and L 0, so that every row of it is out of range until it becomes
+ *   the copy of another request or is set up again.  Payload stays as it is.
+ *   status (device) int32 [n] or NULL: KVR_E_ARG (nothing changes) for an id
+ *   out of range or one that an earlier entry names.
  * kvr_fork_requests: request dst_ids[i] becomes a copy of src_ids[i]: L,
  *   clock, tags and stamps; the ready pages, shared; and of every payload layer
  *   the tail ring, the hot slots with a tag, the host rows of imported pages

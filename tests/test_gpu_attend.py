@@ -336,6 +336,44 @@ def test_same_result_twice_and_on_another_stream():
     assert torch.equal(a[1], c[1]) and torch.equal(a[2], c[2])
 
 
+def test_two_calls_at_once():
+    """Calls on two streams with workspaces of their own."""
+    src = Source(16, 6, "fp8", 512, 64, n_layers=2)
+    n, heads, stride = 6, 20, 900
+    loc = [to_dev(src.words(n, stride, None, 0.1)) for _ in range(2)]
+    q = [torch.randn(n, 1, heads, 576, device="cuda").bfloat16() for _ in range(2)]
+    need = src.ctx.attend_workspace(n, 1, heads, 512, stride)
+    outs = [[torch.zeros(n, 1, heads, 512, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+            for _ in range(2)]
+    ws = [torch.zeros(need, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+
+    def call(i, out, stream=None):
+        src.ctx.attend_rows(i, n, None, q[i], out, fmt="fp8", d_v=512, d_rope=64, scale=0.07,
+                            stride=stride, loc=loc[i], workspace=ws[i], stream=stream)
+
+    for i in range(2):
+        call(i, outs[0][i])
+        torch.cuda.synchronize()
+    for _ in range(5):
+        for i in range(2):
+            call(i, outs[1][i], streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(outs[0][i], outs[1][i])
+        assert not torch.equal(outs[0][0], outs[0][1])
+
+
+def test_every_share_count():
+    """Selections of one to many tiles, so that every number of shares occurs,
+    with counts that leave the last shares empty."""
+    src = Source(17, 3, "bf16", 512, 64, B=2000)
+    for stride in (64, 65, 128, 300, 640, 1999):
+        for count in (None, [stride, 64, 1]):
+            check(src, *run(src, 3, 1, 16, stride, count=count)[:5])
+
+
 def test_captured_and_replayed():
     """One captured call, replayed with new contents and eager work between."""
     src = Source(13, 3, "fp8", 512, 64)
