@@ -13,7 +13,7 @@
 // and the sums are scaled down.
 //
 // A workgroup of NW waves owns MB blocks of 16 query rows and a share of the
-// selection, which it walks in tiles of TILE rows, kept in LDS.  Tiles arrive
+// selection, which it walks in tiles of kTile (64) rows, kept in LDS.  Tiles arrive
 // by 16-byte direct loads to LDS, addresses from the location words, which are
 // read two tiles earlier still.
 //   scores   a wave computes 16 of the tile's rows for one block of query rows
@@ -37,6 +37,29 @@
 // columns' group before they are rounded to bf16.
 //
 // Rows left out are read from a row of zeros and their p is 0.
+//
+// What bounds it (one MI355X; the kernel, then the join of the shares):
+// with few query rows a selection, reading the rows,
+//   64 requests x 16 heads x 2048 fp8 rows of 656 bytes     25 + 4 us, 3.4 TB/s
+//   32 requests x 4 queries x 16 heads x 2048 bf16 rows of a union of 3277,
+//   each query its own rows                        51 + 6 us, 5.9 TB/s read
+//   (from HBM only the union once, 121 MB);
+// with many, the vector, matrix and LDS instructions of two waves a SIMD,
+//   64 requests x 128 heads x 2048 fp8 rows        75 us, 480 TFLOP/s
+//   (0.40 of what a large bf16 product reaches): a tile takes about 5800
+//   cycles, of which a SIMD's vector instructions (exponentials, widened
+//   codes, addresses) are 2540, its matrix instructions 1088 and the LDS' reads
+//   2100, and two waves in order overlap them only in part;
+// with few rows in all, latency: one request x 16 heads x 256 rows takes
+//   10 + 4 us (an empty kernel 4), four dependent loads (lists, words, rows)
+//   and one tile.
+//
+// Split, block and buffers (128 heads as above): scores split over the waves
+// by dimension, two barriers a tile 89 us; 64 query rows and 8 waves 77 and a
+// join of 9; 16 waves of 128 registers 110; 4 waves of 512 registers 92; two
+// workgroups a compute unit 90; 32 query rows, 8 waves and tiles of 64 rows 75
+// (taken).  Tiles of 32 rows took longer in blocks of 16 query rows too (the
+// 16-head cases above 28 instead of 26 and 59 instead of 53 us).
 #include "block.h"
 #include "kvr_internal.h"
 #include "rowformat.h"
@@ -96,6 +119,7 @@ __device__ __forceinline__ void load_lds4(uint32_t lds, const void *src)
 
 // What a row that is left out is read from (the longest row is 1152 bytes).
 __device__ __attribute__((aligned(16))) uint8_t zero_row[1152];
+__device__ int32_t zero_words[4];
 
 struct AttendArgs {
     Shape sh;
@@ -185,16 +209,16 @@ __device__ __forceinline__ const uint8_t *row_address(const Shape &sh, const Row
 }
 
 // A tile in LDS: latents, rope parts and (8-bit rows) scales, each part
-// [TILE rows][its bytes].
-template <int FMT, int DV, int DR, int TILE>
+// [kTile rows][its bytes].
+template <int FMT, int DV, int DR>
 struct Tile {
     static constexpr bool kFp8 = FMT == KVR_ROW_FP8;
     static constexpr int kLatent = kFp8 ? DV : 2 * DV;  // bytes of a row's parts
     static constexpr int kRope = 2 * DR;
     static constexpr int kScales = kFp8 ? scale_bytes(DV) : 0;
-    static constexpr int kRopeAt = TILE * kLatent;
-    static constexpr int kScalesAt = kRopeAt + TILE * kRope;
-    static constexpr int kBytes = kScalesAt + TILE * kScales;
+    static constexpr int kRopeAt = kTile * kLatent;
+    static constexpr int kScalesAt = kRopeAt + kTile * kRope;
+    static constexpr int kBytes = kScalesAt + kTile * kScales;
 
     // The direct loads of ROWS rows, each of up to 1024 consecutive bytes of a
     // part in LDS.
@@ -249,49 +273,56 @@ struct Tile {
     };
 };
 
-template <int FMT, int DV, int DR, int MB, int MQ, int TILE, int BUFS>
-__global__ __launch_bounds__(MB / MQ * TILE / 16 * 64) void attend_kernel(AttendArgs a)
+template <int FMT, int DV, int DR, int MB, int BUFS>
+__global__ __launch_bounds__(MB * kTile * 4) void attend_kernel(AttendArgs a)
 {
     typedef typename Elem<FMT>::type E;
     typedef Mfma<E> M;
     typedef typename M::frag frag;
     typedef E e4 __attribute__((ext_vector_type(4)));
-    typedef Tile<FMT, DV, DR, TILE> TL;
+    typedef Tile<FMT, DV, DR> TL;
     constexpr bool kFp8 = FMT == KVR_ROW_FP8;
     constexpr int kSteps = (DV + DR) / 32;    // MFMA steps of a score
-    constexpr int RG = TILE / 16;             // row blocks of a tile
-    constexpr int NW = MB / MQ * RG;          // waves: MQ blocks of scores each
+    constexpr int RG = kTile / 16;             // row blocks of a tile
+    constexpr int NW = MB * RG;               // waves: a block of scores each
     constexpr int NC = DV / NW / 16;          // value column blocks of a wave
     constexpr int kGroups = kFp8 ? DV / kScaleGroup : 1;
-    constexpr int kRows = TILE / NW;          // rows a wave loads
+    constexpr int kRows = kTile / NW;          // rows a wave loads
     static_assert(DV % (NW * 16) == 0 && kRows >= 4 && kRows <= 16, "");
 
     __shared__ __attribute__((aligned(1024))) uint8_t sTile[BUFS * TL::kBytes];
-    __shared__ __attribute__((aligned(16))) E sP[BUFS - 1][kGroups][MB * 16][TILE];
+    __shared__ __attribute__((aligned(16))) E sP[BUFS - 1][kGroups][MB * 16][kTile];
     __shared__ float sMax[RG][MB * 16];
     __shared__ uint16_t sValid[2][NW];
     __shared__ int sExceeds[4];  // whether a tile's probabilities must be written again
-    __shared__ uint32_t sWord[2][TILE];  // location words, and with a map the
-    __shared__ int32_t sEntry[2][TILE];  // entries, of tiles to come
+    __shared__ uint32_t sWord[2][kTile];  // location words, and with a map the
+    __shared__ int32_t sEntry[2][kTile];  // entries, of tiles to come
 
     const int lane = lane_id(), col = lane & 15, grp = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(wave_id());
-    const int rg = wave % RG, hg = wave / RG;  // the wave's blocks of scores
+    const int rg = wave % RG, hg = wave / RG;  // the wave's block of scores
 
     // workgroups of one selection and share are 8 apart: the same XCD's L2
     // serves their rows
-    const int64_t b = blockIdx.x;
-    const int64_t us = b / (8 * a.groups) * 8 + (b & 7);
-    const int g = (int)(b / 8 % a.groups);
-    if (us >= (int64_t)a.units * a.shares)
+    const uint32_t b = blockIdx.x;  // (below 2^23: n * nq * heads is at most 2^22)
+    const uint32_t turn8 = b / 8 / (uint32_t)a.groups;
+    const uint32_t us = turn8 * 8 + (b & 7);
+    const int g = (int)(b / 8 - turn8 * (uint32_t)a.groups);
+    if (us >= (uint32_t)(a.units * a.shares))
         return;
-    const int unit = (int)(us / a.shares), share = (int)(us % a.shares);
+    const int unit = (int)(us / (uint32_t)a.shares), share = (int)us - unit * a.shares;
     const int i = a.c.map ? unit / a.c.nq : unit;
-    const int r = a.c.req_ids ? a.c.req_ids[i] : i;
+    // The loads that the rows' addresses depend on are issued together (what is
+    // not given is read from the zeros), so that their latencies overlap.
+    const int32_t *req_ids = a.c.req_ids ? a.c.req_ids + i : zero_words;
+    const int32_t *counts = a.c.count ? a.c.count + i : zero_words;
+    const int32_t req_read = *req_ids, count_read = *counts;
+    const LayerPtrs lp = a.layers[a.c.layer];
+    const int r = a.c.req_ids ? req_read : i;
     const bool known = r >= 0 && r < a.sh.n_req;
 
     RowList list;
-    int cnt = a.c.count ? a.c.count[i] : a.c.stride;
+    int cnt = a.c.count ? count_read : a.c.stride;
     list.count = known ? (cnt < 0 ? 0 : (cnt > a.c.stride ? a.c.stride : cnt)) : 0;
     list.len = a.c.map && list.count > 0 ? a.c.k : list.count;
     list.map = a.c.map ? a.c.map + (int64_t)unit * a.c.k : nullptr;
@@ -302,14 +333,13 @@ __global__ __launch_bounds__(MB / MQ * TILE / 16 * 64) void attend_kernel(Attend
     if (list.gathered) {
         list.tail = list.pool = list.hot =
             static_cast<const uint8_t *>(a.c.rows) + (int64_t)i * a.c.stride * a.sh.R;
-    } else if (list.len > 0) {
-        const LayerPtrs lp = a.layers[a.c.layer];
+    } else {
         list.tail = lp.tail + (int64_t)r * a.sh.T * a.sh.R;
         list.pool = lp.pool;
         list.hot = lp.hot + (int64_t)r * a.sh.B * a.sh.R;
     }
 
-    const int tiles = (list.len + TILE - 1) / TILE;
+    const int tiles = (list.len + kTile - 1) / kTile;
     const int per = (tiles + a.shares - 1) / a.shares;
     const int t0 = share * per;
     const int t1 = t0 + per < tiles ? t0 + per : tiles;
@@ -318,29 +348,23 @@ __global__ __launch_bounds__(MB / MQ * TILE / 16 * 64) void attend_kernel(Attend
     // unit is one query)
     const E *q = static_cast<const E *>(a.c.q) + (int64_t)i * a.c.q_stride_entry;
     const int x0 = g * (MB * 16);
-    frag qf[MQ][kSteps];  // of the wave's blocks
+    frag qf[kSteps];  // of the wave's block (past the last query row: that row's,
+                      // whose results are not written)
     auto load_q = [&](auto read) {
+        const int x = x0 + hg * 16 + col;
+        const int xc = x < a.unit_rows ? x : a.unit_rows - 1;
+        const int qi = a.c.map ? unit % a.c.nq : xc / a.c.heads;
+        const int h = a.c.map ? xc : xc % a.c.heads;
+        const E *p = q + (int64_t)qi * a.c.q_stride_query + (int64_t)h * a.c.q_stride_head;
 #pragma unroll
-        for (int mq = 0; mq < MQ; ++mq) {
-            const int x = x0 + (hg * MQ + mq) * 16 + col;
-            const bool in = x < a.unit_rows && t0 < t1;
-            const int xc = in ? x : 0;
-            const int qi = a.c.map ? unit % a.c.nq : xc / a.c.heads;
-            const int h = a.c.map ? xc : xc % a.c.heads;
-            const E *p = q + (int64_t)qi * a.c.q_stride_query + (int64_t)h * a.c.q_stride_head;
-            const frag zero = {};
-#pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
-                // an 8-bit key fragment holds 8 of the 16 codes of one LDS read
-                const int d = kFp8 && s < DV / 32 ? s / 2 * 64 + grp * 16 + (s & 1) * 8
-                                                  : s * 32 + grp * 8;
-                qf[mq][s] = in ? read(p + d) : zero;
-            }
-        }
+        for (int s = 0; s < kSteps; ++s)
+            // an 8-bit key fragment holds 8 of the 16 codes of one LDS read
+            qf[s] = read(p + (kFp8 && s < DV / 32 ? s / 2 * 64 + grp * 16 + (s & 1) * 8
+                                                  : s * 32 + grp * 8));
     };
-    // m: the reference of this lane's query row in each block; m_own, l: those
-    // of the wave's blocks and this lane's shares of their sums
-    float m[MB], m_own[MQ], l[MQ];
+    // m: the reference of this lane's query row in each block; m_own, l: that
+    // of the wave's block and this lane's share of its sum
+    float m[MB], m_own = -__builtin_inff(), l = 0.f;
     f32x4 o[NC][MB];
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
@@ -348,11 +372,6 @@ __global__ __launch_bounds__(MB / MQ * TILE / 16 * 64) void attend_kernel(Attend
 #pragma unroll
         for (int c = 0; c < NC; ++c)
             o[c][mb] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-#pragma unroll
-    for (int mq = 0; mq < MQ; ++mq) {
-        m_own[mq] = -__builtin_inff();
-        l[mq] = 0.f;
     }
     if (threadIdx.x < 3)
         sExceeds[threadIdx.x] = 0;
@@ -362,12 +381,12 @@ __global__ __launch_bounds__(MB / MQ * TILE / 16 * 64) void attend_kernel(Attend
     // address; a row past the list's end reads the last entry's.
     const int mine = wave * kRows + (lane & (kRows - 1));
     auto at = [&](int t) {
-        const int j = t * TILE + mine;
+        const int j = t * kTile + mine;
         return j < list.len ? j : list.len - 1;
     };
     auto entry = [&](int t, int mapped) {
-        const int e = list.map ? mapped : t * TILE + mine;
-        return t < t1 && t * TILE + mine < list.len && e >= 0 && e < list.count ? e : -1;
+        const int e = list.map ? mapped : t * kTile + mine;
+        return t < t1 && t * kTile + mine < list.len && e >= 0 && e < list.count ? e : -1;
     };
     const uint8_t *zeros = zero_row;
     asm volatile("" : "+s"(zeros));  // kept, not looked up for each tile
@@ -399,8 +418,8 @@ __global__ __launch_bounds__(MB / MQ * TILE / 16 * 64) void attend_kernel(Attend
     };
 
     const float to_log2 = a.c.scale * 1.44269504088896340736f;
-    f32x4 s[MQ];    // t_j of the wave's blocks
-    float sum[MQ];  // and the sums of their probabilities
+    f32x4 s;    // t_j of the wave's block
+    float sum;  // and the sum of its probabilities
 
     // (buf: where a tile lies in sTile)
     // LDS reads are issued in batches ahead of the products that use them
@@ -440,7 +459,7 @@ __global__ __launch_bounds__(MB / MQ * TILE / 16 * 64) void attend_kernel(Attend
     // Scores of the wave's block of a tile whose first keys are being read;
     // then(b) starts what else is read or loaded beside batch b.
     auto scores = [&](Keys &key, int buf, auto then) __attribute__((always_inline)) {
-        f32x4 even[MQ] = {}, odd[MQ] = {};
+        f32x4 even = {}, odd = {};
 #pragma unroll
         for (int b = 0; b < kBatches; ++b) {
             if (b + 1 < kBatches)
@@ -448,76 +467,60 @@ __global__ __launch_bounds__(MB / MQ * TILE / 16 * 64) void attend_kernel(Attend
             then(b);
             __builtin_amdgcn_sched_barrier(0);
             if constexpr (kFp8) {
-                f32x4 part[MQ] = {};
+                f32x4 part = {};
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const u32x4 v = key.latent[b & 1][h];
-                    const frag k0 = widen(v[0], v[1]), k1 = widen(v[2], v[3]);
-#pragma unroll
-                    for (int mq = 0; mq < MQ; ++mq)
-                        part[mq] = M::mul(k0, qf[mq][b * 4 + h * 2], part[mq]);
-#pragma unroll
-                    for (int mq = 0; mq < MQ; ++mq)
-                        part[mq] = M::mul(k1, qf[mq][b * 4 + h * 2 + 1], part[mq]);
+                    part = M::mul(widen(v[0], v[1]), qf[b * 4 + h * 2], part);
+                    part = M::mul(widen(v[2], v[3]), qf[b * 4 + h * 2 + 1], part);
                 }
 #pragma unroll
-                for (int mq = 0; mq < MQ; ++mq)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        even[mq][k] = fmaf(part[mq][k], w[k][b], even[mq][k]);
+                for (int k = 0; k < 4; ++k)
+                    even[k] = fmaf(part[k], w[k][b], even[k]);
             } else {
 #pragma unroll
                 for (int j = 0; j < kBatch; j += 2) {
-#pragma unroll
-                    for (int mq = 0; mq < MQ; ++mq)
-                        even[mq] = M::mul(__builtin_bit_cast(frag, key.latent[b & 1][j]),
-                                          qf[mq][b * kBatch + j], even[mq]);
-#pragma unroll
-                    for (int mq = 0; mq < MQ; ++mq)
-                        odd[mq] = M::mul(__builtin_bit_cast(frag, key.latent[b & 1][j + 1]),
-                                         qf[mq][b * kBatch + j + 1], odd[mq]);
+                    even = M::mul(__builtin_bit_cast(frag, key.latent[b & 1][j]),
+                                  qf[b * kBatch + j], even);
+                    odd = M::mul(__builtin_bit_cast(frag, key.latent[b & 1][j + 1]),
+                                 qf[b * kBatch + j + 1], odd);
                 }
             }
             if (b == 0 && DR > 0)
 #pragma unroll
                 for (int st = 0; st < DR / 32; ++st)
-#pragma unroll
-                    for (int mq = 0; mq < MQ; ++mq)
-                        odd[mq] = M::mul(key.rope[st], qf[mq][DV / 32 + st], odd[mq]);
+                    odd = M::mul(key.rope[st], qf[DV / 32 + st], odd);
         }
-#pragma unroll
-        for (int mq = 0; mq < MQ; ++mq)
-            s[mq] = even[mq] + odd[mq];
+        s = even + odd;
     };
 
-    // Probabilities of the wave's block of tile t, into LDS.
+    // Probabilities of the wave's block of tile t, into LDS, rounded to the 16
+    // bits that the matrix instructions take (relative 2^-9 for bf16, 2^-12
+    // for fp16, each on its own; their sum l is taken before the rounding).
     auto pchunk = [&](int head, int chunk) {  // 8 rows of a query row, swizzled
-        return (chunk ^ (TILE == 64 ? head & 7 : (head >> 1) & 3)) * 8;
+        return (chunk ^ (head & 7)) * 8;
     };
     auto write_p = [&](int t, const f32x4 *w) __attribute__((always_inline)) {
         const int pb = BUFS == 3 ? t & 1 : 0;
+        const float ref = m_own == -__builtin_inff() ? 0.f : m_own;
+        float p[4];
 #pragma unroll
-        for (int mq = 0; mq < MQ; ++mq) {
-            const float ref = m_own[mq] == -__builtin_inff() ? 0.f : m_own[mq];
-            float p[4];
+        for (int k = 0; k < 4; ++k)
+            p[k] = exp2_hw(s[k] - ref);
+        sum = (p[0] + p[1]) + (p[2] + p[3]);
+        const int head = hg * 16 + col;
+        const int at = pchunk(head, rg * 2 + (grp >> 1)) + (grp & 1) * 4;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                p[k] = exp2_hw(s[mq][k] - ref);
-            sum[mq] = (p[0] + p[1]) + (p[2] + p[3]);
-            const int head = (hg * MQ + mq) * 16 + col;
-            const int at = pchunk(head, rg * 2 + (grp >> 1)) + (grp & 1) * 4;
+        for (int gi = 0; gi < kGroups; ++gi) {
+            e4 v;
 #pragma unroll
-            for (int gi = 0; gi < kGroups; ++gi) {
-                e4 v;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if constexpr (kFp8)
-                        v[k] = (E)(p[k] * w[k][gi]);
-                    else
-                        v[k] = (E)p[k];
-                }
-                *reinterpret_cast<e4 *>(&sP[pb][gi][head][at]) = v;
+            for (int k = 0; k < 4; ++k) {
+                if constexpr (kFp8)
+                    v[k] = (E)(p[k] * w[k][gi]);
+                else
+                    v[k] = (E)p[k];
             }
+            *reinterpret_cast<e4 *>(&sP[pb][gi][head][at]) = v;
         }
     };
 
@@ -526,12 +529,9 @@ __global__ __launch_bounds__(MB / MQ * TILE / 16 * 64) void attend_kernel(Attend
         const uint32_t counts = sValid[t & 1][first / kRows] >> (first % kRows);
         bool exceeds = false;
 #pragma unroll
-        for (int mq = 0; mq < MQ; ++mq) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                s[mq][k] = (counts >> k) & 1 ? s[mq][k] * to_log2 : -__builtin_inff();
-                exceeds |= s[mq][k] > m_own[mq] + kSlack;
-            }
+        for (int k = 0; k < 4; ++k) {
+            s[k] = (counts >> k) & 1 ? s[k] * to_log2 : -__builtin_inff();
+            exceeds |= s[k] > m_own + kSlack;
         }
         sExceeds[__any(exceeds) ? flag : 3] = 1;
         write_p(t, w);
@@ -541,57 +541,47 @@ __global__ __launch_bounds__(MB / MQ * TILE / 16 * 64) void attend_kernel(Attend
     // maximum becomes the reference, the sums so far are scaled down and the
     // tile's probabilities written again.
     auto settle = [&](int buf, int t) __attribute__((always_inline)) {
-        {
+        float top = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        if (grp == 0)
+            sMax[rg][hg * 16 + col] = top;
+        barrier_lds();
 #pragma unroll
-            for (int mq = 0; mq < MQ; ++mq) {
-                float top = fmaxf(fmaxf(s[mq][0], s[mq][1]), fmaxf(s[mq][2], s[mq][3]));
-                top = fmaxf(top, __shfl_xor(top, 16));
-                top = fmaxf(top, __shfl_xor(top, 32));
-                if (grp == 0)
-                    sMax[rg][(hg * MQ + mq) * 16 + col] = top;
-            }
-            barrier_lds();
+        for (int mb = 0; mb < MB; ++mb) {
+            float to = m[mb];
 #pragma unroll
-            for (int mb = 0; mb < MB; ++mb) {
-                float to = m[mb];
+            for (int k = 0; k < RG; ++k)
+                to = fmaxf(to, sMax[k][mb * 16 + col]);
+            const float alpha = to == -__builtin_inff() ? 1.f : exp2_hw(m[mb] - to);
+            m[mb] = to;
+            m_own = hg == mb ? to : m_own;
+            l = hg == mb ? l * alpha : l;
 #pragma unroll
-                for (int k = 0; k < RG; ++k)
-                    to = fmaxf(to, sMax[k][mb * 16 + col]);
-                const float alpha = to == -__builtin_inff() ? 1.f : exp2_hw(m[mb] - to);
-                m[mb] = to;
-                m_own[mb % MQ] = hg == mb / MQ ? to : m_own[mb % MQ];
-                l[mb % MQ] = hg == mb / MQ ? l[mb % MQ] * alpha : l[mb % MQ];
-#pragma unroll
-                for (int c = 0; c < NC; ++c)
-                    o[c][mb] *= alpha;
-            }
-            f32x4 sc[kFp8 ? 4 : 1];  // the tile's scales once more
-            if constexpr (kFp8)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    sc[k] = *reinterpret_cast<const f32x4 *>(sTile + buf + TL::kScalesAt +
-                                                             (rg * 16 + grp * 4 + k) * 16);
-            write_p(t, sc);
-            barrier_lds();
+            for (int c = 0; c < NC; ++c)
+                o[c][mb] *= alpha;
         }
-    };
-    auto count = [&]() __attribute__((always_inline)) {
+        f32x4 sc[kFp8 ? 4 : 1];  // the tile's scales once more
+        if constexpr (kFp8)
 #pragma unroll
-        for (int mq = 0; mq < MQ; ++mq)
-            l[mq] += sum[mq];
+            for (int k = 0; k < 4; ++k)
+                sc[k] = *reinterpret_cast<const f32x4 *>(sTile + buf + TL::kScalesAt +
+                                                         (rg * 16 + grp * 4 + k) * 16);
+        write_p(t, sc);
+        barrier_lds();
     };
 
     // o[column][query row] += latent[row][column] * p[query row][row] of tile t:
     // its operands, then the products.
     struct Operands {
-        frag p[TILE / 32][MB];
-        i32x2 v[TILE / 32][NC][kFp8 ? 1 : 2];
+        frag p[kTile / 32][MB];
+        i32x2 v[kTile / 32][NC][kFp8 ? 1 : 2];
     };
     const int gi_own = kFp8 ? wave * (DV / NW) / kScaleGroup : 0;
     auto read_p = [&](Operands &op, int t) __attribute__((always_inline)) {
         const int pb = BUFS == 3 ? t & 1 : 0;
 #pragma unroll
-        for (int st = 0; st < TILE / 32; ++st)
+        for (int st = 0; st < kTile / 32; ++st)
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb)
                 op.p[st][mb] = *reinterpret_cast<const frag *>(
@@ -600,7 +590,7 @@ __global__ __launch_bounds__(MB / MQ * TILE / 16 * 64) void attend_kernel(Attend
     auto read_v = [&](Operands &op, int buf) __attribute__((always_inline)) {
         const uint8_t *cur = sTile + buf;
 #pragma unroll
-        for (int st = 0; st < TILE / 32; ++st) {
+        for (int st = 0; st < kTile / 32; ++st) {
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 const int cb = wave * NC + c;  // block of 16 columns
@@ -623,7 +613,7 @@ __global__ __launch_bounds__(MB / MQ * TILE / 16 * 64) void attend_kernel(Attend
     };
     auto values = [&](const Operands &op) __attribute__((always_inline)) {
 #pragma unroll
-        for (int st = 0; st < TILE / 32; ++st) {
+        for (int st = 0; st < kTile / 32; ++st) {
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 frag vf;
@@ -639,40 +629,42 @@ __global__ __launch_bounds__(MB / MQ * TILE / 16 * 64) void attend_kernel(Attend
             }
         }
     };
-    // In the region it ends, the products and the vector instructions beside
-    // them take turns.
-    auto interleave = [&]() __attribute__((always_inline)) {
-#pragma unroll
-        for (int n = 0; n < TILE / 32 * NC * MB; ++n) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // a product
-            __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);   // vector instructions
-        }
-    };
 
     if (t0 < t1) {
         // the entries, words and addresses of the first tiles
-        const int e0 = entry(t0, *entry_at(t0)), e1 = entry(t0 + 1, *entry_at(t0 + 1));
-        int e = entry(t0 + 2, *entry_at(t0 + 2));
-        if (lane < kRows) {
-            sEntry[(t0 + 3) & 1][mine] = *entry_at(t0 + 3);
-            sWord[t0 & 1][mine] = *word_at(e);
+        int mapped[4] = {};
+        if (list.map)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                mapped[k] = list.map[at(t0 + k)];
+        const int e0 = entry(t0, mapped[0]), e1 = entry(t0 + 1, mapped[1]);
+        int e = entry(t0 + 2, mapped[2]);
+        uint32_t w0 = 0, w1 = 0, word = 0;
+        if (list.loc) {
+            w0 = list.loc[e0 < 0 ? 0 : e0];
+            w1 = list.loc[e1 < 0 ? 0 : e1];
+            word = list.loc[e < 0 ? 0 : e];
         }
         // the roles of the buffers and of the flags
         int prev = (BUFS - 1) * TL::kBytes, cur = 0, next = TL::kBytes;
         int f_prev = 2, f_cur = 0, f_next = 1;
-        prepare(e0, *word_at(e0));
+        prepare(e0, w0);
         fetch(cur, t0, 0, 1);
         if (a.wide)
             load_q([](const E *p) { return *reinterpret_cast<const frag *>(p); });
         else
             load_q([](const E *p) {
                 frag f;
-    #pragma unroll
+#pragma unroll
                 for (int e = 0; e < 8; ++e)
                     f[e] = p[e];
                 return f;
             });
-        prepare(e1, *word_at(e1));
+        prepare(e1, w1);
+        if (lane < kRows) {
+            sEntry[(t0 + 3) & 1][mine] = mapped[3];
+            sWord[t0 & 1][mine] = word;
+        }
         // On their way from tile t's turn: the rows of tile t + 1, the words of
         // tile t + 3, the map's entries of tile t + 4.  (Past the last tile they
         // are rows of zeros and repeated words.)
@@ -714,8 +706,6 @@ __global__ __launch_bounds__(MB / MQ * TILE / 16 * 64) void attend_kernel(Attend
             softmax(t, f_cur);
             if (BUFS == 3) {
                 prepare(e, w2);
-                if (!decltype(first)::value)
-                    interleave();
                 turn();
                 ++t;
                 barrier_all();
@@ -737,7 +727,7 @@ __global__ __launch_bounds__(MB / MQ * TILE / 16 * 64) void attend_kernel(Attend
             settle(BUFS == 3 ? prev : cur, BUFS == 3 ? t - 1 : t);
             again = false;
             for (;;) {
-                count();
+                l += sum;
                 if (BUFS == 2) {
                     read_p(op, t);
                     values(op);
@@ -766,13 +756,10 @@ __global__ __launch_bounds__(MB / MQ * TILE / 16 * 64) void attend_kernel(Attend
 
     // the sums of the waves and lane groups that share a query row
     barrier_all();  // also: no load is on its way to LDS when the wave ends
-#pragma unroll
-    for (int mq = 0; mq < MQ; ++mq) {
-        l[mq] += __shfl_xor(l[mq], 16);
-        l[mq] += __shfl_xor(l[mq], 32);
-        if (grp == 0)
-            sMax[rg][(hg * MQ + mq) * 16 + col] = l[mq];
-    }
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    if (grp == 0)
+        sMax[rg][hg * 16 + col] = l;
     barrier_lds();
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
@@ -786,7 +773,7 @@ __global__ __launch_bounds__(MB / MQ * TILE / 16 * 64) void attend_kernel(Attend
         const int64_t at = (int64_t)unit * a.unit_rows + x;  // query row of the call
         const int c0 = wave * (DV / NW) + grp * 4;
         if (a.shares > 1) {
-            const int64_t ps = us * a.unit_rows + x;
+            const int64_t ps = (int64_t)us * a.unit_rows + x;
             if (wave == 0 && grp == 0)
                 *reinterpret_cast<float2 *>(a.stat + 2 * ps) = make_float2(m[mb], sum);
             if (m[mb] == -__builtin_inff() && sum == 0.f)
@@ -813,8 +800,9 @@ __global__ __launch_bounds__(MB / MQ * TILE / 16 * 64) void attend_kernel(Attend
 
 // Joins the shares of each query row: a workgroup per row, its waves taking
 // every fourth share with several in flight, their sums added in wave order.
-// Bound by reading the shares (one after the other, a wave for all, took 19 us
-// for 32 shares of 512 rows).
+// Bound by the latency of reading them: 16 shares of 512 query rows (17 MB) in
+// 5.4 us, of which an empty launch is 4; one wave reading one share after the
+// other took 19 us for 32 shares.
 constexpr int kJoinWaves = 4;
 template <typename E, int DV>
 __global__ __launch_bounds__(kJoinWaves * 64) void join_kernel(AttendArgs a)
@@ -889,11 +877,13 @@ __global__ __launch_bounds__(kJoinWaves * 64) void join_kernel(AttendArgs a)
 template <int FMT, int DV, int DR>
 hipError_t launch_dims(const kvr_ctx *c, const AttendArgs &a, int block, dim3 grid, hipStream_t s)
 {
-    constexpr int kBufs = FMT == KVR_ROW_FP8 || DV == 256 ? 3 : 2;  // what LDS holds
+    // Three tiles where LDS holds them (64 16-bit rows of 576 values are 72 KB):
+    // 64 requests of 128 heads, fp8 rows, take 75 us with three, 79 with two.
+    constexpr int kBufs = FMT == KVR_ROW_FP8 || DV == 256 ? 3 : 2;
     if (block == 16)
-        return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 1, 1, 64, kBufs>, grid,
+        return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 1, kBufs>, grid,
                       dim3(256), 0, s, a);
-    return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 2, 1, 64, kBufs>, grid, dim3(512), 0,
+    return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 2, kBufs>, grid, dim3(512), 0,
                   s, a);
 }
 
@@ -907,21 +897,36 @@ hipError_t launch_format(const kvr_ctx *c, const AttendArgs &a, int block, dim3 
                       : launch_dims<FMT, 256, 0>(c, a, block, grid, s);
 }
 
+template <typename E, int DV>
+hipError_t launch_join(const kvr_ctx *c, const AttendArgs &a, hipStream_t s)
+{
+    return launch(c, KVR_KERNEL_ATTEND, join_kernel<E, DV>,
+                  dim3((unsigned)((int64_t)a.units * a.unit_rows)), dim3(kJoinWaves * 64), 0, s, a);
+}
+
 constexpr int64_t kWorkgroups = 256;  // compute units: one workgroup each
+constexpr int kMaxBlock = 32;         // query rows
 
 int64_t partial_bytes(int64_t rows, int32_t d_v) { return rows * (d_v + 2) * (int64_t)sizeof(float); }
 
 }  // namespace
 
-// A selection shared by unit_rows query rows is cut into blocks of at most 64
-// of them, and into shares (of at least one tile) until every compute unit has
-// a workgroup.
+// A selection shared by unit_rows query rows is cut into blocks of 16 or 32 of
+// them, and into shares (of at least one tile) until every compute unit has a
+// workgroup.
+//   block   16 when that holds all the rows: a block of 32 would do the work of
+//           twice as many (64 requests of 16 heads: 25 us against 28); more rows
+//           go to blocks of 32, which read each tile half as often (64 requests
+//           of 128 heads: 75 us against 120, 8 requests of 64 heads 18 against 19)
+//   shares  256 workgroups (kernel + join): 8 requests of 64 heads, 2048 rows
+//           with 128 of them 22 + 4 us, with 256 18 + 5, with 512 (two rounds)
+//           28 + 9; 64 requests of 16 heads 34 + 4, 25 + 4, 34 + 5
 AttendPlan attend_plan(int32_t n, int32_t nq, int32_t heads, int32_t d_v, int32_t rows, bool mapped)
 {
     AttendPlan p{};
     const int64_t units = mapped ? (int64_t)n * nq : n;
     const int32_t unit_rows = mapped ? heads : nq * heads;
-    p.block = unit_rows <= 16 ? 16 : 32;
+    p.block = unit_rows <= 16 ? 16 : kMaxBlock;
     p.groups = (unit_rows + p.block - 1) / p.block;
     const int64_t tiles = (rows + kTile - 1) / kTile;
     int64_t shares = kWorkgroups / (units * p.groups);
@@ -932,14 +937,14 @@ AttendPlan attend_plan(int32_t n, int32_t nq, int32_t heads, int32_t d_v, int32_
 }
 
 // Over all smaller calls: their query rows times shares are at most the query
-// rows times tiles, and at most a block of 64 for each workgroup.
+// rows times tiles, and at most a block for each workgroup.
 int64_t attend_workspace_bound(int32_t n, int32_t nq, int32_t heads, int32_t d_v, int32_t rows)
 {
     const int64_t all = (int64_t)n * nq * heads, tiles = (rows + kTile - 1) / kTile;
     const int64_t most = all * tiles;
     if (tiles < 2)
         return 0;
-    return partial_bytes(most < kWorkgroups * 64 ? most : kWorkgroups * 64, d_v);
+    return partial_bytes(most < kWorkgroups * kMaxBlock ? most : kWorkgroups * kMaxBlock, d_v);
 }
 
 hipError_t launch_attend(const kvr_ctx *c, const kvr_attend_call &call, const AttendPlan &plan,
@@ -949,6 +954,8 @@ hipError_t launch_attend(const kvr_ctx *c, const kvr_attend_call &call, const At
     a.sh = c->shape;
     a.layers = c->layers_d;
     a.c = call;
+    if (call.rows)
+        a.c.layer = 0;  // (not checked then, and not used)
     a.units = call.map ? call.n * call.nq : call.n;
     a.unit_rows = call.map ? call.heads : call.nq * call.heads;
     a.groups = plan.groups;
@@ -964,18 +971,10 @@ hipError_t launch_attend(const kvr_ctx *c, const kvr_attend_call &call, const At
                                                  : launch_format<KVR_ROW_F16>(c, a, plan.block, grid, s);
     if (e != hipSuccess || a.shares == 1)
         return e;
-    const dim3 rows((unsigned)((int64_t)a.units * a.unit_rows));
     if (call.format == KVR_ROW_F16)
-        return call.d_v == 512
-                   ? launch(c, KVR_KERNEL_ATTEND, join_kernel<_Float16, 512>, rows, dim3(kJoinWaves * 64), 0, s,
-                            a)
-                   : launch(c, KVR_KERNEL_ATTEND, join_kernel<_Float16, 256>, rows, dim3(kJoinWaves * 64), 0, s,
-                            a);
-    return call.d_v == 512
-               ? launch(c, KVR_KERNEL_ATTEND, join_kernel<__bf16, 512>, rows, dim3(kJoinWaves * 64), 0, s,
-                            a)
-               : launch(c, KVR_KERNEL_ATTEND, join_kernel<__bf16, 256>, rows, dim3(kJoinWaves * 64), 0, s,
-                            a);
+        return call.d_v == 512 ? launch_join<_Float16, 512>(c, a, s)
+                               : launch_join<_Float16, 256>(c, a, s);
+    return call.d_v == 512 ? launch_join<__bf16, 512>(c, a, s) : launch_join<__bf16, 256>(c, a, s);
 }
 
 }  // namespace kvr

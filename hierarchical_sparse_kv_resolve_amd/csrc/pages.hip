@@ -12,7 +12,17 @@
 // counts change by integer atomics, so results do not depend on their order.
 //
 // Every kernel here moves whole rows or pages as 16-byte chunks and is bound
-// by the memory it moves (HBM, or the host link for host rows).
+// by the memory it moves.  Measured on one MI355X:
+//   fork      one request of 4096 rows of 1152 bytes, half of its pages ready
+//             (2.4 MB read from and written to host memory, 1.2 MB of HBM
+//             copies): 87 us; four requests of 8192 rows, two layers (22 MB each
+//             way over the host link): 565 us, 80 GB/s of both directions (a
+//             copy engine reaches 57 each way, two at once 57 together).  A tile
+//             of rows per workgroup; workers in a loop (16 to 256) and 2 to 8
+//             chunks a lane were no faster.
+//   compact   256 pages, 30 % free: 8 us to rank them, 7 to move about 50; 16384 pages
+//             of 42 KB, about 3440 of them moved (289 MB): 6 + 10 us to count and rank,
+//             52 to move, 5.6 TB/s
 #include "kvr_internal.h"
 #include "rows.h"
 

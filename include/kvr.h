@@ -501,7 +501,7 @@ int kvr_pack_rows(kvr_ctx *ctx, const kvr_pack_call *call, void *stream);
  *     (bf16 with fp8 rows); strides in elements between entries, queries and
  *     heads, the last dimension contiguous
  *   out (device) [n][nq][heads][d_v] contiguous, of q's type, aligned to 16
- *     bytes; lse (device) float [n][nq][heads] or NULL
+ *     bytes, disjoint from the inputs; lse (device) float [n][nq][heads] or NULL
  *   status (device) int32 [n] or NULL: KVR_E_RANGE for an entry with a
  *     location outside its place (which is left out; rows NULL only),
  *     KVR_E_ARG for a request id out of range (which attends to nothing),
