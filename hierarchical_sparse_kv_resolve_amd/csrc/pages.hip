@@ -20,9 +20,10 @@
 //             copy engine reaches 57 each way, two at once 57 together).  A tile
 //             of rows per workgroup; workers in a loop (16 to 256) and 2 to 8
 //             chunks a lane were no faster.
-//   compact   256 pages, 30 % free: 8 us to rank them, 7 to move about 50; 16384 pages
-//             of 42 KB, about 3440 of them moved (289 MB): 6 + 10 us to count and rank,
-//             52 to move, 5.6 TB/s
+//   compact   256 pages of 73 KB, 30 % free: 8 us to rank them, 5 to move about
+//             50 (an empty kernel 4); 16384 pages of 42 KB, about 3440 of them
+//             moved (289 MB): 6 + 10 us to count and rank, 60 to move, 4.8 TB/s
+//   copies    32 pages of 73 KB, two layers: 6 + 4 us
 #include "kvr_internal.h"
 #include "rows.h"
 
@@ -30,6 +31,7 @@ namespace kvr {
 namespace {
 
 constexpr int NT = kRowThreads;
+constexpr int kFullGrid = 1024;          // workgroups that keep the card busy
 constexpr int kMaxCopyBlocks = 1 << 16;  // grids past this stride over their jobs
 
 // Whether an earlier entry of either list names id (every thread scans a
@@ -248,14 +250,29 @@ __global__ __launch_bounds__(NT) void fork_kernel(ForkArgs a)
 
 // -------------------------------------------------------------- page moves
 
-// One page of one layer within its pool, by the whole workgroup.
-__device__ __forceinline__ void copy_page(const Shape &sh, uint8_t *pool, int32_t from, int32_t to)
+constexpr int kPartChunks = NT * kUnroll;  // 16-byte chunks a workgroup moves at once
+
+// Workgroups that share a page, given how many jobs (pages times layers) there
+// are at most: one if those fill the card, else up to one for each 32 KB.  (32
+// pages of 73 KB, two layers: 10 us with one, 6 with three; a compaction of 256
+// such pages: 7 and 5 us.)
+int page_parts(const Shape &sh, int64_t jobs)
+{
+    const int64_t most = ((int64_t)sh.P * sh.R / 16 + kPartChunks - 1) / kPartChunks;
+    const int64_t want = kFullGrid / (jobs < 1 ? 1 : jobs);
+    return (int)(want < 1 ? 1 : want < most ? want : most);
+}
+
+// Part `part` of `parts` of a page of one layer within its pool, by the whole
+// workgroup.
+__device__ __forceinline__ void copy_page(const Shape &sh, uint8_t *pool, int32_t from, int32_t to,
+                                          int part, int parts)
 {
     const int64_t bytes = (int64_t)sh.P * sh.R;
     const int64_t chunks = bytes / 16;
     const uint8_t *src = pool + from * bytes;
     uint8_t *dst = pool + to * bytes;
-    for (int64_t c0 = 0; c0 < chunks; c0 += NT * kUnroll) {
+    for (int64_t c0 = (int64_t)part * kPartChunks; c0 < chunks; c0 += (int64_t)parts * kPartChunks) {
         u32x4 v[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
@@ -280,7 +297,7 @@ struct CopyArgs {
     int32_t *status;
 };
 
-// grid (entries, layers).  Entries are judged on the state before the call:
+// grid (entries, layers, parts of a page).  Entries are judged on the state before the call:
 // this launch writes no metadata, the commit launch after it does.
 __global__ __launch_bounds__(NT) void copy_pages_kernel(CopyArgs a)
 {
@@ -302,8 +319,8 @@ __global__ __launch_bounds__(NT) void copy_pages_kernel(CopyArgs a)
             st = KVR_E_STATE;
     }
     if (st == KVR_OK)
-        copy_page(sh, a.layers[blockIdx.y].pool, from, ph);
-    if (threadIdx.x == 0 && blockIdx.y == 0)
+        copy_page(sh, a.layers[blockIdx.y].pool, from, ph, blockIdx.z, gridDim.z);
+    if (threadIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
         a.status[i] = st;
 }
 
@@ -465,7 +482,7 @@ struct CompactArgs {
     const LayerPtrs *layers;
     int32_t *page_map, *refs;
     const int32_t *rank, *moves, *move_count, *block_live;
-    int32_t blocks, map_blocks;
+    int32_t blocks, map_blocks, parts;
 };
 
 // Workgroups [0, map_blocks) bring the page maps in line, the others move the
@@ -498,12 +515,14 @@ __global__ __launch_bounds__(NT) void compact_kernel(CompactArgs a)
         return;
     }
     const int moves = *a.move_count;
-    const int64_t jobs = (int64_t)moves * sh.n_layers;
+    const int per_move = sh.n_layers * a.parts;
+    const int64_t jobs = (int64_t)moves * per_move;
     for (int64_t job = blockIdx.x - a.map_blocks; job < jobs; job += gridDim.x - a.map_blocks) {
-        const int k = (int)(job / sh.n_layers), l = (int)(job - (int64_t)k * sh.n_layers);
+        const int k = (int)(job / per_move), rest = (int)(job - (int64_t)k * per_move);
+        const int l = rest / a.parts, part = rest - l * a.parts;
         const int32_t from = a.moves[2 * (int64_t)k], to = a.moves[2 * (int64_t)k + 1];
-        copy_page(sh, a.layers[l].pool, from, to);
-        if (l == 0 && threadIdx.x == 0) {
+        copy_page(sh, a.layers[l].pool, from, to, part, a.parts);
+        if (rest == 0 && threadIdx.x == 0) {
             a.refs[to] = a.refs[from];
             a.refs[from] = 0;
         }
@@ -597,8 +616,9 @@ hipError_t launch_copy_pages(const kvr_ctx *c, int32_t n, const int32_t *req, co
                              const int32_t *phys, int32_t *status, hipStream_t s)
 {
     CopyArgs a{c->shape, c->layers_d, c->page_map, c->page_refs, req, page, phys, status};
-    hipError_t e = launch(c, KVR_KERNEL_PAGES, copy_pages_kernel, dim3(n, c->shape.n_layers),
-                          dim3(NT), 0, s, a);
+    const int parts = page_parts(c->shape, (int64_t)n * c->shape.n_layers);
+    hipError_t e = launch(c, KVR_KERNEL_PAGES, copy_pages_kernel,
+                          dim3(n, c->shape.n_layers, parts), dim3(NT), 0, s, a);
     if (e != hipSuccess)
         return e;
     return launch(c, KVR_KERNEL_PAGES, copy_commit_kernel, dim3((n + NT - 1) / NT), dim3(NT), 0, s,
@@ -637,9 +657,11 @@ hipError_t launch_compact(const kvr_ctx *c, int32_t max_moves, int32_t *moves, i
     if (e != hipSuccess)
         return e;
     CompactArgs k{c->shape, c->layers_d, c->page_map, c->page_refs, a.rank, moves, move_count,
-                  a.block_live, a.blocks, 0};
+                  a.block_live, a.blocks, 0, 1};
     k.map_blocks = (int32_t)blocks_for((int64_t)k.sh.n_req * k.sh.n_pages, 256);
-    const int64_t most = (a.pages / 2 < max_moves ? a.pages / 2 : max_moves) * k.sh.n_layers;
+    const int64_t pages = (a.pages / 2 < max_moves ? a.pages / 2 : max_moves) * k.sh.n_layers;
+    k.parts = page_parts(k.sh, pages);
+    const int64_t most = pages * k.parts;
     const int64_t copies = most < 1 ? 1 : (most > 8192 ? 8192 : most);
     return launch(c, KVR_KERNEL_PAGES, compact_kernel, dim3((unsigned)(k.map_blocks + copies)),
                   dim3(NT), 0, s, k);
