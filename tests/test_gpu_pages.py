@@ -284,6 +284,41 @@ def test_free_list_and_compaction(seed, kw):
             s.release(1)
 
 
+@pytest.mark.parametrize("seed,P,R,NL", [(41, 64, 1152, 2), (42, 129, 256, 1), (43, 128, 256, 3),
+                                          (44, 200, 1152, 1), (45, 16, 4096, 2)])
+def test_long_pages(seed, P, R, NL):
+    """Copies and compaction of pages that several workgroups share: pages of
+    one piece and a little more, of exactly one, of several."""
+    s = State(seed, P=P, R=R, NL=NL, H=5 * P + 3, ready=0.7, spare=9)
+    s.ctx.fork_requests(1, ints(0), ints(3))
+    s.fork(0, 3)
+    free = np.nonzero(s.refs == 0)[0]
+    held = [(r, p) for r in range(s.n_req) for p in range(s.full) if s.page_map[r, p] >= 0]
+    take = [(r, p, int(ph)) for (r, p), ph in zip(held, free[-4:])]
+    assert len(take) == 4
+    status = torch.full((4,), 77, dtype=torch.int32, device="cuda")
+    s.ctx.copy_pages(4, *[ints(*col) for col in zip(*take)], status)
+    for r, p, ph in take:
+        old = s.page_map[r, p]
+        for l in range(NL):
+            s.pool[l][ph] = s.pool[l][old]
+        s.refs[old] -= 1
+        s.refs[ph] += 1
+        s.page_map[r, p] = ph
+    s.check()
+    assert status.cpu().tolist() == [0] * 4
+    s.ctx.release_requests(2, ints(0, 1))
+    s.release(0)
+    s.release(1)
+    moves = torch.zeros(s.pages, 2, dtype=torch.int32, device="cuda")
+    n = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for most in (2, s.pages):
+        s.ctx.compact_pool(most, moves, n, s.ws)
+        plan = s.compact(most)
+        s.check()
+        assert n.item() == len(plan) and moves.cpu().tolist()[:len(plan)] == [list(m) for m in plan]
+
+
 def test_captured_and_replayed():
     """Release, fork and compaction as one graph, replayed over changing state."""
     s = State(31, n_req=8, users=4, ready=0.6)
