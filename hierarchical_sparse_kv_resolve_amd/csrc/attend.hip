@@ -38,7 +38,8 @@
 //
 // Rows left out are read from a row of zeros and their p is 0.
 //
-// What bounds it (one MI355X; the kernel, then the join of the shares):
+// What bounds it (one MI355X; the kernel, then the join of the shares; calls
+// over the same inputs, a few percent more over changing ones):
 // with few query rows a selection, reading the rows,
 //   64 requests x 16 heads x 2048 fp8 rows of 656 bytes     25 + 4 us, 3.4 TB/s
 //   32 requests x 4 queries x 16 heads x 2048 bf16 rows of a union of 3277,

@@ -23,7 +23,7 @@
 //   compact   256 pages of 73 KB, 30 % free: 8 us to rank them, 5 to move about
 //             50 (an empty kernel 4); 16384 pages of 42 KB, about 3440 of them
 //             moved (289 MB): 6 + 10 us to count and rank, 60 to move, 4.8 TB/s
-//   copies    32 pages of 73 KB, two layers: 6 + 4 us
+//   copies    32 pages of 73 KB, two layers: 7 + 4 us
 #include "kvr_internal.h"
 #include "rows.h"
 
