@@ -307,6 +307,19 @@ def _dev_here(x, name: str, nbytes: int = 0, here: int | None = None) -> int | N
     return _dev(_same_device(x, name, here), name, nbytes)
 
 
+def _words(x, name: str, n: int, here: int | None = None) -> int | None:
+    """Address of n 32-bit integers on the current device."""
+    if x is None or isinstance(x, int):
+        return x
+    if hasattr(x, "is_cuda"):
+        kind = _DTYPE_NAMES.get(x.dtype)
+        if kind is None:
+            kind = _DTYPE_NAMES[x.dtype] = str(x.dtype)[6:]
+        if kind != "int32" and kind != "uint32":
+            raise TypeError(f"{name}: expected int32 or uint32, got {x.dtype}")
+    return _dev_here(x, name, 4 * n, here)
+
+
 def _workspace(x, here: int | None = None):
     """(address, bytes) of a workspace tensor; an address is taken to hold what
     the call needs."""
@@ -638,44 +651,40 @@ class Context:
                 raise ValueError(f"map: {map_.ndim} dimensions, the call needs [n, nq, k]")
             k = int(map_.shape[2]) if hasattr(map_, "shape") else 0
             _typed(map_, "map", ("int32",), here, (n, nq, k))
-        if count is not None and not isinstance(count, int):
-            _typed(count, "count", ("int32",), here)
         m = max(n, 0) * max(stride, 0)
         ws, ws_bytes = _workspace(workspace, here)
         strides = q.stride()
         call = AttendCall(layer, code, n, nq, heads, d_v, d_rope, stride, k, scale,
-                          _dev_here(req_ids, "req_ids", 4 * n, here),
-                          _dev_here(loc, "loc", 4 * m, here),
+                          _words(req_ids, "req_ids", n, here),
+                          _words(loc, "loc", m, here),
                           _dev_here(rows, "rows", m * self.cfg.row_bytes, here),
-                          _dev_here(count, "count", 4 * n, here), _dev(map_, "map"),
+                          _words(count, "count", n, here), _dev(map_, "map"),
                           q.data_ptr(), strides[0], strides[1], strides[2], _dev(out, "out"),
-                          _dev(lse, "lse"), _dev_here(status, "status", 4 * n, here), ws, ws_bytes)
+                          _dev(lse, "lse"), _words(status, "status", n, here), ws, ws_bytes)
         _check(lib().kvr_attend_rows(self.handle, ctypes.byref(call), _stream(stream)))
 
     # ------------------------------------------- pages shared by requests
 
     def bind_page_refs(self, refs):
         """int32 [pool_pages] map entries naming each physical page, or None."""
-        _check(lib().kvr_bind_page_refs(self.handle,
-                                        _dev_here(refs, "refs", 4 * self.cfg.pool_pages)))
+        _check(lib().kvr_bind_page_refs(self.handle, _words(refs, "refs", self.cfg.pool_pages)))
 
     def count_page_refs(self, stream=None):
         _check(lib().kvr_count_page_refs(self.handle, _stream(stream)))
 
     def release_requests(self, n, req_ids, status=None, stream=None):
-        _check(lib().kvr_release_requests(self.handle, n, _dev_here(req_ids, "req_ids", 4 * n),
-                                          _dev_here(status, "status", 4 * n), _stream(stream)))
+        _check(lib().kvr_release_requests(self.handle, n, _words(req_ids, "req_ids", n),
+                                          _words(status, "status", n), _stream(stream)))
 
     def fork_requests(self, n, src_ids, dst_ids, status=None, stream=None):
-        _check(lib().kvr_fork_requests(self.handle, n, _dev_here(src_ids, "src_ids", 4 * n),
-                                       _dev_here(dst_ids, "dst_ids", 4 * n),
-                                       _dev_here(status, "status", 4 * n), _stream(stream)))
+        _check(lib().kvr_fork_requests(self.handle, n, _words(src_ids, "src_ids", n),
+                                       _words(dst_ids, "dst_ids", n),
+                                       _words(status, "status", n), _stream(stream)))
 
     def copy_pages(self, n, req_ids, pages, phys, status, stream=None):
-        _check(lib().kvr_copy_pages(self.handle, n, _dev_here(req_ids, "req_ids", 4 * n),
-                                    _dev_here(pages, "pages", 4 * n),
-                                    _dev_here(phys, "phys", 4 * n),
-                                    _dev_here(status, "status", 4 * n), _stream(stream)))
+        _check(lib().kvr_copy_pages(self.handle, n, _words(req_ids, "req_ids", n),
+                                    _words(pages, "pages", n), _words(phys, "phys", n),
+                                    _words(status, "status", n), _stream(stream)))
 
     def pool_workspace(self) -> int:
         """Workspace bytes of list_free_pages and compact_pool."""
@@ -685,14 +694,14 @@ class Context:
     def list_free_pages(self, free_list, free_count, workspace, stream=None):
         ws, ws_bytes = _workspace(workspace)
         _check(lib().kvr_list_free_pages(
-            self.handle, _dev_here(free_list, "free_list", 4 * self.cfg.pool_pages),
-            _dev_here(free_count, "free_count", 4), ws, ws_bytes, _stream(stream)))
+            self.handle, _words(free_list, "free_list", self.cfg.pool_pages),
+            _words(free_count, "free_count", 1), ws, ws_bytes, _stream(stream)))
 
     def compact_pool(self, max_moves, moves, move_count, workspace, stream=None):
         ws, ws_bytes = _workspace(workspace)
-        need = 8 * max(0, min(max_moves, self.cfg.pool_pages))
-        _check(lib().kvr_compact_pool(self.handle, max_moves, _dev_here(moves, "moves", need),
-                                      _dev_here(move_count, "move_count", 4), ws, ws_bytes,
+        need = 2 * max(0, min(max_moves, self.cfg.pool_pages))
+        _check(lib().kvr_compact_pool(self.handle, max_moves, _words(moves, "moves", need),
+                                      _words(move_count, "move_count", 1), ws, ws_bytes,
                                       _stream(stream)))
 
 

@@ -460,6 +460,8 @@ def test_refusals():
     refused(ValueError, "lse: shape", lse=torch.zeros(2, 16, device="cuda"))
     refused(TypeError, "map: expected int32", map_=torch.zeros(2, 1, 4, device="cuda"))
     refused(TypeError, "count: expected int32", count=torch.zeros(2, device="cuda"))
+    refused(TypeError, "loc: expected int32", loc=loc.long())
+    refused(TypeError, "status: expected int32", status=torch.zeros(2, device="cuda"))
     refused(ValueError, "loc: ", loc=loc[:, :39].contiguous())
     refused(ValueError, "count: ", count=torch.zeros(1, dtype=torch.int32, device="cuda"))
     refused(KvrError, "layer 1 outside", layer=1)

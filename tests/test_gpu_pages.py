@@ -360,6 +360,10 @@ def test_refusals():
         s.ctx.fork_requests(2, ints(0, 1), one)
     with pytest.raises(TypeError, match="expected a GPU tensor"):
         s.ctx.fork_requests(1, one.cpu(), one)
+    with pytest.raises(TypeError, match="src_ids: expected int32"):
+        s.ctx.fork_requests(1, one.long(), one)
+    with pytest.raises(TypeError, match="phys: expected int32"):
+        s.ctx.copy_pages(1, one, one, one.float(), status)
     with pytest.raises(ValueError, match="refs: "):
         s.ctx.bind_page_refs(s.dev["refs"][:-1])
     moves = torch.zeros(s.pages, 2, dtype=torch.int32, device="cuda")

@@ -98,6 +98,11 @@ def test_binding_checks():
         kvr._typed(torch.zeros(4), "latent", ("float32",))
     with pytest.raises(TypeError, match="expected a GPU tensor"):
         kvr._dev_here(torch.zeros(4), "loc", 16)
+    with pytest.raises(TypeError, match="loc: expected int32 or uint32, got torch.int64"):
+        kvr._words(torch.zeros(4, dtype=torch.int64), "loc", 4)
+    with pytest.raises(TypeError, match="loc: expected a GPU tensor"):
+        kvr._words(torch.zeros(4, dtype=torch.int32), "loc", 4)
+    assert kvr._words(4096, "loc", 1 << 40) == 4096 and kvr._words(None, "loc", 4) is None
     assert kvr._dev_here(4096, "loc", 1 << 40) == 4096 and kvr._dev_here(None, "loc") is None
     assert kvr._workspace(None) == (None, 0)
     assert kvr._workspace(4096)[0] == 4096
