@@ -496,8 +496,8 @@ __global__ __launch_bounds__(MB * kTile * 4) void attend_kernel(AttendArgs a)
     };
 
     // Probabilities of the wave's block of tile t, into LDS, rounded to the 16
-    // bits that the matrix instructions take (relative 2^-9 for bf16, 2^-12
-    // for fp16, each on its own; their sum l is taken before the rounding).
+    // bits that the matrix instructions take (off by at most 2^-8 of each for
+    // bf16, 2^-11 for fp16; their sum l is taken before the rounding).
     auto pchunk = [&](int head, int chunk) {  // 8 rows of a query row, swizzled
         return (chunk ^ (head & 7)) * 8;
     };

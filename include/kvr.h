@@ -542,7 +542,8 @@ typedef struct kvr_attend_call {
  * attention consumes the rows the location vector names):
  *   s_j = scale * (q . key_j),  out = sum_j exp(s_j - lse) value_j,
  *   lse = ln sum_j exp(s_j)
- * over the entries of the query.  A query without any gets out = 0 and
+ * over the entries of the query (one that is named twice counts twice).  A
+ * query without any, or whose scores are all -infinity, gets out = 0 and
  * lse = -infinity.  Rows left out are not read, whatever they hold; a NaN in
  * a row that takes part shows in the result.  Products of 16-bit values (an
  * e4m3 code is exact in bf16), sums, maxima and exponentials in 32 bits;

@@ -303,6 +303,30 @@ def test_scores_far_apart(fmt):
     check(src, *run(src, 1, 1, 16, 600, words=words, scale=0.0)[:5])
 
 
+@pytest.mark.parametrize("stride", [5, 70, 700])
+def test_infinite_scores(stride):
+    """A head whose scores are all -infinity is as one without rows, one with
+    +infinity is NaN, and neither touches its neighbours."""
+    src = Source(18, 2, "bf16", 512, 64)
+    q = torch.zeros(2, 1, 20, 576, dtype=torch.bfloat16, device="cuda")
+    q[0, 0, 3, 0] = -float("inf")
+    q[1, 0, 18, 1] = float("inf")
+    rows = torch.ones(2, stride, 576, dtype=torch.bfloat16, device="cuda").view(torch.uint8)
+    out = torch.full((2, 1, 20, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((2, 1, 20), 7.0, device="cuda")
+    ws = torch.empty(src.ctx.attend_workspace(2, 1, 20, 512, stride), dtype=torch.uint8, device="cuda")
+    src.ctx.attend_rows(0, 2, None, q, out, fmt="bf16", d_v=512, d_rope=64, scale=0.5,
+                        stride=stride, rows=rows, lse=lse, workspace=ws)
+    torch.cuda.synchronize()
+    assert (out[0, 0, 3] == 0).all() and lse[0, 0, 3].item() == -np.inf
+    assert out[1, 0, 18].isnan().all() and lse[1, 0, 18].isnan()
+    keep = torch.ones(2, 1, 20, dtype=torch.bool, device="cuda")
+    keep[0, 0, 3] = keep[1, 0, 18] = False
+    # p = 1 for every row: out is 1 up to the roundings of 1 / l, lse is ln(stride)
+    assert (out[keep] == 1).all()
+    assert ((lse[keep] - np.log(stride)).abs() <= 32 * EPS32 * (1 + np.log(stride))).all()
+
+
 def test_strided_queries():
     """Queries as a slice of a larger tensor (odd head and entry strides)."""
     src = Source(10, 3, "bf16", 512, 64)
