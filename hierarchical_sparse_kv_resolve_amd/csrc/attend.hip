@@ -43,7 +43,7 @@
 // with few query rows a selection, reading the rows,
 //   64 requests x 16 heads x 2048 fp8 rows of 656 bytes     25 + 4 us, 3.4 TB/s
 //   32 requests x 4 queries x 16 heads x 2048 bf16 rows of a union of 3277,
-//   each query its own rows                        51 + 6 us, 5.9 TB/s read
+//   each query its own rows                        50 + 6 us, 6.0 TB/s read
 //   (from HBM only the union once, 121 MB);
 // with many, the vector, matrix and LDS instructions of two waves a SIMD,
 //   64 requests x 128 heads x 2048 fp8 rows        75 us, 480 TFLOP/s
@@ -303,14 +303,18 @@ __global__ __launch_bounds__(MB * kTile * 4) void attend_kernel(AttendArgs a)
     const int wave = __builtin_amdgcn_readfirstlane(wave_id());
     const int rg = wave % RG, hg = wave / RG;  // the wave's block of scores
 
-    // workgroups of one selection and share are 8 apart: the same XCD's L2
-    // serves their rows
-    const uint32_t b = blockIdx.x;  // (below 2^23: n * nq * heads is at most 2^22)
-    const uint32_t turn8 = b / 8 / (uint32_t)a.groups;
-    const uint32_t us = turn8 * 8 + (b & 7);
-    const int g = (int)(b / 8 - turn8 * (uint32_t)a.groups);
-    if (us >= (uint32_t)(a.units * a.shares))
+    // Workgroups are dealt to the 8 XCDs in turn: each XCD takes a run of
+    // neighbours, so that its L2 serves the rows of one selection and share to
+    // all their blocks, and those of a verification block to its queries.
+    // (With selections and shares dealt to the XCDs in turn instead, the verify
+    // block above took 54 us instead of 51, and one request of 64 x 128 query
+    // rows, which then ran on one XCD, 543 instead of 76.)
+    const uint32_t total = (uint32_t)(a.units * a.shares) * (uint32_t)a.groups;
+    const uint32_t job = (blockIdx.x & 7) * ((total + 7) / 8) + blockIdx.x / 8;
+    if (job >= total)
         return;
+    const uint32_t us = job / (uint32_t)a.groups;
+    const int g = (int)(job - us * (uint32_t)a.groups);
     const int unit = (int)(us / (uint32_t)a.shares), share = (int)us - unit * a.shares;
     const int i = a.c.map ? unit / a.c.nq : unit;
     // The loads that the rows' addresses depend on are issued together (what is
@@ -966,7 +970,7 @@ hipError_t launch_attend(const kvr_ctx *c, const kvr_attend_call &call, const At
     const int64_t parts = (int64_t)a.units * a.shares;
     a.partial = static_cast<float *>(call.workspace);
     a.stat = a.partial ? a.partial + parts * a.unit_rows * call.d_v : nullptr;
-    const dim3 grid((unsigned)((parts + 7) / 8 * 8 * a.groups));
+    const dim3 grid((unsigned)((parts * a.groups + 7) / 8 * 8));
     hipError_t e = call.format == KVR_ROW_FP8    ? launch_format<KVR_ROW_FP8>(c, a, plan.block, grid, s)
                    : call.format == KVR_ROW_BF16 ? launch_format<KVR_ROW_BF16>(c, a, plan.block, grid, s)
                                                  : launch_format<KVR_ROW_F16>(c, a, plan.block, grid, s);

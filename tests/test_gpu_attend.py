@@ -398,6 +398,14 @@ def test_every_share_count():
             check(src, *run(src, 3, 1, 16, stride, count=count)[:5])
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("n,nq,heads,stride", [(1, 16, 100, 70), (3, 40, 33, 130), (9, 2, 17, 64)])
+def test_many_query_rows(fmt, n, nq, heads, stride):
+    """Few selections shared by many blocks of query rows, in numbers that are
+    no multiples of one another."""
+    check(Source(19, n, fmt, 512, 64), *run(Source(19, n, fmt, 512, 64), n, nq, heads, stride)[:5])
+
+
 def test_captured_and_replayed():
     """One captured call, replayed with new contents and eager work between."""
     src = Source(13, 3, "fp8", 512, 64)
