@@ -926,6 +926,9 @@ int64_t partial_bytes(int64_t rows, int32_t d_v) { return rows * (d_v + 2) * (in
 //   shares  256 workgroups (kernel + join): 8 requests of 64 heads, 2048 rows
 //           with 128 of them 22 + 4 us, with 256 18 + 5, with 512 (two rounds)
 //           28 + 9; 64 requests of 16 heads 34 + 4, 25 + 4, 34 + 5
+//           More than 128 blocks stay whole, also where that leaves a round of
+//           few: 65 requests of 128 heads (260 blocks) 140 us, in halves 122 +
+//           14; of 512 rows each 49, in halves 55 + 14
 AttendPlan attend_plan(int32_t n, int32_t nq, int32_t heads, int32_t d_v, int32_t rows, bool mapped)
 {
     AttendPlan p{};
