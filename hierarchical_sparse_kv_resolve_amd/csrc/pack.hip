@@ -123,12 +123,21 @@ __global__ __launch_bounds__(NT) void pack_kernel(PackArgs a, bool wide)
             float scale = top / kE4m3Max;
             scale = scale == 0.f ? 1.f : scale;
             // by the reciprocal (two roundings instead of one, both far below a
-            // code's), except where that would overflow
+            // code's), except where that would overflow.  A subnormal scale is a
+            // whole number of 2^-149 and may be up to a third too small: its
+            // quotients are held to the largest code (a NaN stays one).
             const float inv = 1.f / scale;
-            const bool tiny = __any(scale < kTinyScale);
+            if (__any(scale < kTinyScale)) {
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                x[i] = tiny ? x[i] / scale : x[i] * inv;
+                for (int i = 0; i < N; ++i) {
+                    const float y = x[i] / scale;
+                    x[i] = y > kE4m3Max ? kE4m3Max : y < -kE4m3Max ? -kE4m3Max : y;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    x[i] *= inv;
+            }
             uint32_t code[N / 4];
 #pragma unroll
             for (int i = 0; i < N; i += 4)

@@ -476,7 +476,10 @@ typedef struct kvr_pack_call {
  * kvr_append_rows, a host store or the optional pool.  x is rounded once, to
  * nearest, to the row's 16-bit type; in fp8 rows each group of 128 values has
  * scale = max|x| / 448 (1 for a group of zeros) and codes e4m3(x / scale)
- * (the quotient to 32-bit accuracy).
+ * (the quotient to 32-bit accuracy).  A scale below the smallest normal 32-bit
+ * value is a whole number of 2^-149; quotients by one that is too small for
+ * its group become the largest code, and one that rounds to 0 makes a group
+ * of zeros.
  * The rope part is rounded to 16 bits as it is.  A NaN or an infinity makes
  * its own scale group (its own value, in 16-bit rows; the whole latent when
  * it is normalised) NaN or infinite, no other.  One kernel; n = 0 is a no-op. */

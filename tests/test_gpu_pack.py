@@ -126,6 +126,44 @@ def test_zeros_and_extremes():
     check(pack("fp8", 512, 64, y, rope[:3], w, 1e-6), "fp8", 512, 64, y, rope[:3], w, 1e-6)
 
 
+@pytest.mark.parametrize("d_v", [512, 256])
+@pytest.mark.parametrize("norm", [False, True])
+def test_groups_of_subnormal_scale(d_v, norm):
+    """Groups whose largest value is u steps of 2^-149: the scale u / 448 steps
+    rounds to whole steps (to none below 224, a group of zeros then) and the
+    quotient may exceed the largest code.  Every code is finite, and a value is
+    off by half a step of its code, or by what the largest code times the scale
+    cannot reach, 448 times half a step of the scale; a NaN stays in its group."""
+    step = 2.0 ** -149
+    tops = [1, 3, 200, 223, 225, 300, 447, 448, 500, 627, 671, 673, 700, 1000, 2000, 5000, 1 << 16,
+            1 << 22]
+    rng = np.random.default_rng(8)
+    groups = d_v // 128
+    u = np.array([[tops[(i + g) % len(tops)] for g in range(groups)] for i in range(len(tops))])
+    x = np.floor(rng.random((len(tops), groups, 128)) * (u[..., None] + 1))
+    x[:, :, 5] = u
+    x = torch.from_numpy(x * np.where(rng.random(x.shape) < 0.5, -1, 1)).view(len(tops), d_v)
+    latent, w = (x * step).float().cuda(), None
+    assert torch.equal(latent.cpu().double(), x * step)
+    if norm:  # latents of 1 and such weights: one product each, the same for all rows
+        x = x[9:10].expand(len(tops), d_v)
+        latent, w = torch.ones(len(tops), d_v, device="cuda"), (x[0] * step).float().cuda()
+    rope = torch.zeros(len(tops), 64, device="cuda")
+    rows = pack("fp8", d_v, 64, latent, rope, w, 0.0)
+    got = ref.unpack(rows, "fp8", d_v, 64)[:, :d_v] / step
+    assert got.isfinite().all()
+    top = x.reshape(len(tops), groups, 128).abs().amax(2).repeat_interleave(128, 1)
+    # half a code's step (2^-4 relative; 2^-10 of the scale for the smallest codes), the rest
+    tol = 2.0 ** -4 * x.abs() + 2.0 ** -10 * (top / 448 + 0.5) + 448 * 0.5
+    assert ((got - x).abs() <= tol).all()
+    if not norm:
+        latent[9, 7] = float("nan")
+        bad = ref.unpack(pack("fp8", d_v, 64, latent, rope), "fp8", d_v, 64)[:, :d_v] / step
+        assert not bad[9, :128].isfinite().any()
+        bad[9, :128] = got[9, :128]
+        assert torch.equal(bad, got)
+
+
 def test_nan_and_infinity_stay_in_their_group():
     x = torch.randn(3, 512)
     y = x.clone()
