@@ -154,6 +154,20 @@ __device__ void fork_metadata(const ForkArgs &a, int i, int32_t s, int32_t d)
     }
 }
 
+// Whether row pos of request s has a host copy.
+__device__ __forceinline__ bool host_copy(const ForkArgs &a, int32_t s, int32_t pos)
+{
+    const Shape &sh = a.sh;
+    return pos < a.m.L[s] && pos < sh.host_rows &&
+           (pos >= sh.H || a.m.host_valid[(int64_t)s * sh.n_pages + pos / sh.P]);
+}
+
+// A slot's tag is written by the resolve, its bytes by the fills that follow
+// it, in each layer at its own time.  So slots that the source's last resolve
+// used (their stamp is its clock) are read from their rows' host copies, which
+// is what its fills bring.  (Without a host copy such a slot is not waiting for
+// a fill: it is itself a copy, in a request forked since that resolve.)
+//
 // Jobs: per pair one of metadata, then row tiles of every layer: host rows
 // first (the host link is the slow side), then hot slots and the tail.  No
 // source is a destination of the same call, so what a job reads is not
@@ -212,14 +226,20 @@ __global__ __launch_bounds__(NT) void fork_kernel(ForkArgs a)
         __syncthreads();  // the previous tile's readers are done with sSrc
         if ((int)threadIdx.x < nrows) {
             const int64_t row = j0 + threadIdx.x;
-            bool has = true;
+            const uint8_t *p = from + row * R;
             if (region == 0 && row < sh.H) {
                 const int64_t e = (int64_t)s * sh.n_pages + row / sh.P;
-                has = a.m.page_map[e] < 0 && a.m.host_valid[e];
+                if (a.m.page_map[e] >= 0 || !a.m.host_valid[e])
+                    p = nullptr;
             } else if (region == 1) {
-                has = a.m.tag[(int64_t)s * sh.B + row] >= 0;
+                const int64_t b = (int64_t)s * sh.B + row;
+                const int32_t pos = a.m.tag[b];
+                if (pos < 0)
+                    p = nullptr;
+                else if (a.m.stamp[b] == a.m.clock[s] && host_copy(a, s, pos))
+                    p = lp.host + ((int64_t)s * sh.host_rows + pos) * R;
             }
-            sSrc[threadIdx.x] = has ? from + row * R : nullptr;
+            sSrc[threadIdx.x] = p;
         }
         __syncthreads();
         const int total = nrows * C;

@@ -149,14 +149,15 @@ const char *kvr_last_error(void);
  *   tag       int32  [n_req][B]           row held by a hot slot, -1 = empty
  *   stamp     uint32 [n_req][B]           LRU stamp of a hot slot
  *   clock     uint32 [n_req]              last LRU tick of the request
- * page_map and host_valid change only in kvr_reclaim_pages and
- * kvr_restore_pages. */
+ * page_map and host_valid change only in kvr_reclaim_pages,
+ * kvr_restore_pages and the calls on shared pages (kvr_release_requests,
+ * kvr_fork_requests, kvr_copy_pages, kvr_compact_pool). */
 int kvr_bind_metadata(kvr_ctx *ctx, int32_t *L, int32_t *page_map, uint8_t *host_valid,
                       int32_t *tag, uint32_t *stamp, uint32_t *clock);
 
 /* Bind one payload layer:
  *   tail (device) [n_req][T][R], pool (device) [pool_pages][P][R] (written
- *   only by kvr_restore_pages),
+ *   only by kvr_restore_pages, kvr_copy_pages and kvr_compact_pool),
  *   hot (device) [n_req][B][R], host (pinned) [n_req][H + max_new][R].
  * tail may be NULL when T = 0 and pool when pool_pages = 0. */
 int kvr_bind_layer(kvr_ctx *ctx, int32_t layer, void *tail, void *pool, void *hot,
@@ -587,6 +588,8 @@ int64_t kvr_attend_workspace(int32_t n, int32_t nq, int32_t heads, int32_t d_v, 
  *   its pages go down, page_map becomes -1, host_valid 0, tags -1, stamps 0,
  *   clock 0 and L 0, so that every row of it is out of range until it becomes
  *   the copy of another request or is set up again.  Payload stays as it is.
+ *   What was resolved for a request before (its host fills, gathers, deferred
+ *   appends) must have run before it is set up again or forked into.
  *   status (device) int32 [n] or NULL: KVR_E_ARG (nothing changes) for an id
  *   out of range or one that an earlier entry names.
  * kvr_fork_requests: request dst_ids[i] becomes a copy of src_ids[i]: L,
@@ -595,7 +598,10 @@ int64_t kvr_attend_workspace(int32_t n, int32_t nq, int32_t heads, int32_t d_v, 
  *   that have a host copy and are not ready, and those of decoded rows.  What
  *   dst held before is given up as by kvr_release_requests.  In the copy a
  *   ready page has no host copy (its backup is made when it is reclaimed).
- *   Deferred appends of the source must have been completed.
+ *   The host fills of the source's last resolve may still be outstanding (the
+ *   slots it used are copied from their rows' host copies); fills of earlier
+ *   resolves and deferred appends of the source must have been completed.  A
+ *   drafter's window (kvr_draft_*) is a state of its own and not copied.
  *   src_ids, dst_ids (device) int32 [n]; a request may be the source of several
  *   entries.  status (device) int32 [n] or NULL: KVR_E_ARG (nothing changes)
  *   for an id out of range, a destination that an earlier entry names or a

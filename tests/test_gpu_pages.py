@@ -284,6 +284,97 @@ def test_free_list_and_compaction(seed, kw):
             s.release(1)
 
 
+@pytest.mark.parametrize("seed", [61, 62])
+def test_fork_before_the_fills_have_run(seed):
+    """A fork between a resolve and its fills (of several layers): the copy's hot
+    slots hold their rows' bytes in every layer, whether the fills run later
+    (into the source's slots) or not, and so do those of a copy of the copy,
+    also where a page became ready meanwhile; the copy's next resolve hits them."""
+    s = State(seed, n_req=4, users=1, NL=3, R=48, H=330, P=16, T=21, B=60, new=9, ready=0.4)
+    # one truth: every place holds the row's own bytes
+    byte = s.rng.integers(0, 256, (s.NL, s.H + s.new, s.R), dtype=np.uint8)
+    L = int(s.L[0])
+    for l in range(s.NL):
+        for p in range(s.npg):
+            lo, hi = p * s.P, min(s.H, p * s.P + s.P)
+            if s.page_map[0, p] >= 0:
+                s.dev["pool"][l][int(s.page_map[0, p]), :hi - lo] = torch.from_numpy(byte[l, lo:hi]).cuda()
+            if s.host_valid[0, p]:
+                s.dev["host"][l][0, lo:hi] = torch.from_numpy(byte[l, lo:hi])
+        s.dev["host"][l][0, s.H:L] = torch.from_numpy(byte[l, s.H:L])
+        for pos in range(max(0, L - s.T), L):
+            s.dev["tail"][l][0, pos % s.T] = torch.from_numpy(byte[l, pos]).cuda()
+        s.dev["hot"][l][0] = POISON
+    s.dev["tag"].fill_(-1)
+    s.dev["stamp"].zero_()
+    k, i32 = 32, dict(dtype=torch.int32, device="cuda")
+
+    def resolve(r, sel):
+        out = dict(loc=torch.full((1, k), -1, **i32), fills=torch.zeros(1, s.B, 2, **i32),
+                   count=torch.zeros(1, **i32), status=torch.full((1,), 77, **i32))
+        s.ctx.resolve_rows(1, ints(r), torch.from_numpy(sel.astype(np.int32)[None]).cuda(), None, k,
+                           out["loc"], out["fills"], out["count"], -1, out["status"])
+        torch.cuda.synchronize()
+        assert out["status"].item() == 0
+        return out
+
+    def fill(r, got):
+        s.ctx.reuse_locations(1, list(range(s.NL)), 1, ints(r), got["loc"], None, None, k,
+                              got["fills"], got["count"])
+
+    def slots(r):
+        """Every tagged slot of request r holds its row, in each layer."""
+        torch.cuda.synchronize()
+        tag = s.dev["tag"][r].cpu().numpy()
+        assert (tag >= 0).any()
+        for l in range(s.NL):
+            hot = s.dev["hot"][l][r].cpu().numpy()
+            assert np.array_equal(hot[tag >= 0], byte[l][tag[tag >= 0]]), (r, l)
+
+    def rows(r, sel, got):
+        out = [torch.zeros(1, k, s.R, dtype=torch.uint8, device="cuda") for _ in range(s.NL)]
+        s.ctx.gather_rows(list(range(s.NL)), 1, ints(r), got["loc"], None, k, out)
+        torch.cuda.synchronize()
+        for l in range(s.NL):
+            assert np.array_equal(out[l][0].cpu().numpy(), byte[l][sel]), (r, l)
+
+    away = np.concatenate([np.arange(p * s.P, p * s.P + s.P) for p in range(s.full)
+                           if s.page_map[0, p] < 0])
+    away = away[away < L - s.T]
+    first, second = s.rng.choice(away, k, replace=False), s.rng.choice(away, k, replace=False)
+    second[:20] = first[:20]  # hits among its rows
+    fill(0, resolve(0, first))
+    slots(0)
+    pending = resolve(0, second)
+    assert pending["count"].item() > 0
+    # a page of the pending rows becomes ready
+    p = int(second[-1]) // s.P
+    status = torch.full((1,), 77, **i32)
+    s.ctx.restore_pages(1, ints(0), ints(p), ints(int(np.nonzero(s.refs == 0)[0][0])), status)
+    s.ctx.fork_requests(1, ints(0), ints(1))
+    s.ctx.fork_requests(1, ints(1), ints(2))
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    for r in (1, 2):
+        slots(r)
+    fill(0, pending)  # the source's own
+    for r in (0, 1, 2):
+        slots(r)
+        got = resolve(r, second)
+        assert got["count"].item() == 0
+        rows(r, second, got)
+    # the copy of a request that is resolved again after the fork
+    third = s.rng.choice(away, k, replace=False)
+    got = resolve(2, third)
+    s.ctx.fork_requests(1, ints(2), ints(3))
+    slots(3)
+    fill(2, got)
+    rows(2, third, got)
+    got = resolve(3, third)
+    assert got["count"].item() == 0
+    rows(3, third, got)
+
+
 @pytest.mark.parametrize("seed,P,R,NL", [(41, 64, 1152, 2), (42, 129, 256, 1), (43, 128, 256, 3),
                                           (44, 200, 1152, 1), (45, 16, 4096, 2)])
 def test_long_pages(seed, P, R, NL):
