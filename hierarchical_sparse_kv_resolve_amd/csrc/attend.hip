@@ -9,8 +9,9 @@
 //   t_j = log2(e) * scale * (q . key_j),  p_j = 2^(t_j - m),  l = sum p_j,
 //   out = sum p_j c_j / l,                lse = ln 2 * (m + log2 l)
 // with one pass over the rows: m is a reference at most 8 below the running
-// maximum (so p <= 2^8); when a tile exceeds it, it becomes the maximum and l
-// and the sums are scaled down.
+// maximum (so p <= 2^8; fp16 rows: 4, and every p is raised by 2^11, see
+// Mfma); when a tile exceeds it, it becomes the maximum and l and the sums are
+// scaled down.
 //
 // A workgroup of NW waves owns MB blocks of 16 query rows and a share of the
 // selection, which it walks in tiles of kTile (64) rows, kept in LDS.  Tiles arrive
@@ -69,7 +70,6 @@ namespace kvr {
 namespace {
 
 constexpr int kTile = 64;     // rows per tile
-constexpr float kSlack = 8.f; // log2 of the largest probability kept
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -135,11 +135,18 @@ struct AttendArgs {
     float *stat;        // [units][shares][unit_rows][2]: m, l
 };
 
-// MFMA operands of a 16-bit type.
+// MFMA operands of a 16-bit type.  Probabilities are kept as 2^(t_j - m + kLift),
+// and m is at most kSlack below the running maximum.  bf16 has the exponents of
+// 32 bits and needs no lift.  fp16 ends at 2^16 and has steps of 2^-24, so its
+// probabilities are raised to at most 2^15: the steps are then 2^-35 of the
+// largest probability, and what 2^24 rows (the most a call takes) lose to them
+// stays below 2^-12 of the largest value.  (Without the lift 2^18 rows of weight
+// 2^-25 each, a hundredth of the result together, were lost.)
 template <typename E>
 struct Mfma;
 template <>
 struct Mfma<__bf16> {
+    static constexpr float kSlack = 8.f, kLift = 0.f;
     typedef __bf16 frag __attribute__((ext_vector_type(8)));
     static __device__ __forceinline__ f32x4 mul(frag a, frag b, f32x4 c)
     {
@@ -148,6 +155,7 @@ struct Mfma<__bf16> {
 };
 template <>
 struct Mfma<_Float16> {
+    static constexpr float kSlack = 4.f, kLift = 11.f;
     typedef _Float16 frag __attribute__((ext_vector_type(8)));
     static __device__ __forceinline__ f32x4 mul(frag a, frag b, f32x4 c)
     {
@@ -501,13 +509,14 @@ __global__ __launch_bounds__(MB * kTile * 4) void attend_kernel(AttendArgs a)
 
     // Probabilities of the wave's block of tile t, into LDS, rounded to the 16
     // bits that the matrix instructions take (off by at most 2^-8 of each for
-    // bf16, 2^-11 for fp16; their sum l is taken before the rounding).
+    // bf16, 2^-11 for fp16 or 2^-36 of the largest; their sum l is taken before
+    // the rounding).
     auto pchunk = [&](int head, int chunk) {  // 8 rows of a query row, swizzled
         return (chunk ^ (head & 7)) * 8;
     };
     auto write_p = [&](int t, const f32x4 *w) __attribute__((always_inline)) {
         const int pb = BUFS == 3 ? t & 1 : 0;
-        const float ref = m_own == -__builtin_inff() ? 0.f : m_own;
+        const float ref = m_own == -__builtin_inff() ? 0.f : m_own - M::kLift;
         float p[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -536,7 +545,7 @@ __global__ __launch_bounds__(MB * kTile * 4) void attend_kernel(AttendArgs a)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             s[k] = (counts >> k) & 1 ? s[k] * to_log2 : -__builtin_inff();
-            exceeds |= s[k] > m_own + kSlack;
+            exceeds |= s[k] > m_own + M::kSlack;
         }
         sExceeds[__any(exceeds) ? flag : 3] = 1;
         write_p(t, w);
@@ -780,7 +789,7 @@ __global__ __launch_bounds__(MB * kTile * 4) void attend_kernel(AttendArgs a)
         if (a.shares > 1) {
             const int64_t ps = (int64_t)us * a.unit_rows + x;
             if (wave == 0 && grp == 0)
-                *reinterpret_cast<float2 *>(a.stat + 2 * ps) = make_float2(m[mb], sum);
+                *reinterpret_cast<float2 *>(a.stat + 2 * ps) = make_float2(m[mb] - M::kLift, sum);
             if (m[mb] == -__builtin_inff() && sum == 0.f)
                 continue;  // an empty share: its sums are not read
 #pragma unroll
@@ -790,7 +799,7 @@ __global__ __launch_bounds__(MB * kTile * 4) void attend_kernel(AttendArgs a)
         }
         const float inv = m[mb] == -__builtin_inff() && sum == 0.f ? 0.f : 1.f / sum;
         if (wave == 0 && grp == 0 && a.c.lse)
-            a.c.lse[at] = 0.69314718055994530942f * (m[mb] + __log2f(sum));
+            a.c.lse[at] = 0.69314718055994530942f * (m[mb] - M::kLift + __log2f(sum));
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             typedef E e4 __attribute__((ext_vector_type(4)));

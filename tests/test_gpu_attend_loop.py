@@ -250,3 +250,38 @@ def test_infinite_scores_and_nan_in_late_tiles(fmt, d_v, shape):
     check(src, q[:1, :, ok], out[:1, :, ok], lse[:1, :, ok],
           [[keys[without] for keys in lists[0]]], 0.07)
     check(src, q[pick[1:]], out[pick[1:]], lse[pick[1:]], lists[1:], 0.07)
+
+
+def test_many_rows_of_small_weight():
+    """2^18 fp16 rows a workgroup, each with a probability far below fp16's
+    normal range, which together weigh up to half: two kinds of rows, so the
+    result is their weighted mean in closed form.
+
+    Tolerances, of values of size 1.5 at most: 2^-11 for the probabilities and
+    2^-11 for the result, and sums of 2^18 terms, 64 of them at a time for l and
+    32 in one product for the values: at most 2^13 additions of 2^-24 each."""
+    d_v, heads, nq, stride = 256, 4096, 2, 1 << 18
+    src = Source(600, 1, "f16", d_v, 64, B=2)
+    one = torch.zeros(2, d_v + 64, dtype=torch.float64)
+    one[0, :d_v] = torch.linspace(1.0, 1.5, d_v)
+    one[1, :d_v] = -torch.linspace(1.5, 0.75, d_v)
+    one[0, d_v] = 16.0
+    src.hot[0].copy_(one.half().view(torch.uint8).view(1, 2, src.R))
+    keys = ref.unpack(src.hot[0][0], "f16", d_v, 64)
+    words = np.full((1, stride), (2 << 30) | 1, np.int64)
+    words[0, 77] = 2 << 30
+    # scores of the first row over the others': log2 18 to 27
+    q = torch.zeros(1, nq, heads, d_v + 64, device="cuda")
+    q[..., d_v] = torch.linspace(18.0, 27.0, nq * heads, device="cuda").view(nq, heads)
+    q = q.half()
+    scale = float(np.log(2.0) / 16)
+    out, lse, _ = attend(src, 1, nq, heads, stride, q, scale, words=words)
+    s = (q[0].cpu().double() @ keys.T) * np.float64(np.float32(scale))
+    w = torch.exp(s[..., 1] - s[..., 0]) * (stride - 1)
+    want = (keys[0, :d_v] + w[..., None] * keys[1, :d_v]) / (1 + w[..., None])
+    size = 1.5
+    tol = (2 * HALF["f16"] + 2 * 2 ** 13 * EPS32) * size
+    err = (out[0].cpu().double() - want).abs()
+    assert float(err.max()) <= tol, float(err.max() / tol)
+    want_lse = s[..., 0] + torch.log1p(w)
+    assert ((lse[0].cpu().double() - want_lse).abs() <= (2 ** 13 + 64) * EPS32 * (1 + want_lse)).all()
