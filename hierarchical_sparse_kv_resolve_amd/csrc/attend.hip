@@ -9,7 +9,7 @@
 //   t_j = log2(e) * scale * (q . key_j),  p_j = 2^(t_j - m),  l = sum p_j,
 //   out = sum p_j c_j / l,                lse = ln 2 * (m + log2 l)
 // with one pass over the rows: m is a reference at most 8 below the running
-// maximum (so p <= 2^8; fp16 rows: 4, and every p is raised by 2^11, see
+// maximum (so p <= 2^8; fp16 rows: 6, and every p is raised by 2^9, see
 // Mfma); when a tile exceeds it, it becomes the maximum and l and the sums are
 // scaled down.
 //
@@ -138,10 +138,12 @@ struct AttendArgs {
 // MFMA operands of a 16-bit type.  Probabilities are kept as 2^(t_j - m + kLift),
 // and m is at most kSlack below the running maximum.  bf16 has the exponents of
 // 32 bits and needs no lift.  fp16 ends at 2^16 and has steps of 2^-24, so its
-// probabilities are raised to at most 2^15: the steps are then 2^-35 of the
-// largest probability, and what 2^24 rows (the most a call takes) lose to them
-// stays below 2^-12 of the largest value.  (Without the lift 2^18 rows of weight
-// 2^-25 each, a hundredth of the result together, were lost.)
+// probabilities are raised to at most 2^15: the steps are then 2^-33 of the
+// largest probability, and what 2^22 rows lose to them stays below 2^-12 of the
+// largest value (2^24, the most a call takes: 2^-10).  Without the lift 2^18
+// rows of weight 2^-25 each, a hundredth of the result together, were lost.
+// (The ragged fp16 case: 19.2 us without a lift and slack 8, 19.2 with slack 6
+// and lift 9, 20.3 with slack 4 and lift 11, where sums are scaled more often.)
 template <typename E>
 struct Mfma;
 template <>
@@ -155,7 +157,7 @@ struct Mfma<__bf16> {
 };
 template <>
 struct Mfma<_Float16> {
-    static constexpr float kSlack = 4.f, kLift = 11.f;
+    static constexpr float kSlack = 6.f, kLift = 9.f;
     typedef _Float16 frag __attribute__((ext_vector_type(8)));
     static __device__ __forceinline__ f32x4 mul(frag a, frag b, f32x4 c)
     {
@@ -509,7 +511,7 @@ __global__ __launch_bounds__(MB * kTile * 4) void attend_kernel(AttendArgs a)
 
     // Probabilities of the wave's block of tile t, into LDS, rounded to the 16
     // bits that the matrix instructions take (off by at most 2^-8 of each for
-    // bf16, 2^-11 for fp16 or 2^-36 of the largest; their sum l is taken before
+    // bf16, 2^-11 for fp16 or 2^-34 of the largest; their sum l is taken before
     // the rounding).
     auto pchunk = [&](int head, int chunk) {  // 8 rows of a query row, swizzled
         return (chunk ^ (head & 7)) * 8;

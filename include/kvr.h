@@ -552,7 +552,7 @@ typedef struct kvr_attend_call {
  * a row that takes part shows in the result.  Products of 16-bit values (an
  * e4m3 code is exact in bf16), sums, maxima and exponentials in 32 bits;
  * probabilities are rounded to 16 bits before their product with the values
- * (off by at most 2^-8 of each, with fp16 rows by 2^-11 of it or 2^-36 of the
+ * (off by at most 2^-8 of each, with fp16 rows by 2^-11 of it or 2^-34 of the
  * largest).
  * A selection may be cut into shares that are attended to apart and joined in
  * a fixed order: results do not vary from run to run (another n, nq or heads
