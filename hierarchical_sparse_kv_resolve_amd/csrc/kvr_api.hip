@@ -971,9 +971,15 @@ int kvr_attend_rows(kvr_ctx *ctx, const kvr_attend_call *call, void *stream)
         return rc;
     if (a.stride > (1 << 24))
         return fail(KVR_E_ARG, "stride above 2^24");
-    if (!a.rows)
+    if (!a.rows) {
         if (int rc = check_layer(ctx, a.layer))
             return rc;
+        const kvr::LayerPtrs &lp = ctx->layers_h[a.layer];
+        if ((reinterpret_cast<uintptr_t>(lp.tail) | reinterpret_cast<uintptr_t>(lp.pool) |
+             reinterpret_cast<uintptr_t>(lp.hot)) % 16 != 0)
+            return fail(KVR_E_ARG, "layer %d's tail, pool or hot cache is not aligned to 16 bytes",
+                        a.layer);
+    }
     if (a.n > 0 && (!a.q || !a.out || (a.stride > 0 && !a.rows && !a.loc)))
         return fail(KVR_E_ARG, "q, out and rows or loc are required");
     if (a.q_stride_entry < 0 || a.q_stride_query < 0 || a.q_stride_head < 0)

@@ -491,8 +491,8 @@ int kvr_pack_rows(kvr_ctx *ctx, const kvr_pack_call *call, void *stream);
  *   rows, loc: where row j of request entry i is read.  rows (device)
  *     [n][stride][R] is a gathered buffer (kvr_gather_rows' out; aligned to 16
  *     bytes); with rows NULL the row is read where loc[i][j] names it in
- *     `layer` (tail, optional pool or hot cache; a fresh row's host fill must
- *     have run).  loc (device) uint32 [n][stride] is required with rows NULL;
+ *     `layer` (tail, optional pool or hot cache, here aligned to 16 bytes; a
+ *     fresh row's host fill must have run).  loc (device) uint32 [n][stride] is required with rows NULL;
  *     otherwise it may be NULL.  Entries whose word is KVR_LOC_INVALID are
  *     left out of the attention in both cases.
  *   count (device) int32 [n] or NULL (= stride): only entries j < count[i]

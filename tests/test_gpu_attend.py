@@ -506,3 +506,24 @@ def test_refusals():
         src.ctx.attend_rows(**{**good, "n": 3, "q": torch.cat([q, q[:1]]),
                                "out": torch.cat([out, out[:1]]), "loc": torch.cat([loc, loc[:1]])})
     assert out.isfinite().all()
+
+
+@pytest.mark.parametrize("part", ["tail", "pool", "hot"])
+def test_layer_buffers_off_16_bytes_are_refused(part):
+    """A layer bound 8 bytes off is refused before anything is launched; gathered
+    rows do not read it."""
+    from hierarchical_sparse_kv_resolve_amd import KvrError
+    src = Source(20, 2, "bf16", 512, 64)
+    bufs = {k: getattr(src, k)[0] for k in ("tail", "pool", "hot")}
+    flat = torch.zeros(bufs[part].numel() + 16, dtype=torch.uint8, device="cuda")
+    src.ctx.bind_layer(0, **{**bufs, part: flat[8:-8]}, host=src.host[0])
+    q = torch.zeros(2, 1, 16, 576, dtype=torch.bfloat16, device="cuda")
+    out = torch.full((2, 1, 16, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    kw = dict(fmt="bf16", d_v=512, d_rope=64, scale=0.1, stride=40)
+    with pytest.raises(KvrError, match="not aligned to 16 bytes"):
+        src.ctx.attend_rows(0, 2, None, q, out, **kw,
+                            loc=torch.zeros(2, 40, dtype=torch.int32, device="cuda"))
+    assert (out == 7).all()
+    src.ctx.attend_rows(0, 2, None, q, out, **kw,
+                        rows=torch.zeros(2, 40, src.R, dtype=torch.uint8, device="cuda"))
+    assert (out == 0).all()
