@@ -39,29 +39,31 @@
 //
 // Rows left out are read from a row of zeros and their p is 0.
 //
-// What bounds it (one MI355X; the kernel, then the join of the shares; calls
-// over the same inputs, a few percent more over changing ones):
+// What bounds it (one MI355X, calls over changing inputs; the kernel, then the
+// join of the shares):
 // with few query rows a selection, reading the rows,
-//   64 requests x 16 heads x 2048 fp8 rows of 656 bytes     25 + 4 us, 3.4 TB/s
+//   64 requests x 16 heads x 2048 fp8 rows of 656 bytes     28 + 5 us, 3.1 TB/s
 //   32 requests x 4 queries x 16 heads x 2048 bf16 rows of a union of 3277,
-//   each query its own rows                        50 + 6 us, 6.0 TB/s read
-//   (from HBM only the union once, 121 MB);
+//   each query its own rows                        49 + 6 us, 6.1 TB/s read
+//   (302 MB through the L2s, which miss 241 MB of it: twice the union's 121);
 // with many, the vector, matrix and LDS instructions of two waves a SIMD,
-//   64 requests x 128 heads x 2048 fp8 rows        75 us, 480 TFLOP/s
-//   (0.40 of what a large bf16 product reaches): a tile takes about 5800
-//   cycles, of which a SIMD's vector instructions (exponentials, widened
-//   codes, addresses) are 2540, its matrix instructions 1088 and the LDS' reads
-//   2100, and two waves in order overlap them only in part;
+//   64 requests x 128 heads x 2048 fp8 rows        77 us, 475 TFLOP/s
+//   (0.40 of what a large bf16 product reaches): by its counters a tile takes
+//   5000 cycles, of which a SIMD's vector instructions (exponentials, widened
+//   codes, addresses) issue for 2550 and its matrix unit works for 1090, and
+//   the LDS is busy for 1890, 580 of them bank conflicts; a wave waits for its
+//   turn to issue in 26 % of its cycles and at barriers and counters in 35 %;
 // with few rows in all, latency: one request x 16 heads x 256 rows takes
 //   10 + 4 us (an empty kernel 4), four dependent loads (lists, words, rows)
 //   and one tile.
 //
-// Split, block and buffers (128 heads as above): scores split over the waves
-// by dimension, two barriers a tile 89 us; 64 query rows and 8 waves 77 and a
-// join of 9; 16 waves of 128 registers 110; 4 waves of 512 registers 92; two
-// workgroups a compute unit 90; 32 query rows, 8 waves and tiles of 64 rows 75
-// (taken).  Tiles of 32 rows took longer in blocks of 16 query rows too (the
-// 16-head cases above 28 instead of 26 and 59 instead of 53 us).
+// Split, block and buffers, each against the form of the kernel that it was
+// tried on (128 heads as above, the present form then 75 us): scores split over
+// the waves by dimension, two barriers a tile 89 us; 64 query rows and 8 waves
+// 77 and a join of 9; 16 waves of 128 registers 110; 4 waves of 512 registers
+// 92; two workgroups a compute unit 90; 32 query rows, 8 waves and tiles of 64
+// rows 75 (taken).  Tiles of 32 rows took longer in blocks of 16 query rows too
+// (the 16-head cases above 28 instead of 26 and 59 instead of 53 us then).
 #include "block.h"
 #include "kvr_internal.h"
 #include "rowformat.h"
@@ -817,8 +819,8 @@ __global__ __launch_bounds__(MB * kTile * 4) void attend_kernel(AttendArgs a)
 // Joins the shares of each query row: a workgroup per row, its waves taking
 // every fourth share with several in flight, their sums added in wave order.
 // Bound by the latency of reading them: 16 shares of 512 query rows (17 MB) in
-// 5.4 us, of which an empty launch is 4; one wave reading one share after the
-// other took 19 us for 32 shares.
+// 5.3 us, of which an empty launch is 4, 32 shares in 9.0; one wave a row that
+// reads one share after the other took 9.0 and 16.4.
 constexpr int kJoinWaves = 4;
 template <typename E, int DV>
 __global__ __launch_bounds__(kJoinWaves * 64) void join_kernel(AttendArgs a)
@@ -894,7 +896,7 @@ template <int FMT, int DV, int DR>
 hipError_t launch_dims(const kvr_ctx *c, const AttendArgs &a, int block, dim3 grid, hipStream_t s)
 {
     // Three tiles where LDS holds them (64 16-bit rows of 576 values are 72 KB):
-    // 64 requests of 128 heads, fp8 rows, take 75 us with three, 79 with two.
+    // 64 requests of 128 heads, fp8 rows, took 75 us with three, 79 with two.
     constexpr int kBufs = FMT == KVR_ROW_FP8 || DV == 256 ? 3 : 2;
     if (block == 16)
         return launch(c, KVR_KERNEL_ATTEND, attend_kernel<FMT, DV, DR, 1, kBufs>, grid,
@@ -930,16 +932,23 @@ int64_t partial_bytes(int64_t rows, int32_t d_v) { return rows * (d_v + 2) * (in
 // A selection shared by unit_rows query rows is cut into blocks of 16 or 32 of
 // them, and into shares (of at least one tile) until every compute unit has a
 // workgroup.
-//   block   16 when that holds all the rows: a block of 32 would do the work of
-//           twice as many (64 requests of 16 heads: 25 us against 28); more rows
-//           go to blocks of 32, which read each tile half as often (64 requests
-//           of 128 heads: 75 us against 120, 8 requests of 64 heads 18 against 19)
+//   block   16 when that holds all the rows, else 32, which reads each tile half
+//           as often: 64 requests of 128 heads 76 us against 124 in blocks of
+//           16; 64 requests of 16 heads 27 us in either.  (8 requests of 64
+//           heads over 16-bit rows do better in blocks of 16 with half as many
+//           shares: 19 + 4 us instead of 21 + 5.)
 //   shares  256 workgroups (kernel + join): 8 requests of 64 heads, 2048 rows
-//           with 128 of them 22 + 4 us, with 256 18 + 5, with 512 (two rounds)
-//           28 + 9; 64 requests of 16 heads 34 + 4, 25 + 4, 34 + 5
-//           More than 128 blocks stay whole, also where that leaves a round of
-//           few: 65 requests of 128 heads (260 blocks) 140 us, in halves 122 +
-//           14; of 512 rows each 49, in halves 55 + 14
+//           with 128 of them 22 + 4 us, with 256 21 + 5, with 512 (two rounds)
+//           33 + 9; 64 requests of 16 heads 37 + 4, 27 + 4, 34 + 5
+//           More than 128 blocks stay whole.  129 to 255 of them leave compute
+//           units idle, and the others run faster for it (132 blocks of 32 fp8
+//           tiles 70 us, 252 of them 74): requests of 128 heads over 2048 rows
+//           whole | in halves | in thirds
+//             33   70 | 79 + 8  | 60 + 9       40   70 | 79 + 9 | 62 + 10
+//             48   71 | 81 + 11 | 89 + 12      63   74 | 83 + 14
+//             65  138 | 118 + 14 | 118 + 15    96  141 | 124 + 19 | 153 + 21
+//           over 512 rows 33: 26 | - | 34 + 9, 65: 50 | 54 + 14; 129 requests
+//           of 16 heads 70 | - | 63 + 6
 AttendPlan attend_plan(int32_t n, int32_t nq, int32_t heads, int32_t d_v, int32_t rows, bool mapped)
 {
     AttendPlan p{};

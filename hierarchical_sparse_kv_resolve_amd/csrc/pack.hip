@@ -12,9 +12,10 @@
 // group of 128 is 16 lanes (d_v 512) or 32 lanes (d_v 256) and its maximum is
 // a few lane exchanges.  One pass over the data, the next row's loads issued
 // before a row is worked on, bound by HBM: 131072 rows of 512 + 64 bf16 values
-// to fp8 (237 MB) in 49 us, 4.8 TB/s (43 when inputs are left in the cache by
-// the call before; so measured, a division for each value took 54 us, bound by
-// vector instructions, and without the early loads it took 59).
+// to fp8 (237 MB) in 47 us, 5.0 TB/s, to fp16 (302 MB) in 55 us, 5.5 TB/s.
+// (With inputs left in the cache by the call before, a division for each value
+// took 54 us, bound by vector instructions, where the reciprocal took 43, and
+// without the early loads it took 59.)
 #include "block.h"
 #include "kvr_internal.h"
 #include "rowformat.h"
@@ -50,8 +51,8 @@ __device__ __forceinline__ float to_f32<__bf16>(__bf16 x) { return (float)x; }
 template <>
 __device__ __forceinline__ float to_f32<_Float16>(_Float16 x) { return (float)x; }
 
-// N consecutive values; `wide`: the address is aligned to 16 bytes (or to all
-// of them, if they are fewer).
+// N consecutive values; `wide`: the address is aligned to all of them (8 to 32
+// bytes).
 template <int N, typename T>
 __device__ __forceinline__ void load_values(const T *p, bool wide, float (&x)[N])
 {

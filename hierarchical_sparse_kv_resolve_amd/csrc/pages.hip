@@ -15,15 +15,18 @@
 // by the memory it moves.  Measured on one MI355X:
 //   fork      one request of 4096 rows of 1152 bytes, half of its pages ready
 //             (2.4 MB read from and written to host memory, 1.2 MB of HBM
-//             copies): 87 us; four requests of 8192 rows, two layers (22 MB each
-//             way over the host link): 565 us, 80 GB/s of both directions (a
-//             copy engine reaches 57 each way, two at once 57 together).  A tile
-//             of rows per workgroup; workers in a loop (16 to 256) and 2 to 8
-//             chunks a lane were no faster.
+//             copies): 88 us; four requests of 8192 rows, two layers (22 MB each
+//             way over the host link): 562 us, 80 GB/s of both directions (a
+//             copy engine reaches 57 each way, two at once 57 together), 594
+//             where the last resolve used half of the hot slots, whose rows are
+//             then read from the host.  A tile of rows per workgroup; workers
+//             in a loop (16 to 256) and 2 to 8 chunks a lane were no faster.
 //   compact   256 pages of 73 KB, 30 % free: 8 us to rank them, 5 to move about
 //             50 (an empty kernel 4); 16384 pages of 42 KB, about 3440 of them
 //             moved (289 MB): 6 + 10 us to count and rank, 60 to move, 4.8 TB/s
-//   copies    32 pages of 73 KB, two layers: 7 + 4 us
+//   copies    32 pages of 73 KB, two layers: 9 + 5 us in a trace of single
+//             calls, 7 + 4 by events among calls issued back to back
+//   counts    64 requests' maps over 16384 pages: 1.8 + 2.7 us
 #include "kvr_internal.h"
 #include "rows.h"
 
@@ -274,8 +277,8 @@ constexpr int kPartChunks = NT * kUnroll;  // 16-byte chunks a workgroup moves a
 
 // Workgroups that share a page, given how many jobs (pages times layers) there
 // are at most: one if those fill the card, else up to one for each 32 KB.  (32
-// pages of 73 KB, two layers: 10 us with one, 6 with three; a compaction of 256
-// such pages: 7 and 5 us.)
+// pages of 73 KB, two layers, back to back: 13 us with one, 7 with three; the
+// moves of a compaction of 256 such pages: 6 and 5 us.)
 int page_parts(const Shape &sh, int64_t jobs)
 {
     const int64_t most = ((int64_t)sh.P * sh.R / 16 + kPartChunks - 1) / kPartChunks;

@@ -673,10 +673,15 @@ class Context:
         _check(lib().kvr_count_page_refs(self.handle, _stream(stream)))
 
     def release_requests(self, n, req_ids, status=None, stream=None):
+        """Each listed request gives up its rows and pages.  What was resolved for
+        it before must have run before it is set up again or forked into."""
         _check(lib().kvr_release_requests(self.handle, n, _words(req_ids, "req_ids", n),
                                           _words(status, "status", n), _stream(stream)))
 
     def fork_requests(self, n, src_ids, dst_ids, status=None, stream=None):
+        """Request dst_ids[i] becomes a copy of src_ids[i].  The host fills of the
+        source's last resolve may be outstanding; those of earlier ones, deferred
+        appends and what was resolved for dst_ids[i] must have run."""
         _check(lib().kvr_fork_requests(self.handle, n, _words(src_ids, "src_ids", n),
                                        _words(dst_ids, "dst_ids", n),
                                        _words(status, "status", n), _stream(stream)))
