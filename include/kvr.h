@@ -456,8 +456,9 @@ int kvr_row_layout(int32_t format, int32_t d_v, int32_t d_rope);
  *     elements apart; rope [n][d_rope] likewise (NULL when d_rope is 0);
  *     slices of one projection's output are taken as they are
  *   weight (device) float [d_v] or NULL: with it the latent is normalised,
- *     x = latent / sqrt(mean(latent^2) + eps) * weight (sums in 32 bits);
- *     without it x = latent */
+ *     x = latent / sqrt(mean(latent^2) + eps) * weight (sums in 32 bits, so
+ *     latents above about 8e17 overflow them and become 0); without it
+ *     x = latent */
 typedef struct kvr_pack_call {
     int32_t format;      /* kvr_row_format */
     int32_t value_type;  /* kvr_value_type */

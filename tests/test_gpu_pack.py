@@ -126,6 +126,17 @@ def test_zeros_and_extremes():
     check(pack("fp8", 512, 64, y, rope[:3], w, 1e-6), "fp8", 512, 64, y, rope[:3], w, 1e-6)
 
 
+def test_norm_past_the_32_bit_range():
+    """A row whose squares overflow 32 bits becomes 0, its neighbours keep theirs."""
+    latent = torch.randn(3, 512, device="cuda")
+    latent[1] *= 1e20
+    rope, w = torch.zeros(3, 64, device="cuda"), torch.ones(512, device="cuda")
+    got = ref.unpack(pack("bf16", 512, 64, latent, rope, w, 1e-6), "bf16", 512, 64)
+    assert (got[1] == 0).all()
+    keep = pack("bf16", 512, 64, latent[[0, 2]], rope[[0, 2]], w, 1e-6)
+    assert torch.equal(got[[0, 2]], ref.unpack(keep, "bf16", 512, 64))
+
+
 @pytest.mark.parametrize("d_v", [512, 256])
 @pytest.mark.parametrize("norm", [False, True])
 def test_groups_of_subnormal_scale(d_v, norm):

@@ -213,6 +213,29 @@ def test_reclaim_and_restore_with_counts():
     assert status.item() == 0
 
 
+def test_shared_page_reclaimed_by_all_in_one_call():
+    """Every entry of a shared page lets it go in one call: each gets its own host
+    copy, each names the page, and it is free."""
+    s = State(63, ready=0.6)
+    s.ctx.fork_requests(2, ints(0, 0), ints(1, 4))
+    s.fork(0, 1)
+    s.fork(0, 4)
+    p = int(np.nonzero(s.page_map[0] >= 0)[0][0])
+    ph = int(s.page_map[0, p])
+    assert s.refs[ph] == 3
+    freed = torch.full((4,), 77, dtype=torch.int32, device="cuda")
+    status = torch.full((4,), 77, dtype=torch.int32, device="cuda")
+    s.ctx.reclaim_pages(4, ints(1, 0, 4, 0), ints(p, p, p, p), freed, status)
+    for r in (0, 1, 4):
+        if not s.host_valid[r, p]:
+            for l in range(s.NL):
+                s.host[l][r, p * s.P:(p + 1) * s.P] = s.pool[l][ph]
+        s.host_valid[r, p], s.page_map[r, p] = 1, -1
+    s.refs[ph] = 0
+    s.check()
+    assert freed.cpu().tolist() == [ph, ph, ph, -1] and status.cpu().tolist() == [0] * 4
+
+
 def test_copy_pages():
     """Shared pages become the entries' own; bad entries change nothing."""
     s = State(14, ready=0.6)
