@@ -1,6 +1,7 @@
 // C ABI of the gfx950 sparse KV row resolver: argument checking, context
 // state and launch sequencing.  Every entry point returns a kvr_status and
 // records a message for kvr_last_error(); no exception crosses the ABI.
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -9,6 +10,7 @@
 
 #include "kvr_internal.h"
 #include "rowformat.h"
+#include "values.h"
 
 namespace kvr {
 bool tile_magic_exact(int32_t row_bytes);
@@ -1003,6 +1005,169 @@ int kvr_attend_rows(kvr_ctx *ctx, const kvr_attend_call *call, void *stream)
     }
     hipError_t e = kvr::launch_attend(ctx, a, plan, s);
     return e == hipSuccess ? ok() : hip_fail(e, "attention launch");
+}
+
+// ------------------------------------------------- positions and scores
+
+static int check_rotate_part(const kvr_rotate_call &c, const kvr_rotate_part &p, const char *name)
+{
+    if (p.heads < 0 || p.heads >= (1 << 24) || p.reserved != 0)
+        return fail(KVR_E_ARG, "%s: heads must be in [0, 2^24) and reserved 0", name);
+    if (p.heads == 0)
+        return KVR_OK;
+    if (p.d_head < c.d_rot || p.at < 0 || p.at > p.d_head - c.d_rot)
+        return fail(KVR_E_ARG, "%s: values [%d, %d) are not in a head of %d", name, p.at,
+                    p.at + c.d_rot, p.d_head);
+    if ((int64_t)c.n * p.heads > INT32_MAX || (int64_t)p.heads * p.d_head > INT32_MAX)
+        return fail(KVR_E_ARG, "%s: n * heads and heads * d_head must be below 2^31", name);
+    if (p.x_stride_token < 0 || p.x_stride_head < 0 || p.out_stride_token < 0 ||
+        p.out_stride_head < 0)
+        return fail(KVR_E_ARG, "%s: negative stride", name);
+    if (c.n > 0 && (!p.x || !p.out))
+        return fail(KVR_E_ARG, "%s: x and out are required", name);
+    const uintptr_t e = (uintptr_t)kvr::value_bytes(c.value_type);
+    if (reinterpret_cast<uintptr_t>(p.x) % e != 0 || reinterpret_cast<uintptr_t>(p.out) % e != 0)
+        return fail(KVR_E_ARG, "%s: x or out is not aligned", name);
+    if (p.x == p.out && (p.x_stride_token != p.out_stride_token ||
+                         p.x_stride_head != p.out_stride_head))
+        return fail(KVR_E_ARG, "%s: in place, x and out have the same strides", name);
+    return KVR_OK;
+}
+
+int kvr_rotate_rows(kvr_ctx *ctx, const kvr_rotate_call *call, void *stream)
+{
+    if (int rc = check_ctx(ctx, false))
+        return rc;
+    if (!call)
+        return fail(KVR_E_ARG, "null call");
+    const kvr_rotate_call &c = *call;
+    if (!kvr::value_type_ok(c.value_type))
+        return fail(KVR_E_ARG, "unknown value type %d", c.value_type);
+    if (c.layout != KVR_ROPE_INTERLEAVED && c.layout != KVR_ROPE_HALF)
+        return fail(KVR_E_ARG, "unknown layout %d", c.layout);
+    if (c.n < 0 || c.n >= (1 << 24))
+        return fail(KVR_E_ARG, "n must be in [0, 2^24)");
+    if (c.d_rot < 2 || c.d_rot > 1024 || c.d_rot % 2)
+        return fail(KVR_E_ARG, "d_rot must be even, 2 to 1024");
+    if (int rc = check_rotate_part(c, c.query, "query"))
+        return rc;
+    if (int rc = check_rotate_part(c, c.key, "key"))
+        return rc;
+    if (c.n > 0 && (!c.positions || !c.frequencies))
+        return fail(KVR_E_ARG, "positions and frequencies are required");
+    if (reinterpret_cast<uintptr_t>(c.positions) % 4 != 0 ||
+        reinterpret_cast<uintptr_t>(c.frequencies) % 8 != 0)
+        return fail(KVR_E_ARG, "positions or frequencies is not aligned");
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (int rc = check_stream(ctx, s))
+        return rc;
+    if (c.n == 0)
+        return ok();
+    const hipError_t e = kvr::launch_rotate(ctx, c, s);
+    return e == hipSuccess ? ok() : hip_fail(e, "rotation launch");
+}
+
+int kvr_rope_frequencies(int32_t d_rot, double base, int32_t scaling, double factor,
+                         int32_t original_length, double beta_fast, double beta_slow,
+                         double *frequencies, float *magnitude)
+{
+    if (!frequencies)
+        return fail(KVR_E_ARG, "frequencies is required");
+    if (d_rot < 2 || d_rot > 1024 || d_rot % 2)
+        return fail(KVR_E_ARG, "d_rot must be even, 2 to 1024");
+    if (scaling < KVR_ROPE_NONE || scaling > KVR_ROPE_RAMP)
+        return fail(KVR_E_ARG, "unknown scaling %d", scaling);
+    if (!(base > 1.0) || !std::isfinite(base) || !(factor >= 1.0) || !std::isfinite(factor))
+        return fail(KVR_E_ARG, "base must be above 1, factor at least 1");
+    if (scaling == KVR_ROPE_BASE && d_rot < 4)
+        return fail(KVR_E_ARG, "a changed base needs d_rot of 4 or more");
+    if (scaling == KVR_ROPE_RAMP &&
+        (original_length < 1 || !(beta_slow > 0.0) || !(beta_fast > beta_slow) ||
+         !std::isfinite(beta_fast)))
+        return fail(KVR_E_ARG, "original_length must be >= 1 and beta_fast > beta_slow > 0");
+    const double kTurn = 6.283185307179586476925;
+    if (scaling == KVR_ROPE_BASE)
+        base *= std::pow(factor, (double)d_rot / (d_rot - 2));
+    double low = 0.0, high = 1.0;
+    if (scaling == KVR_ROPE_RAMP) {
+        auto pair = [&](double turns) {
+            return d_rot * std::log(original_length / (kTurn * turns)) / (2.0 * std::log(base));
+        };
+        low = std::fmin(std::fmax(std::floor(pair(beta_fast)), 0.0), d_rot - 1.0);
+        high = std::fmin(std::fmax(std::ceil(pair(beta_slow)), 0.0), d_rot - 1.0);
+        high = std::fmax(high, low + 0.001);
+    }
+    for (int32_t i = 0; i < d_rot / 2; ++i) {
+        const double f = std::pow(base, -2.0 * i / d_rot) / kTurn;
+        double r = scaling == KVR_ROPE_LINEAR ? 1.0 : 0.0;
+        if (scaling == KVR_ROPE_RAMP)
+            r = std::fmin(std::fmax((i - low) / (high - low), 0.0), 1.0);
+        frequencies[i] = f * (1.0 - r) + f / factor * r;
+    }
+    if (magnitude)
+        *magnitude = scaling == KVR_ROPE_RAMP ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
+    return ok();
+}
+
+static int check_logprob_sizes(int32_t n, int32_t vocab)
+{
+    if (n < 0 || n > (1 << 20) || vocab < 1 || vocab > (1 << 24))
+        return fail(KVR_E_ARG, "n must be in [0, 2^20], vocab in [1, 2^24]");
+    return KVR_OK;
+}
+
+int64_t kvr_logprob_workspace(int32_t n, int32_t vocab)
+{
+    if (int rc = check_logprob_sizes(n, vocab))
+        return rc;
+    ok();
+    return kvr::logprob_workspace_bound(n, vocab);
+}
+
+int kvr_token_logprobs(kvr_ctx *ctx, const kvr_logprob_call *call, void *stream)
+{
+    if (int rc = check_ctx(ctx, false))
+        return rc;
+    if (!call)
+        return fail(KVR_E_ARG, "null call");
+    const kvr_logprob_call &c = *call;
+    if (!kvr::value_type_ok(c.value_type))
+        return fail(KVR_E_ARG, "unknown value type %d", c.value_type);
+    if (int rc = check_logprob_sizes(c.n, c.vocab))
+        return rc;
+    if (c.m < 0 || c.m > (1 << 16) || c.top < 0 || c.top > 64 ||
+        (int64_t)c.n * c.m > INT32_MAX)
+        return fail(KVR_E_ARG, "m must be in [0, 2^16], top in [0, 64], n * m below 2^31");
+    if (!(c.scale > 0.f) || !std::isfinite(c.scale))
+        return fail(KVR_E_ARG, "scale must be finite and above 0");
+    if (c.logits_stride < 0)
+        return fail(KVR_E_ARG, "negative stride");
+    if (c.n > 0 && (!c.logits || (c.m > 0 && (!c.tokens || !c.logprob)) ||
+                    (c.top > 0 && (!c.top_ids || !c.top_logprob))))
+        return fail(KVR_E_ARG, "logits, and outputs for the tokens and alternatives asked for, "
+                               "are required");
+    const uintptr_t words = reinterpret_cast<uintptr_t>(c.tokens) |
+                            reinterpret_cast<uintptr_t>(c.logprob) |
+                            reinterpret_cast<uintptr_t>(c.lse) |
+                            reinterpret_cast<uintptr_t>(c.entropy) |
+                            reinterpret_cast<uintptr_t>(c.top_ids) |
+                            reinterpret_cast<uintptr_t>(c.top_logprob);
+    if (reinterpret_cast<uintptr_t>(c.logits) % (uintptr_t)kvr::value_bytes(c.value_type) != 0 ||
+        words % 4 != 0)
+        return fail(KVR_E_ARG, "logits, tokens or an output is not aligned");
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (int rc = check_stream(ctx, s))
+        return rc;
+    if (c.n == 0)
+        return ok();
+    const int64_t need = kvr::logprob_workspace(c.n, c.vocab);
+    if (!c.workspace || c.workspace_bytes < (size_t)need)
+        return fail(KVR_E_ARG, "the workspace has %zu bytes, the call needs %lld",
+                    c.workspace ? c.workspace_bytes : 0, (long long)need);
+    if (reinterpret_cast<uintptr_t>(c.workspace) % 16 != 0)
+        return fail(KVR_E_ARG, "the workspace is not aligned to 16 bytes");
+    const hipError_t e = kvr::launch_logprob(ctx, c, s);
+    return e == hipSuccess ? ok() : hip_fail(e, "log probability launch");
 }
 
 int kvr_status_summary(const int32_t *status, int32_t n, int32_t *first_bad)

@@ -186,6 +186,13 @@ hipError_t launch_compact(const kvr_ctx *c, int32_t max_moves, int32_t *moves, i
 
 hipError_t launch_pack(const kvr_ctx *c, const kvr_pack_call &p, hipStream_t s);
 
+hipError_t launch_rotate(const kvr_ctx *c, const kvr_rotate_call &r, hipStream_t s);
+
+// Workspace bytes of exactly that call, and the largest over smaller ones.
+int64_t logprob_workspace(int32_t n, int32_t vocab);
+int64_t logprob_workspace_bound(int32_t n, int32_t vocab);
+hipError_t launch_logprob(const kvr_ctx *c, const kvr_logprob_call &p, hipStream_t s);
+
 // How a kvr_attend_rows call is cut: `block` query rows (heads, or heads of
 // several queries that share a selection) per workgroup, `shares` shares of
 // the rows.  Workspace bytes of exactly that call, and the largest over calls

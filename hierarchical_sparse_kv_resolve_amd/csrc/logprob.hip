@@ -1,0 +1,361 @@
+// Log probabilities of given tokens, entropy and the most likely alternatives
+// of rows of logits ("Adaptive DHiSparse: Speculative Decoding over a
+// Load-Adaptive KV Hierarchy", section "How it works", paragraph "Speculative
+// state": verification scores the drafted tokens).
+//
+// With m the row's largest logit, f = log2(e) * scale and d_j = f (x_j - m) <= 0
+// (the difference first, so that logits of the type's lowest value do not
+// overflow):
+//   l = sum 2^d_j,  u = -sum 2^d_j d_j   (terms >= 0: nothing cancels)
+//   lse = scale m + ln l,  entropy = ln l + ln 2 u / l
+//   logprob = scale (x - m) - ln l
+//
+// part_kernel reads the logits once: a row is cut into shares of a workgroup
+// each, whose threads keep m, l, u and their largest logit.
+// row_kernel, a workgroup per row, joins the shares.  For the alternatives it
+// takes the threads' largest logits in 64 groups (a thread's lane): the top-th
+// largest of the groups' maxima is a value that at least `top` logits reach,
+// so only the runs of threads whose maximum reaches it are read again, and of
+// those logits the few that reach it are ranked by counting, (value, lower token
+// first), which needs no order of arrival.  Rows with so many that the list
+// overflows (equal logits, or large ones that all fell to one group) are
+// searched once for each alternative instead.
+#include "block.h"
+#include "kvr_internal.h"
+#include "values.h"
+
+namespace kvr {
+namespace {
+
+constexpr int NT = 256;
+constexpr int kRun = 8;        // consecutive logits of a thread: one piece
+constexpr int kList = 1024;    // logits that are ranked
+constexpr float kInf = __builtin_inff();
+
+struct LogprobArgs {
+    kvr_logprob_call c;
+    int32_t shares, pieces;  // of a row
+    int32_t per;             // pieces of a share (a multiple of NT, but for the last)
+    bool wide;
+    float *parts;            // [n][shares][4]: m, l, u
+    float *tops;             // [n][shares][NT]: the threads' largest logits
+};
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Logits [8 piece, 8 piece + 8) of a row, -infinity past its end.
+template <typename T>
+__device__ __forceinline__ void load_piece(const LogprobArgs &a, const T *row, int piece,
+                                           float (&x)[kRun])
+{
+    const int at = piece * kRun;
+    if (at + kRun <= a.c.vocab) {
+        load_run<kRun>(row + at, a.wide, x);
+    } else {
+#pragma unroll
+        for (int k = 0; k < kRun; ++k)
+            x[k] = at + k < a.c.vocab ? (float)row[at + k] : -kInf;
+    }
+}
+
+// Moves l and u to the reference `to` >= m: what m rises by is added to u for
+// each probability.  m may be -infinity (l is 0 then, or NaN).
+__device__ __forceinline__ void raise(float factor, float m, float &l, float &u, float to)
+{
+    const float d = (m - to) * factor;  // NaN for two infinities of one sign
+    const float w = exp2_hw(m == -kInf ? -kInf : d);
+    u = w > 0.f ? w * (u - d * l) : 0.f;
+    l *= w;
+}
+
+// Joins (m, l, u) of another part.
+__device__ __forceinline__ void join(float factor, float &m, float &l, float &u, float m2, float l2,
+                                     float u2)
+{
+    const float to = fmaxf(m, m2);
+    raise(factor, m, l, u, to);
+    raise(factor, m2, l2, u2, to);
+    m = to;
+    l += l2;
+    u += u2;
+}
+
+template <typename T>
+__global__ __launch_bounds__(NT) void part_kernel(LogprobArgs a)
+{
+    __shared__ float sM[NT / 64], sL[NT / 64], sU[NT / 64];
+    const int64_t row_at = blockIdx.x / a.shares;
+    const int share = blockIdx.x % a.shares;
+    const T *row = static_cast<const T *>(a.c.logits) + row_at * a.c.logits_stride;
+    const int p0 = share * a.per;
+    const int p1 = p0 + a.per < a.pieces ? p0 + a.per : a.pieces;
+    const float factor = a.c.scale * 1.44269504088896340736f;
+    float m = -kInf, l = 0.f, u = 0.f;
+    for (int p = p0 + threadIdx.x; p < p1; p += NT) {
+        float x[kRun];
+        load_piece(a, row, p, x);
+        float most = -kInf;
+#pragma unroll
+        for (int k = 0; k < kRun; ++k)
+            most = fmaxf(most, x[k]);
+        const float to = fmaxf(m, most);
+        raise(factor, m, l, u, to);
+        m = to;
+        const float ref = to == -kInf ? 0.f : to;
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) {
+            const float d = (x[k] - ref) * factor;
+            const float e = exp2_hw(d);
+            l += e;
+            u -= e > 0.f ? e * d : 0.f;
+        }
+    }
+    if (a.c.top > 0)
+        a.tops[(int64_t)blockIdx.x * NT + threadIdx.x] = m;
+#pragma unroll
+    for (int k = 32; k >= 1; k >>= 1)
+        join(factor, m, l, u, __shfl_xor(m, k), __shfl_xor(l, k), __shfl_xor(u, k));
+    if (lane_id() == 0) {
+        sM[wave_id()] = m;
+        sL[wave_id()] = l;
+        sU[wave_id()] = u;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int k = 1; k < NT / 64; ++k)
+            join(factor, m, l, u, sM[k], sL[k], sU[k]);
+        float *out = a.parts + (int64_t)blockIdx.x * 4;
+        out[0] = m;
+        out[1] = l;
+        out[2] = u;
+    }
+}
+
+// (x, i) before (y, j): larger, or equal and lower.
+__device__ __forceinline__ bool before(float x, int i, float y, int j)
+{
+    return x > y || (x == y && i < j);
+}
+
+template <typename T>
+__global__ __launch_bounds__(NT) void row_kernel(LogprobArgs a)
+{
+    __shared__ float sValue[kList];
+    __shared__ int sToken[kList];
+    __shared__ int sCount;
+    __shared__ float sM[NT / 64];
+    __shared__ int sI[NT / 64];
+    const int64_t r = blockIdx.x;
+    const int tid = threadIdx.x, lane = lane_id(), wave = wave_id();
+    const T *row = static_cast<const T *>(a.c.logits) + r * a.c.logits_stride;
+    const float factor = a.c.scale * 1.44269504088896340736f;
+    if (tid == 0)
+        sCount = 0;
+
+    // the row's sums, joined in a fixed order by every wave
+    float m = -kInf, l = 0.f, u = 0.f;
+    const float *parts = a.parts + r * a.shares * 4;
+    for (int s = lane; s < a.shares; s += 64)
+        join(factor, m, l, u, parts[4 * s], parts[4 * s + 1], parts[4 * s + 2]);
+#pragma unroll
+    for (int k = 32; k >= 1; k >>= 1)
+        join(factor, m, l, u, __shfl_xor(m, k), __shfl_xor(l, k), __shfl_xor(u, k));
+    // the first lane's, for all: which thread writes an alternative varies, and
+    // the lanes' sums differ in their last bits (their products are not fused alike)
+    auto first = [](float x) {
+        return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
+    };
+    m = first(m), l = first(l), u = first(u);
+    const bool bad = l != l;
+    const float nan = __builtin_nanf("");
+    constexpr float kLn2 = 0.69314718055994530942f;
+    const float log_l = kLn2 * __log2f(l);
+    auto logprob = [&](float x) {
+        return bad ? nan : x == -kInf ? -kInf : (x - m) * a.c.scale - log_l;
+    };
+    if (tid == 0) {
+        if (a.c.lse)
+            a.c.lse[r] = bad ? nan : m == -kInf ? -kInf : m * a.c.scale + log_l;
+        if (a.c.entropy)
+            a.c.entropy[r] = bad ? nan : m == -kInf ? 0.f : log_l + kLn2 * (u / l);
+    }
+    for (int k = tid; k < a.c.m; k += NT) {
+        const int token = a.c.tokens[r * a.c.m + k];
+        const float x = token >= 0 && token < a.c.vocab ? (float)row[token] : -kInf;
+        a.c.logprob[r * a.c.m + k] = logprob(x);
+    }
+    const int top = a.c.top;
+    if (top == 0)
+        return;
+    int32_t *ids = a.c.top_ids + r * top;
+    float *probs = a.c.top_logprob + r * top;
+    for (int k = tid; k < top; k += NT) {
+        ids[k] = -1;
+        probs[k] = bad ? nan : -kInf;
+    }
+    if (bad || m == -kInf)
+        return;
+
+    // groups: the lanes; a wave takes every fourth row of 64 maxima
+    const float *tops = a.tops + r * a.shares * NT;
+    float most = -kInf;
+    for (int s = wave; s < a.shares * (NT / 64); s += NT / 64)
+        most = fmaxf(most, tops[s * 64 + lane]);
+    sValue[tid] = most;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < NT / 64; ++k)
+        most = fmaxf(most, sValue[k * 64 + lane]);
+    // the lane's place among the 64
+    int place = 0;
+    for (int k = 0; k < 64; ++k) {
+        const float y = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(most), k));
+        place += before(y, k, most, lane);
+    }
+    // (uniform: every wave has the same maxima)
+    const uint64_t at = __ballot(place == top - 1);
+    const float bound = __shfl(most, __ffsll((unsigned long long)at) - 1);
+    __syncthreads();
+    for (int s = 0; s < a.shares; ++s) {
+        const float t = tops[s * NT + tid];
+        if (t < bound || t == -kInf)
+            continue;
+        const int p0 = s * a.per;
+        const int p1 = p0 + a.per < a.pieces ? p0 + a.per : a.pieces;
+        for (int p = p0 + tid; p < p1; p += NT) {
+            float x[kRun];
+            load_piece(a, row, p, x);
+#pragma unroll
+            for (int k = 0; k < kRun; ++k)
+                if (x[k] >= bound && x[k] > -kInf) {
+                    const int n = atomicAdd(&sCount, 1);
+                    if (n < kList) {
+                        sValue[n] = x[k];
+                        sToken[n] = p * kRun + k;
+                    }
+                }
+        }
+    }
+    __syncthreads();
+    const int count = sCount;
+    if (count <= kList) {
+        for (int n = tid; n < count; n += NT) {
+            const float x = sValue[n];
+            const int token = sToken[n];
+            int rank = 0;
+            for (int k = 0; k < count; ++k)
+                rank += before(sValue[k], sToken[k], x, token);
+            if (rank < top) {
+                ids[rank] = token;
+                probs[rank] = logprob(x);
+            }
+        }
+        return;
+    }
+    // too many reach the bound: one search of the row for each alternative
+    float last = kInf;
+    int last_token = -1;
+    for (int k = 0; k < top; ++k) {
+        float x = -kInf;
+        int token = a.c.vocab;
+        for (int p = tid; p < a.pieces; p += NT) {
+            float y[kRun];
+            load_piece(a, row, p, y);
+#pragma unroll
+            for (int q = 0; q < kRun; ++q)
+                if (before(last, last_token, y[q], p * kRun + q) &&
+                    before(y[q], p * kRun + q, x, token)) {
+                    x = y[q];
+                    token = p * kRun + q;
+                }
+        }
+#pragma unroll
+        for (int q = 32; q >= 1; q >>= 1) {
+            const float y = __shfl_xor(x, q);
+            const int other = __shfl_xor(token, q);
+            if (before(y, other, x, token)) {
+                x = y;
+                token = other;
+            }
+        }
+        if (lane == 0) {
+            sM[wave] = x;
+            sI[wave] = token;
+        }
+        __syncthreads();
+        x = sM[0];
+        token = sI[0];
+#pragma unroll
+        for (int w = 1; w < NT / 64; ++w)
+            if (before(sM[w], sI[w], x, token)) {
+                x = sM[w];
+                token = sI[w];
+            }
+        __syncthreads();
+        if (x == -kInf)
+            return;  // (uniform)
+        if (tid == 0) {
+            ids[k] = token;
+            probs[k] = logprob(x);
+        }
+        last = x;
+        last_token = token;
+    }
+}
+
+// A row's shares: a piece for each thread at least, and enough workgroups for
+// the compute units.
+int32_t shares_of(int32_t n, int32_t vocab)
+{
+    const int64_t most = ((int64_t)vocab + kRun * NT - 1) / (kRun * NT);
+    const int64_t want = 1024 / n;
+    return (int32_t)(want < 1 ? 1 : want < most ? want : most);
+}
+
+constexpr int64_t kShareBytes = (NT + 4) * sizeof(float);
+
+template <typename T>
+hipError_t launch_typed(const kvr_ctx *c, const LogprobArgs &a, hipStream_t s)
+{
+    const hipError_t e = launch(c, KVR_KERNEL_LOGPROB, part_kernel<T>,
+                                dim3((unsigned)((int64_t)a.c.n * a.shares)), dim3(NT), 0, s, a);
+    if (e != hipSuccess)
+        return e;
+    return launch(c, KVR_KERNEL_LOGPROB, row_kernel<T>, dim3((unsigned)a.c.n), dim3(NT), 0, s, a);
+}
+
+}  // namespace
+
+// Of exactly that call, and the largest over calls of fewer rows or logits.
+int64_t logprob_workspace(int32_t n, int32_t vocab)
+{
+    return n * (int64_t)shares_of(n, vocab) * kShareBytes;
+}
+
+int64_t logprob_workspace_bound(int32_t n, int32_t vocab)
+{
+    const int64_t most = ((int64_t)vocab + kRun * NT - 1) / (kRun * NT) * n;
+    const int64_t many = n > 1024 ? n : 1024;
+    return (most < many ? most : many) * kShareBytes;
+}
+
+hipError_t launch_logprob(const kvr_ctx *c, const kvr_logprob_call &p, hipStream_t s)
+{
+    LogprobArgs a{};
+    a.c = p;
+    a.pieces = (int32_t)(((int64_t)p.vocab + kRun - 1) / kRun);
+    a.shares = shares_of(p.n, p.vocab);
+    a.per = (a.pieces + a.shares * NT - 1) / (a.shares * NT) * NT;
+    a.wide = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 &&
+             p.logits_stride * value_bytes(p.value_type) % 16 == 0;
+    a.parts = static_cast<float *>(p.workspace);
+    a.tops = a.parts + (int64_t)p.n * a.shares * 4;
+    if (p.value_type == KVR_VALUE_F32)
+        return launch_typed<float>(c, a, s);
+    if (p.value_type == KVR_VALUE_BF16)
+        return launch_typed<__bf16>(c, a, s);
+    return launch_typed<_Float16>(c, a, s);
+}
+
+}  // namespace kvr

@@ -17,15 +17,8 @@
 #include <new>
 #include <vector>
 
+#include "draft.h"
 #include "kvr_internal.h"
-
-struct kvr_draft {
-    int32_t n_req, W, C, R;
-    uint8_t *ring;    // [n_req][C][R]
-    int32_t *length;  // [n_req]
-    int32_t *high;    // [n_req]
-    int device;
-};
 
 struct kvr_staging {
     int32_t n;
@@ -164,6 +157,15 @@ DraftArgs draft_args(const kvr_draft *dr, const int32_t *req_ids)
     return d;
 }
 
+int launch_result(hipError_t e, const char *what)
+{
+    if (e != hipSuccess)
+        return api_fail(KVR_E_HIP, "%s: %s", what, hipGetErrorString(e));
+    return api_ok();
+}
+
+}  // namespace
+
 int draft_prologue(const kvr_draft *d, int32_t n, hipStream_t s)
 {
     (void)s;
@@ -177,14 +179,6 @@ int draft_prologue(const kvr_draft *d, int32_t n, hipStream_t s)
     return KVR_OK;
 }
 
-int launch_result(hipError_t e, const char *what)
-{
-    if (e != hipSuccess)
-        return api_fail(KVR_E_HIP, "%s: %s", what, hipGetErrorString(e));
-    return api_ok();
-}
-
-}  // namespace
 }  // namespace kvr
 
 extern "C" {
@@ -195,10 +189,11 @@ int kvr_draft_create(int32_t n_req, int32_t window, int32_t capacity, int32_t ro
     if (!out)
         return kvr::api_fail(KVR_E_ARG, "out is required");
     *out = nullptr;
-    if (n_req < 1 || window < 1 || capacity < window || row_bytes < 16 || row_bytes % 16 ||
-        (int64_t)capacity * row_bytes > ((int64_t)1 << 31))
+    const bool rows = ring || row_bytes != 0;  // else a ring of K/V layers only
+    if (n_req < 1 || window < 1 || capacity < window || (rows && row_bytes < 16) ||
+        row_bytes % 16 || (int64_t)capacity * row_bytes > ((int64_t)1 << 31))
         return kvr::api_fail(KVR_E_ARG, "bad drafter ring shape");
-    if (!ring || !length || !high)
+    if ((rows && !ring) || !length || !high)
         return kvr::api_fail(KVR_E_ARG, "ring, length and high are required");
     kvr_draft *d = new (std::nothrow) kvr_draft();
     if (!d)
@@ -241,6 +236,8 @@ int kvr_draft_append(kvr_draft *d, int32_t n, const int32_t *req_ids, int32_t ro
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (int rc = kvr::draft_prologue(d, n, s))
         return rc;
+    if (!d->ring)
+        return kvr::api_fail(KVR_E_ARG, "the ring holds no rows");
     // at most C rows, so one call never writes a slot twice
     if (rows_each < 0 || rows_each > d->C || (n > 0 && rows_each > 0 && !rows))
         return kvr::api_fail(KVR_E_ARG, "rows_each must be in [0, capacity] with rows given");
@@ -277,6 +274,8 @@ int kvr_draft_window(kvr_draft *d, int32_t n, const int32_t *req_ids, void *out,
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (int rc = kvr::draft_prologue(d, n, s))
         return rc;
+    if (!d->ring)
+        return kvr::api_fail(KVR_E_ARG, "the ring holds no rows");
     if (n > 0 && !out)
         return kvr::api_fail(KVR_E_ARG, "out is required");
     if (n == 0)

@@ -46,17 +46,25 @@ EXPORTS = ("kvr_create", "kvr_destroy", "kvr_last_error", "kvr_bind_metadata", "
            "kvr_staging_acquire", "kvr_staging_release", "kvr_row_layout", "kvr_pack_rows",
            "kvr_attend_rows", "kvr_attend_workspace", "kvr_bind_page_refs", "kvr_count_page_refs",
            "kvr_release_requests", "kvr_fork_requests", "kvr_copy_pages", "kvr_pool_workspace",
-           "kvr_list_free_pages", "kvr_compact_pool")
+           "kvr_list_free_pages", "kvr_compact_pool", "kvr_rotate_rows", "kvr_rope_frequencies",
+           "kvr_token_logprobs", "kvr_logprob_workspace", "kvr_draft_bind_kv",
+           "kvr_draft_write_kv", "kvr_draft_read_kv", "kvr_draft_advance", "kvr_draft_attend",
+           "kvr_draft_attend_workspace")
 
 # kvr_kernel: kinds of the library's kernel launches (launch timing).
 KERNEL_NAMES = ("append", "resolve", "refill", "gather", "dedup", "state", "fused", "step",
-                "attend", "pack", "pages")
+                "attend", "pack", "pages", "rotate", "logprob")
 
 # kvr_row_format, and the 16-bit type of queries, outputs and rope parts.
 ROW_FORMATS = {"bf16": 0, "f16": 1, "fp8": 2}
 _ROW_TYPES = {"bf16": "bfloat16", "f16": "float16", "fp8": "bfloat16"}
 # kvr_value_type by torch dtype name.
 _VALUE_TYPES = {"bfloat16": 0, "float16": 1, "float32": 2}
+# kvr_rope_layout, kvr_rope_scaling, kvr_draft_mask.
+ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp": 3}
+DRAFT_MASKS = {"causal": 0, "block": 1, "kept": 2}
+DRAFT_BLOCK = 64
 
 
 class KvrError(RuntimeError):
@@ -116,6 +124,56 @@ class AttendCall(ctypes.Structure):
                 ("q", ctypes.c_void_p), ("q_stride_entry", ctypes.c_int64),
                 ("q_stride_query", ctypes.c_int64), ("q_stride_head", ctypes.c_int64),
                 ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("status", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class RotatePart(ctypes.Structure):
+    """kvr_rotate_part of include/kvr.h."""
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("x_stride_token", ctypes.c_int64), ("x_stride_head", ctypes.c_int64),
+                ("out_stride_token", ctypes.c_int64), ("out_stride_head", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("d_head", ctypes.c_int32), ("at", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class RotateCall(ctypes.Structure):
+    """kvr_rotate_call of include/kvr.h."""
+    _fields_ = [("value_type", ctypes.c_int32), ("layout", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("d_rot", ctypes.c_int32), ("magnitude", ctypes.c_float),
+                ("inverse", ctypes.c_int32), ("positions", ctypes.c_void_p),
+                ("frequencies", ctypes.c_void_p), ("query", RotatePart), ("key", RotatePart)]
+
+
+class LogprobCall(ctypes.Structure):
+    """kvr_logprob_call of include/kvr.h."""
+    _fields_ = [("value_type", ctypes.c_int32), ("n", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("m", ctypes.c_int32), ("top", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("logits", ctypes.c_void_p), ("logits_stride", ctypes.c_int64),
+                ("tokens", ctypes.c_void_p), ("logprob", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p), ("entropy", ctypes.c_void_p),
+                ("top_ids", ctypes.c_void_p), ("top_logprob", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class DraftWriteCall(ctypes.Structure):
+    """kvr_draft_write_call of include/kvr.h."""
+    _fields_ = [("layer", ctypes.c_int32), ("value_type", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("rows", ctypes.c_int32), ("req_ids", ctypes.c_void_p),
+                ("count", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_stride_entry", ctypes.c_int64), ("k_stride_token", ctypes.c_int64),
+                ("k_stride_head", ctypes.c_int64), ("v_stride_entry", ctypes.c_int64),
+                ("v_stride_token", ctypes.c_int64), ("v_stride_head", ctypes.c_int64),
+                ("status", ctypes.c_void_p)]
+
+
+class DraftAttendCall(ctypes.Structure):
+    """kvr_draft_attend_call of include/kvr.h."""
+    _fields_ = [("layer", ctypes.c_int32), ("mask", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("nq", ctypes.c_int32), ("heads", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("req_ids", ctypes.c_void_p), ("count", ctypes.c_void_p), ("q", ctypes.c_void_p),
+                ("q_stride_entry", ctypes.c_int64), ("q_stride_query", ctypes.c_int64),
+                ("q_stride_head", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p), ("status", ctypes.c_void_p),
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
@@ -184,12 +242,24 @@ def lib():
             "kvr_pool_workspace": [P],
             "kvr_list_free_pages": [P, P, P, P, U, P],
             "kvr_compact_pool": [P, I, P, P, P, U, P],
+            "kvr_rotate_rows": [P, P, P],
+            "kvr_rope_frequencies": [I, ctypes.c_double, I, ctypes.c_double, I, ctypes.c_double,
+                                     ctypes.c_double, P, P],
+            "kvr_token_logprobs": [P, P, P],
+            "kvr_logprob_workspace": [I, I],
+            "kvr_draft_bind_kv": [P, I, I, I, P, P],
+            "kvr_draft_write_kv": [P, P, P],
+            "kvr_draft_read_kv": [P, I, I, P, I, P, P, P, P, P],
+            "kvr_draft_advance": [P, I, P, I, P, P, P],
+            "kvr_draft_attend": [P, P, P],
+            "kvr_draft_attend_workspace": [P, I, I, I],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
             fn.argtypes = args
             fn.restype = ctypes.c_int
-        for name in ("kvr_attend_workspace", "kvr_pool_workspace"):
+        for name in ("kvr_attend_workspace", "kvr_pool_workspace", "kvr_logprob_workspace",
+                     "kvr_draft_attend_workspace"):
             getattr(L, name).restype = ctypes.c_int64
         L.kvr_last_error.argtypes = []
         L.kvr_last_error.restype = ctypes.c_char_p
@@ -338,6 +408,26 @@ def _row_format(fmt: str) -> int:
     if fmt not in ROW_FORMATS:
         raise ValueError(f"unknown row format {fmt!r}: one of {', '.join(ROW_FORMATS)}")
     return ROW_FORMATS[fmt]
+
+
+def _choice(value: str, what: str, of: dict) -> int:
+    if value not in of:
+        raise ValueError(f"unknown {what} {value!r}: one of {', '.join(of)}")
+    return of[value]
+
+
+def rope_frequencies(d_rot, base=10000.0, scaling="none", factor=1.0, original_length=0,
+                     beta_fast=32.0, beta_slow=1.0):
+    """(float64 array [d_rot / 2] of turns per position, magnitude): what
+    Context.rotate_rows takes.  scaling: "none", "linear", "base" or "ramp"; see
+    kvr_rope_scaling."""
+    import numpy as np
+    kind = _choice(scaling, "scaling", ROPE_SCALINGS)
+    out = np.zeros(max(1, d_rot // 2), dtype=np.float64)
+    magnitude = ctypes.c_float()
+    _check(lib().kvr_rope_frequencies(d_rot, base, kind, factor, original_length, beta_fast,
+                                      beta_slow, out.ctypes.data, ctypes.byref(magnitude)))
+    return out, magnitude.value
 
 
 def last_error() -> str:
@@ -663,6 +753,86 @@ class Context:
                           _dev(lse, "lse"), _words(status, "status", n, here), ws, ws_bytes)
         _check(lib().kvr_attend_rows(self.handle, ctypes.byref(call), _stream(stream)))
 
+    # ------------------------------------------- positions and scores
+
+    def rotate_rows(self, n, positions, frequencies, x, out=None, key=None, key_out=None, *, d_rot,
+                    layout, at=0, key_at=0, magnitude=1.0, inverse=False, stream=None):
+        """Rotates values [at, at + d_rot) of each head of x [n, heads, d_head] by
+        its token's position (int32 [n]) times the frequencies (float64
+        [d_rot / 2], turns per position), into out (in place without it), and
+        with them those of key [n, key heads, key d_head].  Last dimensions
+        contiguous; x and key of one type, bf16, fp16 or fp32.  See
+        kvr_rotate_rows."""
+        here = _here()
+        kind = None
+        parts = []
+        for name, src, dst, first in (("x", x, out, at), ("key", key, key_out, key_at)):
+            if src is None:
+                if dst is not None:
+                    raise ValueError(f"{name}: an output without an input")
+                parts.append(RotatePart())
+                continue
+            dst = src if dst is None else dst
+            if getattr(src, "ndim", 3) != 3:
+                raise ValueError(f"{name}: {src.ndim} dimensions, the call needs "
+                                 "[n, heads, d_head]")
+            kind = _typed(src, name, _VALUE_TYPES if kind is None else (kind,), here)
+            _typed(dst, f"{name}'s output", (kind,), here, src.shape)
+            if src.shape[0] != n:
+                raise ValueError(f"{name}: {src.shape[0]} tokens, the call has {n}")
+            a, b = src.stride(), dst.stride()
+            parts.append(RotatePart(src.data_ptr(), dst.data_ptr(), a[0], a[1], b[0], b[1],
+                                    src.shape[1], src.shape[2], first, 0))
+        if kind is None:
+            raise ValueError("x or key is required")
+        _typed(frequencies, "frequencies", ("float64",), here, (d_rot // 2,))
+        call = RotateCall(_VALUE_TYPES[kind], _choice(layout, "layout", ROPE_LAYOUTS), n, d_rot,
+                          magnitude, int(inverse), _words(positions, "positions", n, here),
+                          frequencies.data_ptr(), *parts)
+        _check(lib().kvr_rotate_rows(self.handle, ctypes.byref(call), _stream(stream)))
+
+    @staticmethod
+    def logprob_workspace(n, vocab) -> int:
+        """Workspace bytes for token_logprobs calls of up to these sizes."""
+        got = lib().kvr_logprob_workspace(n, vocab)
+        return got if got >= 0 else _check(got)
+
+    def token_logprobs(self, n, logits, tokens=None, logprob=None, *, lse=None, entropy=None,
+                       top_ids=None, top_logprob=None, scale=1.0, workspace=None, stream=None):
+        """Log probabilities [n, m] of tokens (int32 [n, m]) under rows of logits
+        [n, vocab] (bf16, fp16 or fp32; rows may be strided slices) times scale,
+        their lse and entropy [n], and the most likely tokens with theirs
+        [n, top].  See kvr_token_logprobs."""
+        here = _here()
+        if getattr(logits, "ndim", 2) != 2:
+            raise ValueError(f"logits: {logits.ndim} dimensions, the call needs [n, vocab]")
+        kind = _typed(logits, "logits", _VALUE_TYPES, here)
+        if logits.shape[0] != n:
+            raise ValueError(f"logits: {logits.shape[0]} rows, the call has {n}")
+        m = top = 0
+        if (tokens is None) != (logprob is None) or (top_ids is None) != (top_logprob is None):
+            raise ValueError("tokens go with logprob, and top_ids with top_logprob")
+        if tokens is not None:
+            _typed(tokens, "tokens", ("int32",), here)
+            m = tokens.shape[1] if tokens.ndim == 2 else -1
+            _typed(tokens, "tokens", ("int32",), here, (n, m))
+            _typed(logprob, "logprob", ("float32",), here, (n, m))
+        if top_ids is not None:
+            _typed(top_ids, "top_ids", ("int32",), here)
+            top = top_ids.shape[1] if top_ids.ndim == 2 else -1
+            _typed(top_ids, "top_ids", ("int32",), here, (n, top))
+            _typed(top_logprob, "top_logprob", ("float32",), here, (n, top))
+        for name, t in (("lse", lse), ("entropy", entropy)):
+            if t is not None:
+                _typed(t, name, ("float32",), here, (n,))
+        ws, ws_bytes = _workspace(workspace, here)
+        call = LogprobCall(_VALUE_TYPES[kind], n, logits.shape[1], m, top, scale,
+                           logits.data_ptr(), logits.stride(0), _dev(tokens, "tokens"),
+                           _dev(logprob, "logprob"), _dev(lse, "lse"), _dev(entropy, "entropy"),
+                           _dev(top_ids, "top_ids"), _dev(top_logprob, "top_logprob"), ws,
+                           ws_bytes)
+        _check(lib().kvr_token_logprobs(self.handle, ctypes.byref(call), _stream(stream)))
+
     # ------------------------------------------- pages shared by requests
 
     def bind_page_refs(self, refs):
@@ -780,11 +950,13 @@ class Residency:
 
 class DraftRing:
     """Drafter visible-window ring (kvr_draft_*) over caller-owned device
-    buffers: ring [n_req][capacity][row_bytes], length and high int32 [n_req]."""
+    buffers: ring [n_req][capacity][row_bytes] (or None, with row_bytes 0, for a
+    ring of K/V layers only), length and high int32 [n_req]."""
 
     def __init__(self, n_req, window, capacity, row_bytes, ring, length, high):
         h = ctypes.c_void_p()
         self.n_req, self.window_rows, self.row_bytes = n_req, window, row_bytes
+        self.capacity, self.kv_heads, self.d_head = capacity, 0, 0
         _check(lib().kvr_draft_create(n_req, window, capacity, row_bytes,
                                       _dev(ring, "ring", max(n_req, 0) * max(capacity, 0) *
                                            max(row_bytes, 0)),
@@ -822,6 +994,91 @@ class DraftRing:
         _check(lib().kvr_draft_window(self.handle, n, _dev(req_ids, "req_ids", 4 * n),
                                       _dev(out, "out", need), _dev(visible, "visible", 4 * n),
                                       _dev(status, "status", 4 * n), _stream(stream)))
+
+    # ------------------------------------------- keys and values in 8 bits
+
+    def bind_kv(self, n_layers, kv_heads, d_head, codes, scales):
+        """K/V layers of the ring: codes (8-bit) [n_layers, n_req, capacity / 64,
+        kv_heads, 2, 64 * d_head] and scales uint8 [n_layers, n_req,
+        capacity / 64, kv_heads, 2].  See kvr_draft_bind_kv."""
+        here = _here()
+        units = max(n_layers, 0) * self.n_req * (self.capacity // DRAFT_BLOCK) * max(kv_heads, 0) * 2
+        _check(lib().kvr_draft_bind_kv(
+            self.handle, n_layers, kv_heads, d_head,
+            _dev_here(codes, "codes", units * DRAFT_BLOCK * max(d_head, 0), here),
+            _dev_here(scales, "scales", units, here)))
+        self.kv_heads, self.d_head = kv_heads, d_head
+
+    def write_kv(self, layer, n, req_ids, k, v, count=None, status=None, stream=None):
+        """New tokens' keys and values [n, rows, kv_heads, d_head] (bf16, fp16 or
+        fp32, one type; strided slices with contiguous heads) of a layer, at the
+        positions after the rows kept; count int32 [n] of them (all, without it).
+        See kvr_draft_write_kv."""
+        here = _here()
+        if getattr(k, "ndim", 4) != 4:
+            raise ValueError(f"k: {k.ndim} dimensions, the call needs [n, rows, kv_heads, d_head]")
+        kind = _typed(k, "k", _VALUE_TYPES, here)
+        shape = (n, int(k.shape[1]), self.kv_heads, self.d_head)
+        _typed(k, "k", (kind,), here, shape)
+        _typed(v, "v", (kind,), here, shape)
+        ks, vs = k.stride(), v.stride()
+        call = DraftWriteCall(layer, _VALUE_TYPES[kind], n, shape[1],
+                              _words(req_ids, "req_ids", n, here),
+                              _words(count, "count", n, here), k.data_ptr(), v.data_ptr(),
+                              ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
+                              _words(status, "status", n, here))
+        _check(lib().kvr_draft_write_kv(self.handle, ctypes.byref(call), _stream(stream)))
+
+    def read_kv(self, layer, n, req_ids, k, v, visible=None, status=None, stream=None):
+        """The visible rows of a layer, oldest first, into k and v [n, window,
+        kv_heads, d_head] (bf16, fp16 or fp32; rows past the window's length are
+        untouched), their number into visible.  See kvr_draft_read_kv."""
+        here = _here()
+        shape = (n, self.window_rows, self.kv_heads, self.d_head)
+        kind = _typed(k, "k", _VALUE_TYPES, here, shape)
+        _typed(v, "v", (kind,), here, shape)
+        _check(lib().kvr_draft_read_kv(self.handle, layer, n, _words(req_ids, "req_ids", n, here),
+                                       _VALUE_TYPES[kind], _dev(k, "k"), _dev(v, "v"),
+                                       _words(visible, "visible", n, here),
+                                       _words(status, "status", n, here), _stream(stream)))
+
+    def advance(self, n, req_ids, rows, count=None, status=None, stream=None):
+        """The tokens written to the K/V layers (count of each entry, or rows) become
+        rows kept.  See kvr_draft_advance."""
+        here = _here()
+        _check(lib().kvr_draft_advance(self.handle, n, _words(req_ids, "req_ids", n, here), rows,
+                                       _words(count, "count", n, here),
+                                       _words(status, "status", n, here), _stream(stream)))
+
+    def attend_workspace(self, n, nq, heads) -> int:
+        """Workspace bytes for attend calls of up to these sizes."""
+        got = lib().kvr_draft_attend_workspace(self.handle, n, nq, heads)
+        return got if got >= 0 else _check(got)
+
+    def attend(self, layer, n, req_ids, q, out, *, scale, mask="causal", count=None, lse=None,
+               status=None, workspace=None, stream=None):
+        """Attention of q [n, nq, heads, d_head] (bf16) over the window of a layer
+        into out of that shape and lse [n, nq, heads]: each query sees the last
+        window rows up to its own token ("causal"), up to the last new token
+        ("block") or up to the last row kept ("kept").  See kvr_draft_attend."""
+        here = _here()
+        if getattr(q, "ndim", 4) != 4:
+            raise ValueError(f"q: {q.ndim} dimensions, the call needs [n, nq, heads, d_head]")
+        kind = ("bfloat16",)
+        _typed(q, "q", kind, here)
+        shape = (n, int(q.shape[1]), int(q.shape[2]), self.d_head)
+        _typed(q, "q", kind, here, shape)
+        _typed(out, "out", kind, here, shape)
+        if lse is not None:
+            _typed(lse, "lse", ("float32",), here, shape[:3])
+        ws, ws_bytes = _workspace(workspace, here)
+        qs = q.stride()
+        call = DraftAttendCall(layer, _choice(mask, "mask", DRAFT_MASKS), n, shape[1], shape[2],
+                               scale, _words(req_ids, "req_ids", n, here),
+                               _words(count, "count", n, here), q.data_ptr(), qs[0], qs[1], qs[2],
+                               _dev(out, "out"), _dev(lse, "lse"),
+                               _words(status, "status", n, here), ws, ws_bytes)
+        _check(lib().kvr_draft_attend(self.handle, ctypes.byref(call), _stream(stream)))
 
 
 class StagingPool:

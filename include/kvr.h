@@ -567,6 +567,140 @@ int kvr_attend_rows(kvr_ctx *ctx, const kvr_attend_call *call, void *stream);
  * one); 0 is possible.  Negative or too large arguments give KVR_E_ARG. */
 int64_t kvr_attend_workspace(int32_t n, int32_t nq, int32_t heads, int32_t d_v, int32_t rows);
 
+/* Rotary positions.  A head's rotated part is d_rot consecutive values, taken
+ * as d_rot / 2 pairs (u, v); at position p pair i becomes
+ *   u' = magnitude * (u cos a - v sin a),  v' = magnitude * (v cos a + u sin a),
+ *   a = 2 pi p frequencies[i]
+ * (inverse: a negated, which takes positions off again, and with them the
+ * gradient of the outputs to that of the inputs).  p * frequency and its whole
+ * turns are taken in 64 bits, the rest in 32; each value is rounded once, to
+ * its type. */
+typedef enum kvr_rope_layout {
+    KVR_ROPE_INTERLEAVED = 0, /* pair i: values 2i and 2i + 1         */
+    KVR_ROPE_HALF = 1,        /* pair i: values i and i + d_rot / 2   */
+} kvr_rope_layout;
+
+/* Heads of one tensor: x and out (device) [n][heads][d_head] of the call's
+ * value type, strides in elements, the last dimension contiguous; values
+ * [at, at + d_rot) of each head are rotated, the others copied.  out == x (with
+ * x's strides) rotates in place and leaves the others alone; otherwise out is
+ * disjoint from the inputs.  heads 0: no such tensor. */
+typedef struct kvr_rotate_part {
+    const void *x;
+    void *out;
+    int64_t x_stride_token;
+    int64_t x_stride_head;
+    int64_t out_stride_token;
+    int64_t out_stride_head;
+    int32_t heads;
+    int32_t d_head;
+    int32_t at;
+    int32_t reserved;  /* must be 0 */
+} kvr_rotate_part;
+
+/* Arguments of kvr_rotate_rows.
+ *   positions (device) int32 [n]; frequencies (device) double [d_rot / 2], in
+ *   turns per position (kvr_rope_frequencies); d_rot even, 2 to 1024
+ *   query, key: the two tensors rotated at the same positions in one launch,
+ *   such as the rope parts of a step's queries and of its new rows' key
+ * Limits: n and each part's heads below 2^24, n * heads below 2^31. */
+typedef struct kvr_rotate_call {
+    int32_t value_type;  /* kvr_value_type */
+    int32_t layout;      /* kvr_rope_layout */
+    int32_t n;
+    int32_t d_rot;
+    float magnitude;
+    int32_t inverse;
+    const int32_t *positions;
+    const double *frequencies;
+    kvr_rotate_part query;
+    kvr_rotate_part key;
+} kvr_rotate_call;
+
+/* Rotates queries and the rope parts of keys before kvr_attend_rows,
+ * kvr_pack_rows, kvr_draft_write_kv or kvr_draft_attend take them.  One kernel;
+ * n = 0 is a no-op. */
+int kvr_rotate_rows(kvr_ctx *ctx, const kvr_rotate_call *call, void *stream);
+
+/* Stretching of the frequencies for contexts longer than a model was trained
+ * on, by `factor` >= 1:
+ *   NONE    f_i = base^(-2i / d_rot) / (2 pi)
+ *   LINEAR  f_i / factor (positions interpolated)
+ *   BASE    base * factor^(d_rot / (d_rot - 2)) in place of base, which
+ *           stretches the slowest pair by factor and the fastest not at all
+ *   RAMP    f_i (1 - r_i) + f_i / factor * r_i, where r_i rises from 0 to 1
+ *           over the pairs between those that turn beta_fast and beta_slow times
+ *           in original_length positions: r_i = clamp((i - low) / (high - low)),
+ *           pair(t) = d_rot ln(original_length / (2 pi t)) / (2 ln base),
+ *           low = floor(pair(beta_fast)), high = ceil(pair(beta_slow)), both
+ *           held to [0, d_rot - 1] and high at least low + 0.001; the magnitude is
+ *           0.1 ln(factor) + 1 (1 in the other kinds) */
+typedef enum kvr_rope_scaling {
+    KVR_ROPE_NONE = 0,
+    KVR_ROPE_LINEAR = 1,
+    KVR_ROPE_BASE = 2,
+    KVR_ROPE_RAMP = 3,
+} kvr_rope_scaling;
+
+/* Host helper: frequencies (host) double [d_rot / 2] and *magnitude (or NULL).
+ * base > 1, factor >= 1; RAMP also takes original_length >= 1 and
+ * beta_fast > beta_slow > 0, the other kinds ignore them. */
+int kvr_rope_frequencies(int32_t d_rot, double base, int32_t scaling, double factor,
+                         int32_t original_length, double beta_fast, double beta_slow,
+                         double *frequencies, float *magnitude);
+
+/* Arguments of kvr_token_logprobs.
+ *   logits (device) [n][vocab] of value_type, rows logits_stride elements apart
+ *   scale  multiplies the logits (1 / temperature); finite and above 0
+ *   tokens (device) int32 [n][m]: given tokens of each row, such as the one a
+ *     drafter proposed; logprob (device) float [n][m] out
+ *   lse, entropy (device) float [n] out, or NULL
+ *   top_ids (device) int32 [n][top], top_logprob (device) float [n][top] out
+ *   workspace (device), aligned to 16 bytes: at least
+ *     kvr_logprob_workspace(n, vocab) bytes; written by the call, so calls that
+ *     may run at once each need their own
+ * Limits: n at most 2^20, vocab 1 to 2^24, m at most 2^16, top at most 64,
+ * n * m below 2^31.  Outputs are contiguous and disjoint from the inputs. */
+typedef struct kvr_logprob_call {
+    int32_t value_type;  /* kvr_value_type */
+    int32_t n;
+    int32_t vocab;
+    int32_t m;
+    int32_t top;
+    float scale;
+    const void *logits;
+    int64_t logits_stride;
+    const int32_t *tokens;
+    float *logprob;
+    float *lse;
+    float *entropy;
+    int32_t *top_ids;
+    float *top_logprob;
+    void *workspace;
+    size_t workspace_bytes;
+} kvr_logprob_call;
+
+/* Log probabilities of given tokens under each row of logits ("Adaptive
+ * DHiSparse", section "How it works", paragraph "Speculative state": the
+ * target model's rows of a verification block, or a drafter's), with x_j the
+ * scaled logits:
+ *   lse = ln sum_j exp(x_j),  logprob = x_token - lse,
+ *   entropy = -sum_j p_j ln p_j,  p_j = exp(x_j - lse)
+ * and the `top` tokens of the largest logits (as given, before the scale) with
+ * their log probabilities, largest first, the lower token first among equals.
+ * Logits of -infinity have probability 0 (log probability -infinity) and are
+ * no alternatives; places past the last alternative get token -1 and
+ * -infinity.  A token outside [0, vocab) has log probability -infinity.  A row of
+ * -infinity alone has lse -infinity, entropy 0 and log probabilities
+ * -infinity; one that holds a NaN or +infinity has NaN in every float and -1 in
+ * every token.  32-bit sums in a fixed order: results do not vary from run to
+ * run.  Two kernels; n = 0 is a no-op. */
+int kvr_token_logprobs(kvr_ctx *ctx, const kvr_logprob_call *call, void *stream);
+
+/* Workspace bytes of kvr_token_logprobs for calls of up to n rows of up to
+ * vocab logits.  Bad sizes give KVR_E_ARG. */
+int64_t kvr_logprob_workspace(int32_t n, int32_t vocab);
+
 /* Pages shared between requests.
  *
  * A ready page is never written again, so several requests may map one
@@ -701,7 +835,9 @@ int kvr_residency_counts(const kvr_residency *res, int64_t *free_pages, int64_t 
  *   kvr_draft_create: ring (device) [n_req][C][row_bytes] (row_bytes a
  *     multiple of 16), length and high (device) int32 [n_req] (rows kept, and
  *     highest position ever written + 1); all caller-owned; the current device
- *     is the ring's.  kvr_draft_reset zeroes length and high (stream-ordered).
+ *     is the ring's.  A drafter that keeps its rows in K/V layers only
+ *     (kvr_draft_bind_kv) passes a NULL ring and row_bytes 0; append and window
+ *     are refused then.  kvr_draft_reset zeroes length and high (stream-ordered).
  *   kvr_draft_append: rows (device) [n][rows_each][row_bytes], rows_each <= C,
  *     appended at positions length .. length + rows_each - 1.
  *   kvr_draft_rollback: keep (device) int32 [n]; status KVR_E_RANGE (nothing
@@ -725,6 +861,139 @@ int kvr_draft_rollback(kvr_draft *d, int32_t n, const int32_t *req_ids, const in
                        int32_t *status, void *stream);
 int kvr_draft_window(kvr_draft *d, int32_t n, const int32_t *req_ids, void *out,
                      int32_t *visible, int32_t *status, void *stream);
+
+/* The drafter's keys and values in 8 bits, in the same ring: position p lies in
+ * slot p mod C of every layer, and length, high, window and rollback are the
+ * ring's.  A ring block is KVR_DRAFT_BLOCK (64) slots; in each layer it holds,
+ * for each K/V head, the keys [64][d_head] and the values [d_head][64] (a
+ * dimension's 64 tokens side by side) as e4m3 codes, and one scale for the keys
+ * and one for the values, a byte b that stands for 2^(b - 127).
+ *   kvr_draft_bind_kv: codes (device, aligned to 16 bytes)
+ *     [n_layers][n_req][C / 64][kv_heads][2][64 * d_head], scales (device) uint8
+ *     [n_layers][n_req][C / 64][kv_heads][2]; C must be a multiple of 64,
+ *     kv_heads 1 to 256, d_head 64, 128 or 256.  Needs every other call on this
+ *     ring out meanwhile.
+ *   kvr_draft_write_kv: new tokens of one layer at positions length ..
+ *     length + count - 1, for kvr_draft_attend to see; length stays, so that
+ *     every layer of a step writes at the same positions, until
+ *     kvr_draft_advance.  A block's scale becomes the smallest power of two
+ *     (2^-100 at least) with which its largest value is at most 448, over
+ *     the rows it then holds: new ones and those kept.  New values are
+ *     rounded once, to the nearest code; codes of rows kept are moved to a
+ *     changed scale, which is exact but for values that fall below the smallest
+ *     normal code.  Slots of a touched block that hold no row (not written yet,
+ *     or dropped by a rollback) become 0, others are left as they were.  A token
+ *     whose key or value in a head holds a NaN or an infinity gets a key of NaN
+ *     codes there and zeros for such values: it shows as NaN in the queries that
+ *     see it, and in no others.
+ *   kvr_draft_read_kv: the visible rows of one layer, oldest first, as
+ *     kvr_draft_window; code * scale in the type asked for (exact in 32 bits
+ *     and in bf16).
+ *   kvr_draft_advance: length += count and high follows, once the layers have
+ *     written their tokens.  What is drafted and rejected is dropped with
+ *     kvr_draft_rollback.
+ * count (device) int32 [n] or NULL (= rows): new tokens of entry i, 0 to rows;
+ * the inputs and outputs of the others are neither read nor written.
+ * status (device) int32 [n] or NULL: KVR_OK; KVR_E_ARG for a request or a count
+ * out of range; KVR_E_STATE for a length below 0 or above high; KVR_E_CAPACITY
+ * for a length that would pass 2^31 - 65; such entries change and write nothing
+ * else. */
+#define KVR_DRAFT_BLOCK 64
+
+int kvr_draft_bind_kv(kvr_draft *d, int32_t n_layers, int32_t kv_heads, int32_t d_head,
+                      void *codes, uint8_t *scales);
+
+/* Arguments of kvr_draft_write_kv: k, v (device) [n][rows][kv_heads][d_head] of
+ * value_type, strides in elements between entries, tokens and heads, the last
+ * dimension contiguous (slices of one projection's output are taken as they
+ * are).  rows at most C - 63, so that no block is touched twice. */
+typedef struct kvr_draft_write_call {
+    int32_t layer;
+    int32_t value_type;  /* kvr_value_type */
+    int32_t n;
+    int32_t rows;
+    const int32_t *req_ids;
+    const int32_t *count;
+    const void *k;
+    const void *v;
+    int64_t k_stride_entry;
+    int64_t k_stride_token;
+    int64_t k_stride_head;
+    int64_t v_stride_entry;
+    int64_t v_stride_token;
+    int64_t v_stride_head;
+    int32_t *status;
+} kvr_draft_write_call;
+
+int kvr_draft_write_kv(kvr_draft *d, const kvr_draft_write_call *call, void *stream);
+
+/* k, v (device) [n][W][kv_heads][d_head] of value_type, contiguous, aligned to
+ * 16 bytes; visible (device) int32 [n] or NULL receives the number of rows. */
+int kvr_draft_read_kv(kvr_draft *d, int32_t layer, int32_t n, const int32_t *req_ids,
+                      int32_t value_type, void *k, void *v, int32_t *visible, int32_t *status,
+                      void *stream);
+
+int kvr_draft_advance(kvr_draft *d, int32_t n, const int32_t *req_ids, int32_t rows,
+                      const int32_t *count, int32_t *status, void *stream);
+
+/* Which rows query j of an entry sees: the last W (or fewer) rows before
+ * position `end`. */
+typedef enum kvr_draft_mask {
+    KVR_DRAFT_CAUSAL = 0, /* end = length + j + 1: the tokens up to its own   */
+    KVR_DRAFT_WHOLE = 1,  /* end = length + count: all of the new tokens      */
+    KVR_DRAFT_KEPT = 2,   /* end = length: none of them (they need no row)   */
+} kvr_draft_mask;
+
+/* Arguments of kvr_draft_attend.
+ *   q (device) bf16 [n][nq][heads][d_head], strides in elements, the last
+ *     dimension contiguous; query head h reads K/V head h / (heads / kv_heads)
+ *   count (device) int32 [n] or NULL (= nq): queries of entry i (and new tokens
+ *     that kvr_draft_write_kv wrote); those past it are not read, their outputs
+ *     not written
+ *   out (device) bf16 [n][nq][heads][d_head] contiguous, aligned to 16 bytes,
+ *     disjoint from the inputs; lse (device) float [n][nq][heads] or NULL
+ *   status as above, and KVR_E_RANGE for an entry of which a query sees a row
+ *     that a later one has overwritten (after a rollback)
+ *   workspace (device), aligned to 16 bytes: at least
+ *     kvr_draft_attend_workspace(d, n, nq, heads) bytes; written by the call, so
+ *     calls that may run at once each need their own
+ * heads is a multiple of kv_heads, at most 4096; n * nq * heads at most 2^22;
+ * with KVR_DRAFT_CAUSAL nq is at most C - W + 1, with KVR_DRAFT_WHOLE at
+ * most C. */
+typedef struct kvr_draft_attend_call {
+    int32_t layer;
+    int32_t mask;  /* kvr_draft_mask */
+    int32_t n;
+    int32_t nq;
+    int32_t heads;
+    float scale;
+    const int32_t *req_ids;
+    const int32_t *count;
+    const void *q;
+    int64_t q_stride_entry;
+    int64_t q_stride_query;
+    int64_t q_stride_head;
+    void *out;
+    float *lse;
+    int32_t *status;
+    void *workspace;
+    size_t workspace_bytes;
+} kvr_draft_attend_call;
+
+/* Attention of new tokens' queries over the drafter's window:
+ *   s_j = scale * (q . key_j),  out = sum_j exp(s_j - lse) value_j,
+ *   lse = ln sum_j exp(s_j)
+ * over the rows the query sees; one that sees none gets out = 0 and
+ * lse = -infinity.  Codes are exact in bf16; products, sums, maxima and
+ * exponentials in 32 bits; probabilities are rounded to bf16 before their product
+ * with the values.  Rows may be cut into shares that are joined in a fixed
+ * order: results do not vary from run to run (another n, nq or heads may cut
+ * them otherwise).  One kernel, or two with shares; n = 0 is a no-op. */
+int kvr_draft_attend(kvr_draft *d, const kvr_draft_attend_call *call, void *stream);
+
+/* Workspace bytes of kvr_draft_attend calls of up to n entries, nq queries and
+ * heads heads on this ring; 0 is possible.  Bad sizes give KVR_E_ARG. */
+int64_t kvr_draft_attend_workspace(const kvr_draft *d, int32_t n, int32_t nq, int32_t heads);
 
 /* Verification staging reuse: a target layer's staging buffer is handed out
  * again only after the kernels that read it have finished.  A pool of n_buffers caller-owned buffers, named by
@@ -780,6 +1049,8 @@ typedef enum kvr_kernel {
     KVR_KERNEL_ATTEND = 8,   /* attention over resolved rows, and the join of its shares */
     KVR_KERNEL_PACK = 9,     /* rows of new tokens */
     KVR_KERNEL_PAGES = 10,   /* fork, release, page copies, free list, compaction */
+    KVR_KERNEL_ROTATE = 11,  /* rotary positions */
+    KVR_KERNEL_LOGPROB = 12, /* log probabilities, and the join of their parts */
 } kvr_kernel;
 
 int kvr_timing_begin(kvr_ctx *ctx, int32_t capacity);
