@@ -29,7 +29,9 @@ namespace {
 
 constexpr int NT = 256;
 constexpr int kRun = 8;        // consecutive logits of a thread: one piece
-constexpr int kList = 1024;    // logits that are ranked
+constexpr int kBatch = 4;      // pieces of a thread in flight
+constexpr int kTops = 8;       // maxima of a thread in flight
+constexpr int kList = 1024;    // logits that are ranked, and runs that are read for them
 constexpr float kInf = __builtin_inff();
 
 struct LogprobArgs {
@@ -91,24 +93,38 @@ __global__ __launch_bounds__(NT) void part_kernel(LogprobArgs a)
     const int p1 = p0 + a.per < a.pieces ? p0 + a.per : a.pieces;
     const float factor = a.c.scale * 1.44269504088896340736f;
     float m = -kInf, l = 0.f, u = 0.f;
-    for (int p = p0 + threadIdx.x; p < p1; p += NT) {
-        float x[kRun];
-        load_piece(a, row, p, x);
-        float most = -kInf;
+    auto add = [&](auto &x) __attribute__((always_inline)) {  // [pieces][kRun]
+        float to = m;
 #pragma unroll
-        for (int k = 0; k < kRun; ++k)
-            most = fmaxf(most, x[k]);
-        const float to = fmaxf(m, most);
+        for (auto &piece : x)
+#pragma unroll
+            for (float y : piece)
+                to = fmaxf(to, y);
         raise(factor, m, l, u, to);
         m = to;
         const float ref = to == -kInf ? 0.f : to;
 #pragma unroll
-        for (int k = 0; k < kRun; ++k) {
-            const float d = (x[k] - ref) * factor;
-            const float e = exp2_hw(d);
-            l += e;
-            u -= e > 0.f ? e * d : 0.f;
-        }
+        for (auto &piece : x)
+#pragma unroll
+            for (float y : piece) {
+                const float d = (y - ref) * factor;
+                const float e = exp2_hw(d);
+                l += e;
+                u -= e > 0.f ? e * d : 0.f;
+            }
+    };
+    int p = p0 + threadIdx.x;
+    for (; p + (kBatch - 1) * NT < p1; p += kBatch * NT) {
+        float x[kBatch][kRun];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            load_piece(a, row, p + k * NT, x[k]);
+        add(x);
+    }
+    for (; p < p1; p += NT) {
+        float x[1][kRun];
+        load_piece(a, row, p, x[0]);
+        add(x);
     }
     if (a.c.top > 0)
         a.tops[(int64_t)blockIdx.x * NT + threadIdx.x] = m;
@@ -138,20 +154,44 @@ __device__ __forceinline__ bool before(float x, int i, float y, int j)
     return x > y || (x == y && i < j);
 }
 
-template <typename T>
-__global__ __launch_bounds__(NT) void row_kernel(LogprobArgs a)
+// Floats as integers of the same order.
+__device__ __forceinline__ uint32_t key_of(float x)
 {
+    const uint32_t u = __float_as_uint(x);
+    return u ^ (u >> 31 ? 0xFFFFFFFFu : 0x80000000u);
+}
+
+// The n-th largest of the 64 lanes' values, bit by bit from the top.
+__device__ __forceinline__ float nth_largest(float x, int n)
+{
+    const uint32_t key = key_of(x);
+    uint32_t found = 0;
+#pragma unroll
+    for (int bit = 31; bit >= 0; --bit) {
+        const uint32_t trial = found | 1u << bit;
+        if (__popcll(__ballot(key >= trial)) >= n)
+            found = trial;
+    }
+    return __uint_as_float(found ^ (found >> 31 ? 0x80000000u : 0xFFFFFFFFu));
+}
+
+// NR threads a row.
+template <typename T, int NR>
+__global__ __launch_bounds__(NR) void row_kernel(LogprobArgs a)
+{
+    constexpr int kWaves = NR / 64;
     __shared__ float sValue[kList];
     __shared__ int sToken[kList];
-    __shared__ int sCount;
-    __shared__ float sM[NT / 64];
-    __shared__ int sI[NT / 64];
+    __shared__ int sRun[kList];
+    __shared__ int sRuns, sCount;
+    __shared__ float sM[kWaves];
+    __shared__ int sI[kWaves];
     const int64_t r = blockIdx.x;
     const int tid = threadIdx.x, lane = lane_id(), wave = wave_id();
     const T *row = static_cast<const T *>(a.c.logits) + r * a.c.logits_stride;
     const float factor = a.c.scale * 1.44269504088896340736f;
     if (tid == 0)
-        sCount = 0;
+        sRuns = sCount = 0;
 
     // the row's sums, joined in a fixed order by every wave
     float m = -kInf, l = 0.f, u = 0.f;
@@ -180,7 +220,7 @@ __global__ __launch_bounds__(NT) void row_kernel(LogprobArgs a)
         if (a.c.entropy)
             a.c.entropy[r] = bad ? nan : m == -kInf ? 0.f : log_l + kLn2 * (u / l);
     }
-    for (int k = tid; k < a.c.m; k += NT) {
+    for (int k = tid; k < a.c.m; k += NR) {
         const int token = a.c.tokens[r * a.c.m + k];
         const float x = token >= 0 && token < a.c.vocab ? (float)row[token] : -kInf;
         a.c.logprob[r * a.c.m + k] = logprob(x);
@@ -190,40 +230,52 @@ __global__ __launch_bounds__(NT) void row_kernel(LogprobArgs a)
         return;
     int32_t *ids = a.c.top_ids + r * top;
     float *probs = a.c.top_logprob + r * top;
-    for (int k = tid; k < top; k += NT) {
+    for (int k = tid; k < top; k += NR) {
         ids[k] = -1;
         probs[k] = bad ? nan : -kInf;
     }
     if (bad || m == -kInf)
         return;
 
-    // groups: the lanes; a wave takes every fourth row of 64 maxima
+    // the threads' largest logits, several in flight; groups: the lanes
     const float *tops = a.tops + r * a.shares * NT;
+    const int runs = a.shares * NT;
+    auto for_tops = [&](auto each) __attribute__((always_inline)) {
+        for (int q = tid; q < runs; q += NR * kTops) {
+            float t[kTops];
+#pragma unroll
+            for (int k = 0; k < kTops; ++k)
+                t[k] = q + k * NR < runs ? tops[q + k * NR] : -kInf;
+#pragma unroll
+            for (int k = 0; k < kTops; ++k)
+                each(q + k * NR, t[k]);
+        }
+    };
     float most = -kInf;
-    for (int s = wave; s < a.shares * (NT / 64); s += NT / 64)
-        most = fmaxf(most, tops[s * 64 + lane]);
+    for_tops([&](int, float t) { most = fmaxf(most, t); });
     sValue[tid] = most;
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < NT / 64; ++k)
+    for (int k = 0; k < kWaves; ++k)
         most = fmaxf(most, sValue[k * 64 + lane]);
-    // the lane's place among the 64
-    int place = 0;
-    for (int k = 0; k < 64; ++k) {
-        const float y = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(most), k));
-        place += before(y, k, most, lane);
-    }
-    // (uniform: every wave has the same maxima)
-    const uint64_t at = __ballot(place == top - 1);
-    const float bound = __shfl(most, __ffsll((unsigned long long)at) - 1);
+    const float bound = nth_largest(most, top);  // (uniform: every wave has the same maxima)
+    for_tops([&](int q, float t) {
+        if (t >= bound && t > -kInf) {
+            const int n = atomicAdd(&sRuns, 1);
+            if (n < kList)
+                sRun[n] = q;
+        }
+    });
     __syncthreads();
-    for (int s = 0; s < a.shares; ++s) {
-        const float t = tops[s * NT + tid];
-        if (t < bound || t == -kInf)
-            continue;
-        const int p0 = s * a.per;
-        const int p1 = p0 + a.per < a.pieces ? p0 + a.per : a.pieces;
-        for (int p = p0 + tid; p < p1; p += NT) {
+    const int found = sRuns;
+    const int each = a.per / NT;  // pieces of a run
+    if (found <= kList)
+        for (int q = tid; q < found * each; q += NR) {
+            const int run = sRun[q / each], s = run / NT;
+            const int p = s * a.per + q % each * NT + run % NT;
+            const int p1 = (s + 1) * a.per < a.pieces ? (s + 1) * a.per : a.pieces;
+            if (p >= p1)
+                continue;
             float x[kRun];
             load_piece(a, row, p, x);
 #pragma unroll
@@ -236,11 +288,10 @@ __global__ __launch_bounds__(NT) void row_kernel(LogprobArgs a)
                     }
                 }
         }
-    }
     __syncthreads();
     const int count = sCount;
-    if (count <= kList) {
-        for (int n = tid; n < count; n += NT) {
+    if (found <= kList && count <= kList) {
+        for (int n = tid; n < count; n += NR) {
             const float x = sValue[n];
             const int token = sToken[n];
             int rank = 0;
@@ -259,7 +310,7 @@ __global__ __launch_bounds__(NT) void row_kernel(LogprobArgs a)
     for (int k = 0; k < top; ++k) {
         float x = -kInf;
         int token = a.c.vocab;
-        for (int p = tid; p < a.pieces; p += NT) {
+        for (int p = tid; p < a.pieces; p += NR) {
             float y[kRun];
             load_piece(a, row, p, y);
 #pragma unroll
@@ -287,7 +338,7 @@ __global__ __launch_bounds__(NT) void row_kernel(LogprobArgs a)
         x = sM[0];
         token = sI[0];
 #pragma unroll
-        for (int w = 1; w < NT / 64; ++w)
+        for (int w = 1; w < kWaves; ++w)
             if (before(sM[w], sI[w], x, token)) {
                 x = sM[w];
                 token = sI[w];
@@ -322,7 +373,11 @@ hipError_t launch_typed(const kvr_ctx *c, const LogprobArgs &a, hipStream_t s)
                                 dim3((unsigned)((int64_t)a.c.n * a.shares)), dim3(NT), 0, s, a);
     if (e != hipSuccess)
         return e;
-    return launch(c, KVR_KERNEL_LOGPROB, row_kernel<T>, dim3((unsigned)a.c.n), dim3(NT), 0, s, a);
+    if (a.shares * NT <= 256 * kTops)
+        return launch(c, KVR_KERNEL_LOGPROB, row_kernel<T, 256>, dim3((unsigned)a.c.n), dim3(256), 0,
+                      s, a);
+    return launch(c, KVR_KERNEL_LOGPROB, row_kernel<T, 1024>, dim3((unsigned)a.c.n), dim3(1024), 0, s,
+                  a);
 }
 
 }  // namespace

@@ -95,7 +95,8 @@ __device__ __forceinline__ Entry attend_entry(const AttendArgs &a, int i)
 }
 
 template <int D, int MB, int NW, bool SPLIT>
-__global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 2)))
+void attend_kernel(AttendArgs a)
 {
     constexpr int kRows = 16 * MB;          // query rows of a wave
     constexpr int kSteps = D / 32;          // MFMA steps of a score
@@ -158,6 +159,10 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
                 for (int k = 0; k < 8; ++k)
                     qf[mb][s][k] = p[k];
             }
+            // a negative scale goes into the queries, so that the largest product
+            // is the largest score
+            if (a.c.scale < 0.f)
+                qf[mb][s] = -qf[mb][s];
         }
     }
 
@@ -172,38 +177,41 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
             o[c][mb] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    struct Raw {
-        u32x4 k[4][kLoads], v[kCols];
-        uint32_t k_scale, v_scale;
-    };
+    // A block's keys and values.  The next keys are loaded once the scores are
+    // taken, the next values after the products, into the same registers.
+    u32x4 k[4][kLoads], v[kCols];
+    uint32_t k_scale = 0, v_scale = 0;
     const int64_t head_bytes = 2 * kBlock * D;
     const int64_t first = (int64_t)e.r * a.w.blocks * a.w.kv_heads + kvh;
     const int k_at = ((col >> 2) * 16 + (col & 3)) * D + grp * 16;
     const int v_at = kBlock * D + col * kBlock + grp * 16;
-    auto load = [&](Raw &raw, int b) __attribute__((always_inline)) {
-        const int64_t at = first + (int64_t)(b % a.w.blocks) * a.w.kv_heads;
-        const uint8_t *p = a.w.codes + at * head_bytes;
+    auto at_block = [&](int b) { return first + (int64_t)(b % a.w.blocks) * a.w.kv_heads; };
+    auto load_keys = [&](int64_t at) __attribute__((always_inline)) {
+        const uint8_t *p = a.w.codes + at * head_bytes + k_at;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int n = 0; n < kLoads; ++n)
-                raw.k[j][n] = *reinterpret_cast<const u32x4 *>(p + k_at + j * 4 * D + n * 64);
+                k[j][n] = *reinterpret_cast<const u32x4 *>(p + j * 4 * D + n * 64);
+        k_scale = a.w.scales[at * 2];
+    };
+    auto load_values = [&](int64_t at) __attribute__((always_inline)) {
+        const uint8_t *p = a.w.codes + at * head_bytes + v_at;
 #pragma unroll
         for (int c = 0; c < kCols; ++c)
-            raw.v[c] = *reinterpret_cast<const u32x4 *>(p + v_at + c * 16 * kBlock);
-        raw.k_scale = a.w.scales[at * 2];
-        raw.v_scale = a.w.scales[at * 2 + 1];
+            v[c] = *reinterpret_cast<const u32x4 *>(p + c * 16 * kBlock);
+        v_scale = a.w.scales[at * 2 + 1];
     };
 
-    const float to_log2 = a.c.scale * 1.44269504088896340736f;
+    // (at least the smallest normal: a scale of 0 leaves masked scores at -infinity)
+    const float to_log2 = fmaxf(fabsf(a.c.scale) * 1.44269504088896340736f, 1e-37f);
     const int step = SPLIT ? NW : 1;
     int b = SPLIT ? b0 + wave : b0;
-    Raw raw, next;
-    if (b < b1)
-        load(raw, b);
+    if (b < b1) {
+        load_keys(at_block(b));
+        load_values(at_block(b));
+    }
     for (; b < b1; b += step) {
-        if (b + step < b1)
-            load(next, b + step);
         f32x4 s[4][MB];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -212,31 +220,38 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
                 s[j][mb] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int st = 0; st < kSteps; ++st) {
-                const u32x4 w = raw.k[j][st / 2];
+                const u32x4 w = k[j][st / 2];
                 const frag kf = widen(w[(st & 1) * 2], w[(st & 1) * 2 + 1], 1.f);
 #pragma unroll
                 for (int mb = 0; mb < MB; ++mb)
                     s[j][mb] = mfma(kf, qf[mb][st], s[j][mb]);
             }
         }
-        const float factor = to_log2 * scale_value(raw.k_scale);
-        const bool whole = b >= full0 && b < full1;
+        const float factor = fmaxf(to_log2 * scale_value(k_scale), 1e-37f);
+        const bool more = b + step < b1;
+        const int64_t at_next = at_block(b + step);
+        if (more)
+            load_keys(at_next);
+        if (b < full0 || b >= full1) {
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int pos = b * kBlock + grp * 16 + j * 4 + x;
+                        if (pos < lo[mb] || pos >= hi[mb])
+                            s[j][mb][x] = -__builtin_inff();
+                    }
+        }
         frag pf[2][MB];
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
-            float top = -__builtin_inff();
+            float top = fmaxf(fmaxf(s[0][mb][0], s[0][mb][1]), s[0][mb][2]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    s[j][mb][k] *= factor;
-                    if (!whole) {
-                        const int pos = b * kBlock + grp * 16 + j * 4 + k;
-                        s[j][mb][k] = pos >= lo[mb] && pos < hi[mb] ? s[j][mb][k]
-                                                                    : -__builtin_inff();
-                    }
-                    top = fmaxf(top, s[j][mb][k]);
-                }
+            for (int x = 3; x < 15; x += 2)
+                top = fmaxf(fmaxf(top, s[x / 4][mb][x % 4]), s[(x + 1) / 4][mb][(x + 1) % 4]);
+            top = fmaxf(top, s[3][mb][3]) * factor;
             if (__any(top > m[mb] + kSlack)) {
                 top = fmaxf(top, __shfl_xor(top, 16));
                 top = fmaxf(top, __shfl_xor(top, 32));
@@ -252,24 +267,25 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float p = exp2_hw(s[j][mb][k] - ref);
+                for (int x = 0; x < 4; ++x) {
+                    const float p = exp2_hw(fmaf(s[j][mb][x], factor, -ref));
                     l[mb] += p;
-                    // rounded to bf16 for the product (at most 2^-9 of it)
-                    pf[j / 2][mb][(j & 1) * 4 + k] = (__bf16)p;
+                    // rounded to bf16 for the product (at most 2^-8 of it)
+                    pf[j / 2][mb][(j & 1) * 4 + x] = (__bf16)p;
                 }
         }
-        const float v_unit = scale_value(raw.v_scale);
+        const float v_unit = scale_value(v_scale);
 #pragma unroll
         for (int c = 0; c < kCols; ++c)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const frag vf = widen(raw.v[c][h * 2], raw.v[c][h * 2 + 1], v_unit);
+                const frag vf = widen(v[c][h * 2], v[c][h * 2 + 1], v_unit);
 #pragma unroll
                 for (int mb = 0; mb < MB; ++mb)
                     o[c][mb] = mfma(vf, pf[h][mb], o[c][mb]);
             }
-        raw = next;
+        if (more)
+            load_values(at_next);
     }
 
     const int64_t part = (int64_t)unit * a.shares + share;
@@ -280,12 +296,12 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
         l[mb] += __shfl_xor(l[mb], 32);
     }
     // row x of the head, value columns d .. d + 3 of the unnormalised sums
-    auto write = [&](int x, int d, float mx, float lx, f32x4 v) __attribute__((always_inline)) {
+    auto write = [&](int x, int d, float mx, float lx, f32x4 sums) __attribute__((always_inline)) {
         if (a.shares > 1) {
             const int64_t ps = part * unit_rows + x;
             if (d == 0)
                 *reinterpret_cast<float2 *>(a.stat + 2 * ps) = make_float2(mx, lx);
-            *reinterpret_cast<f32x4 *>(a.partial + ps * D + d) = v;
+            *reinterpret_cast<f32x4 *>(a.partial + ps * D + d) = sums;
             return;
         }
         const int j = x / a.group, h = kvh * a.group + x % a.group;
@@ -296,7 +312,7 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
         bf16x4 r;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            r[k] = (__bf16)(v[k] * inv);
+            r[k] = (__bf16)(sums[k] * inv);
         *reinterpret_cast<bf16x4 *>(static_cast<__bf16 *>(a.c.out) + at * D + d) = r;
     };
     if constexpr (!SPLIT) {
@@ -332,7 +348,7 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
 #pragma unroll
             for (int w = 0; w < NW; ++w)
                 mx = fmaxf(mx, sStat[(w * kRows + row) * 2]);
-            f32x4 v = {0.f, 0.f, 0.f, 0.f};
+            f32x4 sums = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
                 const int at = w * kRows + row;
@@ -340,9 +356,9 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(AttendArgs a)
                 // (a wave without a score above -infinity has sums of 0 or NaN)
                 const float weight = mw == -__builtin_inff() ? 1.f : exp2_hw(mw - mx);
                 lx += weight * lw;
-                v += weight * *reinterpret_cast<const f32x4 *>(&sO[at * kStride + d]);
+                sums += weight * *reinterpret_cast<const f32x4 *>(&sO[at * kStride + d]);
             }
-            write(x0 + row, d, mx, lx, v);
+            write(x0 + row, d, mx, lx, sums);
         }
     }
 }
@@ -428,18 +444,23 @@ __global__ __launch_bounds__(kJoinWaves * 64) void join_kernel(AttendArgs a)
 constexpr int64_t kUnits = 256;  // compute units
 constexpr int kWaves = 4;
 
+// Query rows of a wave with many of them, in blocks of 16: as many as two waves
+// a SIMD have registers for (one, with heads of 256).
+constexpr int blocks_of_16(int d) { return d == 256 ? 1 : 2; }
+
 int64_t partial_bytes(int64_t rows, int32_t d) { return rows * (d + 2) * (int64_t)sizeof(float); }
 
 template <int D>
 hipError_t launch_dim(const AttendArgs &a, const DraftPlan &p, dim3 grid, hipStream_t s)
 {
+    constexpr int MB = blocks_of_16(D);
     hipError_t e;
     if (!p.split)
-        e = launch(nullptr, 0, attend_kernel<D, 2, kWaves, false>, grid, dim3(kWaves * 64), 0, s, a);
+        e = launch(nullptr, 0, attend_kernel<D, MB, kWaves, false>, grid, dim3(kWaves * 64), 0, s, a);
     else if (p.blocks_of_16 == 1)
         e = launch(nullptr, 0, attend_kernel<D, 1, kWaves, true>, grid, dim3(kWaves * 64), 0, s, a);
     else
-        e = launch(nullptr, 0, attend_kernel<D, 2, kWaves, true>, grid, dim3(kWaves * 64), 0, s, a);
+        e = launch(nullptr, 0, attend_kernel<D, MB, kWaves, true>, grid, dim3(kWaves * 64), 0, s, a);
     if (e != hipSuccess || a.shares == 1)
         return e;
     const int64_t rows = (int64_t)a.c.n * a.c.nq * a.c.heads;
@@ -454,7 +475,7 @@ DraftPlan draft_plan(int32_t n, int32_t nq, int32_t heads, int32_t kv_heads, int
     DraftPlan p{};
     const int64_t rows = (int64_t)nq * (heads / kv_heads);  // of an entry and head
     const int64_t units = (int64_t)n * kv_heads;
-    p.blocks_of_16 = rows <= 16 ? 1 : 2;
+    p.blocks_of_16 = rows <= 16 ? 1 : blocks_of_16(d_head);
     p.waves = kWaves;
     p.split = rows < 128;
     const int64_t tile = 16 * p.blocks_of_16 * (p.split ? 1 : kWaves);
