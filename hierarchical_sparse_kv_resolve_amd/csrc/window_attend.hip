@@ -10,19 +10,35 @@
 // and l and the sums are scaled down.
 //
 // A wave owns MB blocks of 16 query rows of one K/V head and walks ring blocks
-// of 64 tokens, 16-byte loads straight from memory into the operands of
-// 16x16x32 MFMA, the next block's on their way beside the products:
+// of 64 tokens by 16x16x32 MFMA:
 //   scores  (keys x queries) 4 tiles of 16 tokens.  Row 4 g + k of tile j is
 //           token 16 g + 4 j + k, so that lane group g ends up with the
 //           probabilities of tokens 16 g .. 16 g + 15,
 //   values  which are, 8 at a time, the other operand's columns: the values lie
 //           [d][64 tokens], and a lane reads the same 16 tokens of a dimension.
-// Nothing passes through LDS and no wave waits for another; a query row stays in
-// one lane (mod 16), so maxima and sums are the lane's own but for one exchange
-// between lane groups where a reference changes, and one at the end.
+// Probabilities never leave their lane; a query row stays in one lane (mod 16), so
+// maxima and sums are the lane's own but for one exchange between lane groups where
+// a reference changes, and one at the end.
 //
 // Codes become bf16 exactly, with their block's scale (a power of two): the
 // keys' is folded into log2(e) * scale, the values' into the conversion.
+//
+// Two kernels (draft_plan says which, with both sides): split_kernel, whose waves
+// have the same query rows, take different blocks straight from memory and join
+// their sums at the end; and shared_kernel, whose waves have query rows of their own
+// and share each block, converted once, in LDS.
+//
+// What bounds them (one MI355X):
+//   64 requests x 32 heads (8 K/V) of 128, windows of 4096    97 us, 5.5 TB/s: HBM
+//   one prompt chunk of 2048 tokens, the same heads and window  140 us, 980
+//   TFLOP/s, 0.81 of a large bf16 product: by its counters the matrix units are
+//   busy for 45 % of the cycles and vector instructions issue in 56 %; a matrix
+//   instruction keeps the issue port for half of its time, so the two hardly
+//   overlap
+//   one request's token, window 1024   11 us: latency of 3 blocks a wave
+// (Tried for the prompt chunk: every wave on its own from memory 186 us, its
+// loads a key apart; codes in LDS, converted by each wave, 146; with the
+// exponentials beside the next block's products 154; 4 waves a workgroup 153.)
 #include "block.h"
 #include "draft.h"
 #include "kvr_internal.h"
@@ -94,272 +110,569 @@ __device__ __forceinline__ Entry attend_entry(const AttendArgs &a, int i)
     return e;
 }
 
-template <int D, int MB, int NW, bool SPLIT>
-__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 2)))
-void attend_kernel(AttendArgs a)
+// The work of a workgroup: a share of the tokens for a tile of the query rows of
+// an entry and head.  Workgroups are dealt to the 8 XCDs in turn: each XCD takes a
+// run of neighbours, so that its L2 serves the tokens of one head to all of them.
+struct Job {
+    int i, kvh, tile, share;
+    int64_t part;  // (entry, head, share)
+};
+
+__device__ __forceinline__ bool job_of(const AttendArgs &a, Job &j)
 {
-    constexpr int kRows = 16 * MB;          // query rows of a wave
-    constexpr int kSteps = D / 32;          // MFMA steps of a score
-    constexpr int kLoads = D / 64;          // 16-byte loads of a key in a lane
-    constexpr int kCols = D / 16;           // blocks of 16 value columns
-    __shared__ __attribute__((aligned(16))) float sO[SPLIT ? NW * kRows * (D + 4) : 1];
-    __shared__ float sStat[SPLIT ? NW * kRows * 2 : 1];
-
-    const int lane = lane_id(), col = lane & 15, grp = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(wave_id());
-
-    // Workgroups are dealt to the 8 XCDs in turn: each XCD takes a run of
-    // neighbours, so that its L2 serves the tokens of one head to all of them.
     const uint32_t job = (blockIdx.x & 7) * ((a.jobs + 7) / 8) + blockIdx.x / 8;
     if (job >= a.jobs)
-        return;
-    const int share = (int)(job % (uint32_t)a.shares);
+        return false;
+    j.share = (int)(job % (uint32_t)a.shares);
     const uint32_t rest = job / (uint32_t)a.shares;
-    const int tile = (int)(rest % (uint32_t)a.tiles);
-    const uint32_t unit = rest / (uint32_t)a.tiles;  // entry and K/V head
-    const int i = (int)(unit / (uint32_t)a.w.kv_heads), kvh = (int)(unit % (uint32_t)a.w.kv_heads);
+    j.tile = (int)(rest % (uint32_t)a.tiles);
+    const uint32_t unit = rest / (uint32_t)a.tiles;
+    j.i = (int)(unit / (uint32_t)a.w.kv_heads);
+    j.kvh = (int)(unit % (uint32_t)a.w.kv_heads);
+    j.part = (int64_t)unit * a.shares + j.share;
+    return true;
+}
 
-    const Entry e = attend_entry(a, i);
-    if (a.c.status && kvh == 0 && tile == 0 && share == 0 && threadIdx.x == 0)
-        a.c.status[i] = e.status;
-    const int x0 = SPLIT ? tile * kRows : (tile * NW + wave) * kRows;
-    const int rows = e.count * a.group;  // of the entry and head
-    if (e.status != KVR_OK || x0 >= rows)
-        return;  // (with SPLIT, the whole workgroup)
+// Blocks of tokens that query rows [x0, x1) see, [b0, b1), and those that all of
+// them see whole, [full0, full1).
+struct Span {
+    int b0, b1, full0, full1;
+};
 
-    // blocks of tokens that the wave's rows see, and which of them all rows see whole
-    const int j0 = x0 / a.group;
-    const int j1 = (x0 + kRows < rows ? x0 + kRows - 1 : rows - 1) / a.group;
-    const int end0 = end_of(a.c.mask, e, j0), end1 = end_of(a.c.mask, e, j1);
+__device__ __forceinline__ Span span_of(const AttendArgs &a, const Entry &e, int x0, int x1)
+{
+    const int end0 = end_of(a.c.mask, e, x0 / a.group);
+    const int end1 = end_of(a.c.mask, e, (x1 - 1) / a.group);
     const int lo0 = end0 > a.w.W ? end0 - a.w.W : 0, lo1 = end1 > a.w.W ? end1 - a.w.W : 0;
-    const int b_first = lo0 / kBlock, b_last = (end1 + kBlock - 1) / kBlock;
-    const int per = (b_last - b_first + a.shares - 1) / a.shares;
-    const int b0 = b_first + share * per;
-    const int b1 = b0 + per < b_last ? b0 + per : b_last;
-    const int full0 = (lo1 + kBlock - 1) / kBlock, full1 = end0 / kBlock;
+    return {lo0 / kBlock, (end1 + kBlock - 1) / kBlock, (lo1 + kBlock - 1) / kBlock,
+            end0 / kBlock};
+}
 
-    // queries; past the last row: that row's, whose results are not written
-    int hi[MB], lo[MB];  // tokens that the lane's row of each block sees
-    frag qf[MB][kSteps];
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb) {
-        const int x = x0 + mb * 16 + col, xc = x < rows ? x : rows - 1;
-        const int j = xc / a.group, h = kvh * a.group + xc % a.group;
-        hi[mb] = end_of(a.c.mask, e, j);
-        lo[mb] = hi[mb] > a.w.W ? hi[mb] - a.w.W : 0;
-        const __bf16 *q = static_cast<const __bf16 *>(a.c.q) + i * a.c.q_stride_entry +
-                          j * a.c.q_stride_query + h * a.c.q_stride_head;
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            const __bf16 *p = q + s / 2 * 64 + grp * 16 + (s & 1) * 8;
-            if (a.wide) {
-                qf[mb][s] = *reinterpret_cast<const frag *>(p);
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    qf[mb][s][k] = p[k];
-            }
-            // a negative scale goes into the queries, so that the largest product
-            // is the largest score
-            if (a.c.scale < 0.f)
-                qf[mb][s] = -qf[mb][s];
-        }
-    }
+// A share of them.
+__device__ __forceinline__ void cut(Span &s, int share, int shares)
+{
+    const int per = (s.b1 - s.b0 + shares - 1) / shares;
+    s.b0 += share * per;
+    s.b1 = s.b0 + per < s.b1 ? s.b0 + per : s.b1;
+}
 
-    float m[MB], l[MB];
+// A wave's query rows x0 .. x0 + 16 MB - 1 of an entry and head.
+template <int D, int MB>
+struct Rows {
+    static constexpr int kSteps = D / 32;  // MFMA steps of a score
+    static constexpr int kCols = D / 16;   // blocks of 16 value columns
+    static constexpr int kKeys = D / 64;   // 16-byte pieces of a key in a lane
+    typedef f32x4 Scores[4][MB];           // of a block's 4 tiles of 16 tokens
+    frag q[MB][kSteps];
+    int lo[MB], hi[MB];  // tokens that the lane's row of each block sees
+    // m (0 before the first score), how far above it scores may be (-infinity
+    // before the first), the lane's share of l
+    float ref[MB], slack[MB], l[MB];
     f32x4 o[kCols][MB];
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb) {
-        m[mb] = -__builtin_inff();
-        l[mb] = 0.f;
-#pragma unroll
-        for (int c = 0; c < kCols; ++c)
-            o[c][mb] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
+    u32x4 p[2][MB];  // probabilities: 8 tokens of each lane group in a frag
 
-    // A block's keys and values.  The next keys are loaded once the scores are
-    // taken, the next values after the products, into the same registers.
-    u32x4 k[4][kLoads], v[kCols];
-    uint32_t k_scale = 0, v_scale = 0;
-    const int64_t head_bytes = 2 * kBlock * D;
-    const int64_t first = (int64_t)e.r * a.w.blocks * a.w.kv_heads + kvh;
-    const int k_at = ((col >> 2) * 16 + (col & 3)) * D + grp * 16;
-    const int v_at = kBlock * D + col * kBlock + grp * 16;
-    auto at_block = [&](int b) { return first + (int64_t)(b % a.w.blocks) * a.w.kv_heads; };
-    auto load_keys = [&](int64_t at) __attribute__((always_inline)) {
-        const uint8_t *p = a.w.codes + at * head_bytes + k_at;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int n = 0; n < kLoads; ++n)
-                k[j][n] = *reinterpret_cast<const u32x4 *>(p + j * 4 * D + n * 64);
-        k_scale = a.w.scales[at * 2];
-    };
-    auto load_values = [&](int64_t at) __attribute__((always_inline)) {
-        const uint8_t *p = a.w.codes + at * head_bytes + v_at;
-#pragma unroll
-        for (int c = 0; c < kCols; ++c)
-            v[c] = *reinterpret_cast<const u32x4 *>(p + c * 16 * kBlock);
-        v_scale = a.w.scales[at * 2 + 1];
-    };
-
-    // (at least the smallest normal: a scale of 0 leaves masked scores at -infinity)
-    const float to_log2 = fmaxf(fabsf(a.c.scale) * 1.44269504088896340736f, 1e-37f);
-    const int step = SPLIT ? NW : 1;
-    int b = SPLIT ? b0 + wave : b0;
-    if (b < b1) {
-        load_keys(at_block(b));
-        load_values(at_block(b));
-    }
-    for (; b < b1; b += step) {
-        f32x4 s[4][MB];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-#pragma unroll
-            for (int mb = 0; mb < MB; ++mb)
-                s[j][mb] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int st = 0; st < kSteps; ++st) {
-                const u32x4 w = k[j][st / 2];
-                const frag kf = widen(w[(st & 1) * 2], w[(st & 1) * 2 + 1], 1.f);
-#pragma unroll
-                for (int mb = 0; mb < MB; ++mb)
-                    s[j][mb] = mfma(kf, qf[mb][st], s[j][mb]);
-            }
-        }
-        const float factor = fmaxf(to_log2 * scale_value(k_scale), 1e-37f);
-        const bool more = b + step < b1;
-        const int64_t at_next = at_block(b + step);
-        if (more)
-            load_keys(at_next);
-        if (b < full0 || b >= full1) {
-#pragma unroll
-            for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int pos = b * kBlock + grp * 16 + j * 4 + x;
-                        if (pos < lo[mb] || pos >= hi[mb])
-                            s[j][mb][x] = -__builtin_inff();
-                    }
-        }
-        frag pf[2][MB];
+    // Rows past the last one are that row's, and not written.
+    __device__ __forceinline__ void init(const AttendArgs &a, const Entry &e, int i, int kvh, int x0,
+                                         int rows)
+    {
+        const int col = lane_id() & 15, grp = lane_id() >> 4;
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
-            float top = fmaxf(fmaxf(s[0][mb][0], s[0][mb][1]), s[0][mb][2]);
+            const int x = x0 + mb * 16 + col, xc = x < rows ? x : rows - 1;
+            const int j = xc / a.group, h = kvh * a.group + xc % a.group;
+            hi[mb] = end_of(a.c.mask, e, j);
+            lo[mb] = hi[mb] > a.w.W ? hi[mb] - a.w.W : 0;
+            const __bf16 *at = static_cast<const __bf16 *>(a.c.q) + i * a.c.q_stride_entry +
+                               j * a.c.q_stride_query + h * a.c.q_stride_head;
 #pragma unroll
-            for (int x = 3; x < 15; x += 2)
-                top = fmaxf(fmaxf(top, s[x / 4][mb][x % 4]), s[(x + 1) / 4][mb][(x + 1) % 4]);
-            top = fmaxf(top, s[3][mb][3]) * factor;
-            if (__any(top > m[mb] + kSlack)) {
-                top = fmaxf(top, __shfl_xor(top, 16));
-                top = fmaxf(top, __shfl_xor(top, 32));
-                const float to = fmaxf(m[mb], top);
-                const float alpha = to == -__builtin_inff() ? 1.f : exp2_hw(m[mb] - to);
-                m[mb] = to;
-                l[mb] *= alpha;
+            for (int st = 0; st < kSteps; ++st) {
+                const __bf16 *from = at + st / 2 * 64 + grp * 16 + (st & 1) * 8;
+                if (a.wide) {
+                    q[mb][st] = *reinterpret_cast<const frag *>(from);
+                } else {
 #pragma unroll
-                for (int c = 0; c < kCols; ++c)
-                    o[c][mb] *= alpha;
+                    for (int k = 0; k < 8; ++k)
+                        q[mb][st][k] = from[k];
+                }
+                // a negative scale goes into the queries, so that the largest
+                // product is the largest score
+                if (a.c.scale < 0.f)
+                    q[mb][st] = -q[mb][st];
             }
-            const float ref = m[mb] == -__builtin_inff() ? 0.f : m[mb];
+            ref[mb] = 0.f;
+            slack[mb] = -__builtin_inff();
+            l[mb] = 0.f;
+#pragma unroll
+            for (int c = 0; c < kCols; ++c)
+                o[c][mb] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+    }
+
+    // Products with a block's keys: key(g) is the lane's operand of step g % kSteps of
+    // tile g / kSteps.  Operands are asked for `AHEAD` steps early, and beside(g) is
+    // issued while the matrix unit works on step g (fences keep it so).
+    template <int AHEAD, typename K, typename F>
+    __device__ __forceinline__ void scores(K key, Scores &s, F beside)
+    {
+        constexpr int N = 4 * kSteps;
+        frag k[N];
+#pragma unroll
+        for (int g = 0; g < AHEAD; ++g)
+            k[g] = key(g);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int g = 0; g < N; ++g) {
+            const int j = g / kSteps, st = g % kSteps;
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb)
+                s[j][mb] = mfma(k[g], q[mb][st], st == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : s[j][mb]);
+            if (g + AHEAD < N)
+                k[g + AHEAD] = key(g + AHEAD);
+            beside(g);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+
+    // Leaves out the tokens of block b that a row does not see.
+    __device__ __forceinline__ void mask(Scores &s, int b)
+    {
+        int first = b * kBlock + (lane_id() >> 4) * 16;
+        asm("" : "+v"(first));  // (compared here, not ahead of the loop for each token)
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const float p = exp2_hw(fmaf(s[j][mb][x], factor, -ref));
-                    l[mb] += p;
-                    // rounded to bf16 for the product (at most 2^-8 of it)
-                    pf[j / 2][mb][(j & 1) * 4 + x] = (__bf16)p;
+                    const uint32_t pos = (uint32_t)(first - lo[mb] + j * 4 + x);
+                    if (pos >= (uint32_t)(hi[mb] - lo[mb]))
+                        s[j][mb][x] = -__builtin_inff();
                 }
+    }
+
+    // Scores relative to the reference, t - m, in place of the products (factor makes
+    // t of one), and the lane's largest of each block of rows: part g of `of`.
+    __device__ __forceinline__ void relative(Scores &s, float factor, float (&top)[MB], int g, int of)
+    {
+#pragma unroll
+        for (int e = g * 8 * MB / of; e < (g + 1) * 8 * MB / of; ++e) {
+            const int mb = e / 8, j = e / 2 % 4, x = e % 2 * 2;
+            const float y0 = fmaf(s[j][mb][x], factor, -ref[mb]);
+            const float y1 = fmaf(s[j][mb][x + 1], factor, -ref[mb]);
+            s[j][mb][x] = y0;
+            s[j][mb][x + 1] = y1;
+            top[mb] = e % 8 == 0 ? fmaxf(y0, y1) : fmaxf(fmaxf(top[mb], y0), y1);
         }
-        const float v_unit = scale_value(v_scale);
+    }
+
+    // Where one is above the slack, the maximum becomes the reference.
+    __device__ __forceinline__ void settle(Scores &s, const float (&top)[MB])
+    {
+        bool exceeds = false;
 #pragma unroll
-        for (int c = 0; c < kCols; ++c)
+        for (int mb = 0; mb < MB; ++mb)
+            exceeds |= top[mb] > slack[mb];
+        if (!__any(exceeds))
+            return;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const frag vf = widen(v[c][h * 2], v[c][h * 2 + 1], v_unit);
-#pragma unroll
-                for (int mb = 0; mb < MB; ++mb)
-                    o[c][mb] = mfma(vf, pf[h][mb], o[c][mb]);
+        for (int mb = 0; mb < MB; ++mb) {
+            float by = fmaxf(top[mb], __shfl_xor(top[mb], 16));
+            by = fmaxf(by, __shfl_xor(by, 32));
+            if (slack[mb] == -__builtin_inff()) {  // none so far
+                if (by == -__builtin_inff())
+                    continue;
+                slack[mb] = kSlack;
+            } else {
+                by = fmaxf(by, 0.f);
             }
+            const float alpha = exp2_hw(-by);  // (finite sums of 0 stay 0 in the first case)
+            ref[mb] += by;
+            l[mb] = l[mb] == 0.f ? 0.f : l[mb] * alpha;
+#pragma unroll
+            for (int c = 0; c < kCols; ++c)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    o[c][mb][x] = o[c][mb][x] == 0.f ? 0.f : o[c][mb][x] * alpha;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                s[j][mb] -= by;
+        }
+    }
+
+    // Probabilities of a block: part g of `of`, in pairs.
+    __device__ __forceinline__ void probabilities(const Scores &s, int g, int of)
+    {
+#pragma unroll
+        for (int e = g * 8 * MB / of; e < (g + 1) * 8 * MB / of; ++e) {
+            const int mb = e / 8, j = e / 2 % 4, x = e % 2 * 2;
+            const float y0 = exp2_hw(s[j][mb][x]), y1 = exp2_hw(s[j][mb][x + 1]);
+            l[mb] += y0;
+            l[mb] += y1;
+            // rounded to bf16 for the products (at most 2^-8 of it); summed and
+            // rounded here, so that a pair takes one register from now on
+            uint32_t pair = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)y0, (__bf16)y1});
+            asm volatile("" : "+v"(pair), "+v"(l[mb]));
+            p[j / 2][mb][(j & 1) * 2 + x / 2] = pair;
+        }
+    }
+
+    // Sums over a block's values: value(g) is the lane's operand of tokens 8 (g % 2) ..
+    // of each 16, columns 16 (g / 2) ..; as in scores.
+    template <int AHEAD, typename V, typename F>
+    __device__ __forceinline__ void values(V value, F beside)
+    {
+        constexpr int N = 2 * kCols;
+        frag v[N];
+#pragma unroll
+        for (int g = 0; g < AHEAD; ++g)
+            v[g] = value(g);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int g = 0; g < N; ++g) {
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb)
+                o[g / 2][mb] = mfma(v[g], __builtin_bit_cast(frag, p[g % 2][mb]), o[g / 2][mb]);
+            if (g + AHEAD < N)
+                v[g + AHEAD] = value(g + AHEAD);
+            beside(g);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+
+    // m of the sums.
+    __device__ __forceinline__ float reference(int mb) const
+    {
+        return slack[mb] == -__builtin_inff() ? -__builtin_inff() : ref[mb];
+    }
+
+    // The lane groups' sums of probabilities.
+    __device__ __forceinline__ void total()
+    {
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) {
+            l[mb] += __shfl_xor(l[mb], 16);
+            l[mb] += __shfl_xor(l[mb], 32);
+        }
+    }
+};
+
+// What the products are multiplied by: log2(e) scale, and the keys' unit.  (At
+// least a small normal: masked scores stay -infinity with a scale of 0.)
+__device__ __forceinline__ float score_factor(float scale, uint32_t key_scale)
+{
+    return fmaxf(fabsf(scale) * 1.44269504088896340736f * scale_value(key_scale), 1e-37f);
+}
+
+// Row x of the head, columns d .. d + 3 of its unnormalised sums.
+template <int D>
+__device__ __forceinline__ void write_sums(const AttendArgs &a, const Job &job, int x, int d, float m,
+                                           float l, f32x4 sums)
+{
+    if (a.shares > 1) {
+        const int64_t at = job.part * (a.c.nq * a.group) + x;
+        if (d == 0)
+            *reinterpret_cast<float2 *>(a.stat + 2 * at) = make_float2(m, l);
+        *reinterpret_cast<f32x4 *>(a.partial + at * D + d) = sums;
+        return;
+    }
+    const int j = x / a.group, h = job.kvh * a.group + x % a.group;
+    const int64_t at = ((int64_t)job.i * a.c.nq + j) * a.c.heads + h;
+    const float inv = m == -__builtin_inff() && l == 0.f ? 0.f : 1.f / l;
+    if (d == 0 && a.c.lse)
+        a.c.lse[at] = 0.69314718055994530942f * (m + __log2f(l));
+    bf16x4 r;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        r[k] = (__bf16)(sums[k] * inv);
+    *reinterpret_cast<bf16x4 *>(static_cast<__bf16 *>(a.c.out) + at * D + d) = r;
+}
+
+// Few query rows: the NW waves of a workgroup have the same ones and take every
+// NW-th block of tokens, straight from memory into registers (the next keys once
+// the scores are taken, the next values after the products); their sums are joined
+// through LDS.
+template <int D, int MB, int NW>
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 2)))
+void split_kernel(AttendArgs a)
+{
+    typedef Rows<D, MB> R;
+    constexpr int kRows = 16 * MB, kStride = D + 4;
+    __shared__ __attribute__((aligned(16))) float sO[NW * kRows * kStride];
+    __shared__ float sStat[NW * kRows * 2];
+    const int lane = lane_id(), col = lane & 15, grp = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(wave_id());
+    Job job;
+    if (!job_of(a, job))
+        return;
+    const Entry e = attend_entry(a, job.i);
+    if (a.c.status && job.kvh == 0 && job.tile == 0 && job.share == 0 && threadIdx.x == 0)
+        a.c.status[job.i] = e.status;
+    const int x0 = job.tile * kRows, rows = e.count * a.group;
+    if (e.status != KVR_OK || x0 >= rows)
+        return;
+    Span span = span_of(a, e, x0, x0 + kRows < rows ? x0 + kRows : rows);
+    cut(span, job.share, a.shares);
+    R r;
+    r.init(a, e, job.i, job.kvh, x0, rows);
+
+    u32x4 k[4][R::kKeys], v[R::kCols];
+    uint32_t k_scale = 0, v_scale = 0;
+    const int64_t head_bytes = 2 * kBlock * D;
+    const int64_t first = (int64_t)e.r * a.w.blocks * a.w.kv_heads + job.kvh;
+    const int k_at = ((col >> 2) * 16 + (col & 3)) * D + grp * 16;
+    const int v_at = kBlock * D + col * kBlock + grp * 16;
+    auto at_block = [&](int b) { return first + (int64_t)(b % a.w.blocks) * a.w.kv_heads; };
+    auto load_keys = [&](int64_t at) __attribute__((always_inline)) {
+        const uint8_t *from = a.w.codes + at * head_bytes + k_at;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int n = 0; n < R::kKeys; ++n)
+                k[j][n] = *reinterpret_cast<const u32x4 *>(from + j * 4 * D + n * 64);
+        k_scale = a.w.scales[at * 2];
+    };
+    auto load_values = [&](int64_t at) __attribute__((always_inline)) {
+        const uint8_t *from = a.w.codes + at * head_bytes + v_at;
+#pragma unroll
+        for (int c = 0; c < R::kCols; ++c)
+            v[c] = *reinterpret_cast<const u32x4 *>(from + c * 16 * kBlock);
+        v_scale = a.w.scales[at * 2 + 1];
+    };
+    int b = span.b0 + wave;
+    if (b < span.b1) {
+        load_keys(at_block(b));
+        load_values(at_block(b));
+    }
+    for (; b < span.b1; b += NW) {
+        typename R::Scores s;
+        float top[MB];
+        auto alone = [](int) {};
+        r.template scores<1>(
+            [&](int g) __attribute__((always_inline)) {
+                const int st = g % R::kSteps;
+                const u32x4 w = k[g / R::kSteps][st / 2];
+                return widen(w[st % 2 * 2], w[st % 2 * 2 + 1], 1.f);
+            },
+            s, alone);
+        const float factor = score_factor(a.c.scale, k_scale);
+        const bool more = b + NW < span.b1;
+        const int64_t at_next = at_block(b + NW);
+        if (more)
+            load_keys(at_next);
+        if (b < span.full0 || b >= span.full1)
+            r.mask(s, b);
+        r.relative(s, factor, top, 0, 1);
+        r.settle(s, top);
+        r.probabilities(s, 0, 1);
+        const float unit = scale_value(v_scale);
+        r.template values<1>(
+            [&](int g) __attribute__((always_inline)) {
+                return widen(v[g / 2][g % 2 * 2], v[g / 2][g % 2 * 2 + 1], unit);
+            },
+            alone);
         if (more)
             load_values(at_next);
     }
 
-    const int64_t part = (int64_t)unit * a.shares + share;
-    const int unit_rows = a.c.nq * a.group;
+    r.total();
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
-        l[mb] += __shfl_xor(l[mb], 16);
-        l[mb] += __shfl_xor(l[mb], 32);
+        const int at = wave * kRows + mb * 16 + col;
+        if (grp == 0) {
+            sStat[at * 2] = r.reference(mb);
+            sStat[at * 2 + 1] = r.l[mb];
+        }
+#pragma unroll
+        for (int c = 0; c < R::kCols; ++c)
+            *reinterpret_cast<f32x4 *>(&sO[at * kStride + c * 16 + grp * 4]) = r.o[c][mb];
     }
-    // row x of the head, value columns d .. d + 3 of the unnormalised sums
-    auto write = [&](int x, int d, float mx, float lx, f32x4 sums) __attribute__((always_inline)) {
-        if (a.shares > 1) {
-            const int64_t ps = part * unit_rows + x;
-            if (d == 0)
-                *reinterpret_cast<float2 *>(a.stat + 2 * ps) = make_float2(mx, lx);
-            *reinterpret_cast<f32x4 *>(a.partial + ps * D + d) = sums;
-            return;
-        }
-        const int j = x / a.group, h = kvh * a.group + x % a.group;
-        const int64_t at = ((int64_t)i * a.c.nq + j) * a.c.heads + h;
-        const float inv = mx == -__builtin_inff() && lx == 0.f ? 0.f : 1.f / lx;
-        if (d == 0 && a.c.lse)
-            a.c.lse[at] = 0.69314718055994530942f * (mx + __log2f(lx));
-        bf16x4 r;
+    __syncthreads();
+    // the waves' sums, joined in wave order
+    for (int q = threadIdx.x; q < kRows * D / 4; q += NW * 64) {
+        const int row = q / (D / 4), d = q % (D / 4) * 4;
+        if (x0 + row >= rows)
+            break;
+        float m = -__builtin_inff(), l = 0.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            r[k] = (__bf16)(sums[k] * inv);
-        *reinterpret_cast<bf16x4 *>(static_cast<__bf16 *>(a.c.out) + at * D + d) = r;
+        for (int w = 0; w < NW; ++w)
+            m = fmaxf(m, sStat[(w * kRows + row) * 2]);
+        f32x4 sums = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const int at = w * kRows + row;
+            const float mw = sStat[at * 2], lw = sStat[at * 2 + 1];
+            // (a wave without a score above -infinity has sums of 0 or NaN)
+            const float weight = mw == -__builtin_inff() ? 1.f : exp2_hw(mw - m);
+            l += weight * lw;
+            sums += weight * *reinterpret_cast<const f32x4 *>(&sO[at * kStride + d]);
+        }
+        write_sums<D>(a, job, x0 + row, d, m, l, sums);
+    }
+}
+
+// A workgroup barrier for LDS: loads from memory stay in flight.
+__device__ __forceinline__ void barrier_lds()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// Many query rows: the NW waves of a workgroup have some each and share the blocks
+// of tokens, of which each converts its part to bf16 (the values with their
+// scale), once for all, into LDS.
+//
+// While one block is worked on, the next is converted into the other half of LDS,
+// and the codes of the one after it are on their way.
+//
+// 16-byte pieces lie at piece ^ swizzle of their row, so that the 16 rows that a
+// lane group reads at once are in different banks: keys in rows 16 a + 4 j + b (a,
+// b = 0 .. 3) of 2 D bytes, values in 16 consecutive rows of 128.
+template <int D, int MB, int NW>
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NW / 4)))
+void shared_kernel(AttendArgs a)
+{
+    typedef Rows<D, MB> R;
+    constexpr int kPart = kBlock * D / NW / 16;       // 16-code pieces of a wave, keys or values
+    constexpr int kLoads = (kPart + 63) / 64;
+    constexpr int kHalf = 2 * kBlock * D;             // bytes of a block's keys or values
+    __shared__ __attribute__((aligned(1024))) uint8_t sTile[2][2 * kHalf];  // keys, values
+    const int lane = lane_id(), col = lane & 15, grp = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(wave_id());
+    Job job;
+    if (!job_of(a, job))
+        return;
+    const Entry e = attend_entry(a, job.i);
+    if (a.c.status && job.kvh == 0 && job.tile == 0 && job.share == 0 && threadIdx.x == 0)
+        a.c.status[job.i] = e.status;
+    const int rows = e.count * a.group;
+    const int first_row = job.tile * NW * 16 * MB;  // of the workgroup, and of the wave
+    if (e.status != KVR_OK || first_row >= rows)
+        return;
+    const int x0 = first_row + wave * 16 * MB;
+    auto below = [&](int x) { return x < rows ? x : rows; };
+    Span all = span_of(a, e, first_row, below(first_row + NW * 16 * MB));
+    cut(all, job.share, a.shares);
+    const bool idle = x0 >= rows;
+    const Span own = span_of(a, e, idle ? rows - 1 : x0, below(x0 + 16 * MB));
+    R r;
+    r.init(a, e, job.i, job.kvh, idle ? rows - 1 : x0, rows);
+
+    auto key_swizzle = [](int row) {
+        return D == 64 ? (row >> 4 & 3) * 2 + (row >> 1 & 1) : (row >> 4 & 3) * 4 + (row & 3);
     };
-    if constexpr (!SPLIT) {
+    auto value_swizzle = [](int row) { return row >> 1 & 7; };
+    const int64_t first = (int64_t)e.r * a.w.blocks * a.w.kv_heads + job.kvh;
+    // (past the last block: that one's again, not used)
+    auto at_block = [&](int b) {
+        return first + (int64_t)((b < all.b1 ? b : all.b1 - 1) % a.w.blocks) * a.w.kv_heads;
+    };
+    // The lane's pieces of a block: codes from `from`, bf16 values to the two `to`.
+    u32x4 k_raw[kLoads], v_raw[kLoads];
+    uint32_t k_scale = 0, v_scale = 0;
+    int from[kLoads], k_to[kLoads][2], v_to[kLoads][2];
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb) {
-            const int x = x0 + mb * 16 + col;
-            if (x >= rows)
-                continue;
+    for (int n = 0; n < kLoads; ++n) {
+        const int piece = wave * kPart + n * 64 + lane;
+        const int key = piece / (D / 16), value = piece / 4;
+        from[n] = piece * 16;
 #pragma unroll
-            for (int c = 0; c < kCols; ++c)
-                write(x, c * 16 + grp * 4, m[mb], l[mb], o[c][mb]);
+        for (int h = 0; h < 2; ++h) {
+            k_to[n][h] = key * 2 * D + ((piece % (D / 16) * 2 + h) ^ key_swizzle(key)) * 16;
+            v_to[n][h] = kHalf + value * 128 + ((piece % 4 * 2 + h) ^ value_swizzle(value)) * 16;
         }
-    } else {
-        constexpr int kStride = D + 4;
+    }
+    const bool mine = kPart >= 64 || lane < kPart;
+    auto load = [&](int b) __attribute__((always_inline)) {
+        const int64_t at = at_block(b);
+        const uint8_t *codes = a.w.codes + at * (2 * kBlock * D);
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb) {
-            const int at = wave * kRows + mb * 16 + col;
-            if (grp == 0) {
-                sStat[at * 2] = m[mb];
-                sStat[at * 2 + 1] = l[mb];
+        for (int n = 0; n < kLoads; ++n)
+            if (mine) {
+                k_raw[n] = *reinterpret_cast<const u32x4 *>(codes + from[n]);
+                v_raw[n] = *reinterpret_cast<const u32x4 *>(codes + kBlock * D + from[n]);
             }
+        k_scale = a.w.scales[at * 2];
+        v_scale = a.w.scales[at * 2 + 1];
+    };
+    uint32_t next_scale = 0;  // of the keys of the block stored last
+    auto store = [&](uint8_t *to) __attribute__((always_inline)) {
+        const float unit = scale_value(v_scale);
 #pragma unroll
-            for (int c = 0; c < kCols; ++c)
-                *reinterpret_cast<f32x4 *>(&sO[at * kStride + c * 16 + grp * 4]) = o[c][mb];
-        }
-        __syncthreads();
-        // the waves' sums, joined in wave order
-        for (int q = threadIdx.x; q < kRows * D / 4; q += NW * 64) {
-            const int row = q / (D / 4), d = q % (D / 4) * 4;
-            if (x0 + row >= rows)
-                break;
-            float mx = -__builtin_inff(), lx = 0.f;
+        for (int n = 0; n < kLoads; ++n)
 #pragma unroll
-            for (int w = 0; w < NW; ++w)
-                mx = fmaxf(mx, sStat[(w * kRows + row) * 2]);
-            f32x4 sums = {0.f, 0.f, 0.f, 0.f};
+            for (int h = 0; h < 2; ++h)
+                if (mine) {
+                    *reinterpret_cast<frag *>(to + k_to[n][h]) =
+                        widen(k_raw[n][h * 2], k_raw[n][h * 2 + 1], 1.f);
+                    *reinterpret_cast<frag *>(to + v_to[n][h]) =
+                        widen(v_raw[n][h * 2], v_raw[n][h * 2 + 1], unit);
+                }
+        next_scale = k_scale;
+    };
+    int k_at[R::kSteps < 4 ? R::kSteps : 4], v_at[2];
 #pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                const int at = w * kRows + row;
-                const float mw = sStat[at * 2], lw = sStat[at * 2 + 1];
-                // (a wave without a score above -infinity has sums of 0 or NaN)
-                const float weight = mw == -__builtin_inff() ? 1.f : exp2_hw(mw - mx);
-                lx += weight * lw;
-                sums += weight * *reinterpret_cast<const f32x4 *>(&sO[at * kStride + d]);
-            }
-            write(x0 + row, d, mx, lx, sums);
-        }
+    for (int st = 0; st < R::kSteps && st < 4; ++st) {
+        const int row = (col >> 2) * 16 + (col & 3);
+        k_at[st] = row * 2 * D + ((st / 2 * 8 + grp * 2 + st % 2) ^ key_swizzle(row)) * 16;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        v_at[h] = kHalf + col * 128 + ((grp * 2 + h) ^ value_swizzle(col)) * 16;
+
+    int t = all.b0;  // the block that is worked on next
+    if (t < all.b1) {
+        load(t);
+        store(sTile[t & 1]);
+        load(t + 1);
+    }
+    float factor = 0.f;
+    auto next = [&]() __attribute__((always_inline)) {
+        barrier_lds();
+        factor = score_factor(a.c.scale, next_scale);
+        ++t;
+        store(sTile[t & 1]);
+        load(t + 1);
+    };
+    auto nothing = [](int) {};
+    // (blocks that this wave's rows do not see come before and after those that
+    // they do)
+    const int b0 = idle || own.b0 > all.b1 ? all.b1 : own.b0;
+    const int b1 = own.b1 < all.b1 ? own.b1 : all.b1;
+    while (t < b0)
+        next();
+    for (int b = t; b < b1; ++b) {
+        next();
+        typename R::Scores s;
+        float top[MB];
+        const uint8_t *tile = sTile[b & 1];
+        r.template scores<4>(
+            [&](int g) __attribute__((always_inline)) {
+                const int j = g / R::kSteps, st = g % R::kSteps;
+                return *reinterpret_cast<const frag *>(tile + k_at[st % 4] + st / 4 * 256 +
+                                                       j * 8 * D);
+            },
+            s, nothing);
+        if (b < own.full0 || b >= own.full1)
+            r.mask(s, b);
+        r.relative(s, factor, top, 0, 1);
+        r.settle(s, top);
+        r.probabilities(s, 0, 1);
+        r.template values<4>(
+            [&](int g) __attribute__((always_inline)) {
+                return *reinterpret_cast<const frag *>(tile + v_at[g % 2] + g / 2 * 16 * 128);
+            },
+            nothing);
+    }
+    while (t < all.b1)
+        next();
+    r.total();
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+        const int x = x0 + mb * 16 + col;
+        if (x >= rows)
+            continue;
+#pragma unroll
+        for (int c = 0; c < R::kCols; ++c)
+            write_sums<D>(a, job, x, c * 16 + grp * 4, r.reference(mb), r.l[mb], r.o[c][mb]);
     }
 }
 
@@ -442,25 +755,35 @@ __global__ __launch_bounds__(kJoinWaves * 64) void join_kernel(AttendArgs a)
 }
 
 constexpr int64_t kUnits = 256;  // compute units
-constexpr int kWaves = 4;
 
-// Query rows of a wave with many of them, in blocks of 16: as many as two waves
-// a SIMD have registers for (one, with heads of 256).
-constexpr int blocks_of_16(int d) { return d == 256 ? 1 : 2; }
+// A wave's blocks of 16 query rows where there are many: as many as two waves a SIMD
+// have registers for.
+constexpr int split_rows(int d) { return d == 256 ? 1 : 2; }
+
+// Waves that share a block in LDS, each with 32 query rows (with heads of 256 they
+// need more than half of a SIMD's registers).
+constexpr int shared_waves(int d) { return d == 256 ? 4 : 8; }
 
 int64_t partial_bytes(int64_t rows, int32_t d) { return rows * (d + 2) * (int64_t)sizeof(float); }
 
 template <int D>
 hipError_t launch_dim(const AttendArgs &a, const DraftPlan &p, dim3 grid, hipStream_t s)
 {
-    constexpr int MB = blocks_of_16(D);
+    auto run = [&](void (*kernel)(AttendArgs), int waves) {
+        return launch(nullptr, 0, kernel, grid, dim3(waves * 64), 0, s, a);
+    };
     hipError_t e;
-    if (!p.split)
-        e = launch(nullptr, 0, attend_kernel<D, MB, kWaves, false>, grid, dim3(kWaves * 64), 0, s, a);
-    else if (p.blocks_of_16 == 1)
-        e = launch(nullptr, 0, attend_kernel<D, 1, kWaves, true>, grid, dim3(kWaves * 64), 0, s, a);
+    if constexpr (D == 64)
+        e = p.blocks_of_16 == 2 ? run(split_kernel<D, 2, 4>, 4)
+            : p.waves == 4      ? run(split_kernel<D, 1, 4>, 4)
+                                : run(split_kernel<D, 1, 8>, 8);
+    else if constexpr (D == 128)
+        e = !p.split              ? run(shared_kernel<D, 2, 8>, 8)
+            : p.blocks_of_16 == 2 ? run(split_kernel<D, 2, 4>, 4)
+            : p.waves == 4        ? run(split_kernel<D, 1, 4>, 4)
+                                  : run(split_kernel<D, 1, 8>, 8);
     else
-        e = launch(nullptr, 0, attend_kernel<D, MB, kWaves, true>, grid, dim3(kWaves * 64), 0, s, a);
+        e = !p.split ? run(shared_kernel<D, 2, 4>, 4) : run(split_kernel<D, 1, 4>, 4);
     if (e != hipSuccess || a.shares == 1)
         return e;
     const int64_t rows = (int64_t)a.c.n * a.c.nq * a.c.heads;
@@ -475,33 +798,55 @@ DraftPlan draft_plan(int32_t n, int32_t nq, int32_t heads, int32_t kv_heads, int
     DraftPlan p{};
     const int64_t rows = (int64_t)nq * (heads / kv_heads);  // of an entry and head
     const int64_t units = (int64_t)n * kv_heads;
-    p.blocks_of_16 = rows <= 16 ? 1 : blocks_of_16(d_head);
-    p.waves = kWaves;
-    p.split = rows < 128;
-    const int64_t tile = 16 * p.blocks_of_16 * (p.split ? 1 : kWaves);
-    p.tiles = (int32_t)((rows + tile - 1) / tile);
-    // a share takes a block of tokens for each wave at least
     const int64_t blocks = ((int64_t)tokens + kBlock - 1) / kBlock + 1;
-    const int64_t most = (blocks + kWaves - 1) / kWaves;
-    int64_t shares = 2 * kUnits / (units * p.tiles);
-    shares = shares < most ? shares : most;
-    p.shares = (int32_t)(shares < 1 ? 1 : shares);
+    // shared_kernel takes whole rounds of the compute units (256 query rows a
+    // workgroup): a chunk of 1024 tokens (128 workgroups) 134 us against 101 split,
+    // 1500 (188) 135 against 149, 2048 (256) 140 against 195, 2400 (300) 262 against
+    // 242, 3000 (375) 264 against 290.  So with 0.7 of its rounds full.  Heads of 256
+    // (128 query rows a workgroup) gain from it, with shares, at any number (chunks of
+    // 128 and 1024 tokens, 16 heads: 41 and 140 us, split 41 and 238), heads of 64 at
+    // none (1024 tokens of 64 heads 101, split 95).
+    const int64_t shared = 16 * 2 * shared_waves(d_head);
+    const int64_t full = units * ((rows + shared - 1) / shared);
+    const int64_t rounds = (full + kUnits - 1) / kUnits;
+    p.split = d_head == 64 || rows < shared || (d_head == 128 && 10 * full < 7 * kUnits * rounds);
+    p.blocks_of_16 = !p.split ? 2
+                     : rows <= 16 || units * ((rows + 15) / 16) <= kUnits ? 1
+                                                                          : split_rows(d_head);
+    // (blocks of 16 while that leaves no workgroup waiting: 8 requests of 8 queries
+    // x 4 heads 12 us, in blocks of 32 15; 16 requests of 16 queries x 4 heads 31, 23)
+    const int64_t tile = p.split ? 16 * p.blocks_of_16 : shared;
+    p.tiles = (int32_t)((rows + tile - 1) / tile);
+    const int64_t groups = units * p.tiles;
+    p.waves = !p.split ? shared_waves(d_head) : d_head == 256 || groups > kUnits ? 4 : 8;
+    if (p.split && p.blocks_of_16 == 2)
+        p.waves = 4;
+    // (8 waves where there are few workgroups: 32 requests of 4 queries x 7 heads of 64
+    // 10 us, with 4 waves 12; 512 workgroups, window 256: 15, 12)
+    // Shares where they take 24 blocks of 16 KB or more off a workgroup, which pays
+    // for the join: one request x 32 heads, window 4096, 26 us in one share, 11 in 8
+    // (8 workgroups); 16 requests 34, 33 in 2; window 1024: 16 requests 12, 14 in 2.
+    int64_t shares = kUnits / groups;
+    shares = shares < blocks / p.waves ? shares : blocks / p.waves;
+    if (shares < 2 || (blocks - blocks / shares) * d_head < 24 * 128)
+        shares = 1;
+    p.shares = (int32_t)shares;
     p.workspace = p.shares > 1 ? partial_bytes(units * p.shares * rows, d_head) : 0;
     return p;
 }
 
 // Over all smaller calls: their query rows times shares are at most the query
-// rows times the most shares, and at most the rows of 512 workgroups.
+// rows times the most shares, and at most the rows of 256 workgroups.
 int64_t draft_workspace_bound(int32_t n, int32_t nq, int32_t heads, int32_t kv_heads,
                               int32_t d_head, int32_t window)
 {
     const int64_t blocks = ((int64_t)window + nq - 1 + kBlock - 1) / kBlock + 1;
-    const int64_t most = (blocks + kWaves - 1) / kWaves;
-    const int64_t all = (int64_t)n * nq * heads, tile = 32 * kWaves;
+    const int64_t most = blocks / 4, all = (int64_t)n * nq * heads;
+    const int64_t tile = 16 * 2 * shared_waves(d_head);
     (void)kv_heads;
     if (most < 2)
         return 0;
-    return partial_bytes(all * most < 2 * kUnits * tile ? all * most : 2 * kUnits * tile, d_head);
+    return partial_bytes(all * most < kUnits * tile ? all * most : kUnits * tile, d_head);
 }
 
 hipError_t launch_draft_attend(const kvr_draft *d, const kvr_draft_attend_call &c,

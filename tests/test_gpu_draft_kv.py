@@ -332,6 +332,23 @@ def test_attend_prompts(mask, d, kv, group, nq):
         check_attend(R, [0, 1, 2], q, mask, out, lse, c)
 
 
+@pytest.mark.parametrize("d,n,kv,group,nq,W", [(128, 45, 4, 4, 64, 100), (128, 23, 8, 1, 256, 70),
+                                               (256, 1, 1, 1, 140, 2500), (256, 3, 2, 3, 60, 130)])
+@pytest.mark.parametrize("mask", ["causal", "block"])
+def test_attend_rows_that_share_blocks(d, n, kv, group, nq, W, mask):
+    """Enough query rows for the waves of a workgroup to share each block: full ones, and
+    entries with fewer rows than a workgroup, a wave or anything."""
+    C = (W + nq + 63) // 64 * 64 + 64
+    lengths = [(0, W // 2, W + 64 * r, 3 * W + r)[r % 4] for r in range(n)]
+    count = None
+    if n > 1:
+        count = [(nq, 0, 1, nq // 2 + 1, nq - 1)[r % 5] for r in range(n)]
+    R = filled(d + W, n, W, C, kv, d, lengths, nq)
+    q = torch.randn(n, nq, kv * group, d, device=DEV).bfloat16()
+    out, lse = attend(R, list(range(n)), q, mask, count)
+    check_attend(R, list(range(n)), q, mask, out, lse, count)
+
+
 @pytest.mark.parametrize("W,nq,n", [(1, 1, 2), (1, 5, 1), (64, 1, 1), (5000, 1, 1), (3500, 3, 3),
                                     (700, 1, 40)])
 def test_attend_window_sizes(W, nq, n):
@@ -492,11 +509,12 @@ def test_layers_past_32_bits():
 
 def test_two_calls_at_once():
     """Two layers on two streams, each with its own workspace."""
-    R = filled(6, 4, 500, 640, 2, 128, [600] * 4, 1, layers=2, layer=0)
+    R = filled(6, 4, 3500, 3648, 2, 128, [3600] * 4, 1, layers=2, layer=0)
     R.codes[1], R.scales[1] = R.codes[0], R.scales[0]
     q = torch.randn(4, 1, 16, 128, device=DEV).bfloat16()
     want, want_lse = attend(R, [0, 1, 2, 3], q, "causal")
     need = R.ring.attend_workspace(4, 1, 16)
+    assert need > 0
     streams = [torch.cuda.Stream() for _ in range(2)]
     outs = [torch.zeros_like(q) for _ in range(2)]
     ws = [torch.zeros(need, dtype=torch.uint8, device=DEV) for _ in range(2)]
@@ -547,12 +565,13 @@ def test_captured_and_replayed():
 
 
 def test_same_results_every_time():
-    R = filled(9, 2, 1000, 1152, 1, 128, [2000, 900], 1)
-    q = torch.randn(2, 1, 16, 128, device=DEV).bfloat16()
-    first = attend(R, [0, 1], q, "causal")
-    for _ in range(5):
-        again = attend(R, [0, 1], q, "causal")
-        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    for W, nq in ((1000, 1), (3000, 1), (300, 40)):
+        R = filled(9, 2, W, (W + 191) // 64 * 64, 1, 128, [2 * W, W - 100], nq)
+        q = torch.randn(2, nq, 16, 128, device=DEV).bfloat16()
+        first = attend(R, [0, 1], q, "causal")
+        for _ in range(5):
+            again = attend(R, [0, 1], q, "causal")
+            assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
 def test_refusals():
@@ -607,7 +626,7 @@ def test_refusals():
     refused(a, KvrError, "193 new tokens", good, q=wide, out=wide.clone(), mask="block")
     flat = torch.zeros(q.numel() + 8, dtype=torch.bfloat16, device=DEV)
     refused(a, KvrError, "not aligned", good, out=flat[4:-4].view(q.shape))
-    R2 = filled(10, 1, 1000, 1152, 1, 64, [1000], 1)
+    R2 = filled(10, 1, 8000, 8128, 1, 64, [8000], 1)
     q1 = torch.zeros(1, 1, 4, 64, dtype=torch.bfloat16, device=DEV)
     refused(R2.ring.attend, KvrError, "the workspace has 0 bytes", dict(
         layer=0, n=1, req_ids=None, q=q1, out=torch.zeros_like(q1), scale=0.1))
