@@ -13,7 +13,7 @@
 // part_kernel reads the logits once: a row is cut into shares of a workgroup
 // each, whose threads keep m, l, u and their largest logit.
 // row_kernel, a workgroup per row, joins the shares.  For the alternatives it
-// takes the threads' largest logits in 64 groups (a thread's lane): the top-th
+// takes the threads' largest logits in 128 groups (every 128th piece): the top-th
 // largest of the groups' maxima is a value that at least `top` logits reach,
 // so only the runs of threads whose maximum reaches it are read again, and of
 // those logits the few that reach it are ranked by counting, (value, lower token
@@ -30,7 +30,6 @@ namespace {
 constexpr int NT = 256;
 constexpr int kRun = 8;        // consecutive logits of a thread: one piece
 constexpr int kBatch = 4;      // pieces of a thread in flight
-constexpr int kTops = 8;       // maxima of a thread in flight
 constexpr int kList = 1024;    // logits that are ranked, and runs that are read for them
 constexpr float kInf = __builtin_inff();
 
@@ -161,29 +160,31 @@ __device__ __forceinline__ uint32_t key_of(float x)
     return u ^ (u >> 31 ? 0xFFFFFFFFu : 0x80000000u);
 }
 
-// The n-th largest of the 64 lanes' values, bit by bit from the top.
-__device__ __forceinline__ float nth_largest(float x, int n)
+// The n-th largest of the 64 lanes' two values, bit by bit from the top.
+__device__ __forceinline__ float nth_largest(float x, float y, int n)
 {
-    const uint32_t key = key_of(x);
+    const uint32_t kx = key_of(x), ky = key_of(y);
     uint32_t found = 0;
 #pragma unroll
     for (int bit = 31; bit >= 0; --bit) {
         const uint32_t trial = found | 1u << bit;
-        if (__popcll(__ballot(key >= trial)) >= n)
+        if (__popcll(__ballot(kx >= trial)) + __popcll(__ballot(ky >= trial)) >= n)
             found = trial;
     }
     return __uint_as_float(found ^ (found >> 31 ? 0x80000000u : 0xFFFFFFFFu));
 }
 
-// NR threads a row.
-template <typename T, int NR>
+// NR threads a row, TOPS maxima of the threads before in each at once.
+template <typename T, int NR, int TOPS>
 __global__ __launch_bounds__(NR) void row_kernel(LogprobArgs a)
 {
     constexpr int kWaves = NR / 64;
+    __shared__ float sMost[kWaves][64];
     __shared__ float sValue[kList];
     __shared__ int sToken[kList];
     __shared__ int sRun[kList];
     __shared__ int sRuns, sCount;
+    __shared__ float sSum[2];  // m and ln l (NaN where anything is)
     __shared__ float sM[kWaves];
     __shared__ int sI[kWaves];
     const int64_t r = blockIdx.x;
@@ -193,79 +194,89 @@ __global__ __launch_bounds__(NR) void row_kernel(LogprobArgs a)
     if (tid == 0)
         sRuns = sCount = 0;
 
-    // the row's sums, joined in a fixed order by every wave
-    float m = -kInf, l = 0.f, u = 0.f;
-    const float *parts = a.parts + r * a.shares * 4;
-    for (int s = lane; s < a.shares; s += 64)
-        join(factor, m, l, u, parts[4 * s], parts[4 * s + 1], parts[4 * s + 2]);
-#pragma unroll
-    for (int k = 32; k >= 1; k >>= 1)
-        join(factor, m, l, u, __shfl_xor(m, k), __shfl_xor(l, k), __shfl_xor(u, k));
-    // the first lane's, for all: which thread writes an alternative varies, and
-    // the lanes' sums differ in their last bits (their products are not fused alike)
-    auto first = [](float x) {
-        return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
-    };
-    m = first(m), l = first(l), u = first(u);
-    const bool bad = l != l;
-    const float nan = __builtin_nanf("");
-    constexpr float kLn2 = 0.69314718055994530942f;
-    const float log_l = kLn2 * __log2f(l);
-    auto logprob = [&](float x) {
-        return bad ? nan : x == -kInf ? -kInf : (x - m) * a.c.scale - log_l;
-    };
-    if (tid == 0) {
-        if (a.c.lse)
-            a.c.lse[r] = bad ? nan : m == -kInf ? -kInf : m * a.c.scale + log_l;
-        if (a.c.entropy)
-            a.c.entropy[r] = bad ? nan : m == -kInf ? 0.f : log_l + kLn2 * (u / l);
-    }
-    for (int k = tid; k < a.c.m; k += NR) {
-        const int token = a.c.tokens[r * a.c.m + k];
-        const float x = token >= 0 && token < a.c.vocab ? (float)row[token] : -kInf;
-        a.c.logprob[r * a.c.m + k] = logprob(x);
-    }
     const int top = a.c.top;
-    if (top == 0)
+    const int runs = top > 0 ? a.shares * NT : 0;
+    const float *tops = a.tops + r * a.shares * NT;
+    float t[TOPS];
+#pragma unroll
+    for (int k = 0; k < TOPS; ++k)
+        t[k] = tid + k * NR < runs ? tops[tid + k * NR] : -kInf;
+
+    // The last wave joins the row's sums, in a fixed order, and writes what needs no
+    // more than them: beside the other waves' reads, below.
+    constexpr float kLn2 = 0.69314718055994530942f;
+    auto logprob = [&](float x, float m, float log_l) {
+        return log_l != log_l ? log_l : x == -kInf ? -kInf : (x - m) * a.c.scale - log_l;
+    };
+    auto sums = [&]() {
+        if (wave != kWaves - 1)
+            return;
+        auto logit = [&](int k) {
+            const int token = a.c.tokens[r * a.c.m + k];
+            return token >= 0 && token < a.c.vocab ? (float)row[token] : -kInf;
+        };
+        const float given = lane < a.c.m ? logit(lane) : 0.f;
+        float m = -kInf, l = 0.f, u = 0.f;
+        const float *parts = a.parts + r * a.shares * 4;
+        for (int s = lane; s < a.shares; s += 64)
+            join(factor, m, l, u, parts[4 * s], parts[4 * s + 1], parts[4 * s + 2]);
+#pragma unroll
+        for (int k = 32; k >= 1; k >>= 1)
+            join(factor, m, l, u, __shfl_xor(m, k), __shfl_xor(l, k), __shfl_xor(u, k));
+        // the first lane's, for all: the lanes' sums differ in their last bits (their
+        // products are not fused alike)
+        auto first = [](float x) {
+            return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
+        };
+        m = first(m), l = first(l), u = first(u);
+        const bool bad = l != l;  // a NaN, or an infinity
+        const float log_l = bad ? __builtin_nanf("") : kLn2 * __log2f(l);
+        if (lane == 0) {
+            sSum[0] = m;
+            sSum[1] = log_l;
+            if (a.c.lse)
+                a.c.lse[r] = bad ? log_l : m == -kInf ? -kInf : m * a.c.scale + log_l;
+            if (a.c.entropy)
+                a.c.entropy[r] = bad ? log_l : m == -kInf ? 0.f : log_l + kLn2 * (u / l);
+        }
+        for (int k = lane; k < a.c.m; k += 64)
+            a.c.logprob[r * a.c.m + k] = logprob(k == lane ? given : logit(k), m, log_l);
+    };
+    if (top == 0) {
+        sums();
         return;
+    }
     int32_t *ids = a.c.top_ids + r * top;
     float *probs = a.c.top_logprob + r * top;
-    for (int k = tid; k < top; k += NR) {
-        ids[k] = -1;
-        probs[k] = bad ? nan : -kInf;
-    }
-    if (bad || m == -kInf)
-        return;
 
-    // the threads' largest logits, several in flight; groups: the lanes
-    const float *tops = a.tops + r * a.shares * NT;
-    const int runs = a.shares * NT;
-    auto for_tops = [&](auto each) __attribute__((always_inline)) {
-        for (int q = tid; q < runs; q += NR * kTops) {
-            float t[kTops];
-#pragma unroll
-            for (int k = 0; k < kTops; ++k)
-                t[k] = q + k * NR < runs ? tops[q + k * NR] : -kInf;
-#pragma unroll
-            for (int k = 0; k < kTops; ++k)
-                each(q + k * NR, t[k]);
-        }
-    };
+    // the maxima of 128 groups (a lane of the even or the odd waves)
     float most = -kInf;
-    for_tops([&](int, float t) { most = fmaxf(most, t); });
-    sValue[tid] = most;
-    __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kWaves; ++k)
-        most = fmaxf(most, sValue[k * 64 + lane]);
-    const float bound = nth_largest(most, top);  // (uniform: every wave has the same maxima)
-    for_tops([&](int q, float t) {
-        if (t >= bound && t > -kInf) {
+    for (int k = 0; k < TOPS; ++k)
+        most = fmaxf(most, t[k]);
+    for (int q = tid + TOPS * NR; q < runs; q += NR)
+        most = fmaxf(most, tops[q]);
+    sMost[wave][lane] = most;
+    __syncthreads();
+    float even = -kInf, odd = -kInf;
+#pragma unroll
+    for (int k = 0; k < kWaves; k += 2) {
+        even = fmaxf(even, sMost[k][lane]);
+        odd = fmaxf(odd, sMost[k + 1][lane]);
+    }
+    const float bound = nth_largest(even, odd, top);  // (uniform: the same in every wave)
+    auto keep = [&](int q, float x) __attribute__((always_inline)) {
+        if (x >= bound && x > -kInf) {
             const int n = atomicAdd(&sRuns, 1);
             if (n < kList)
                 sRun[n] = q;
         }
-    });
+    };
+#pragma unroll
+    for (int k = 0; k < TOPS; ++k)
+        keep(tid + k * NR, t[k]);
+    for (int q = tid + TOPS * NR; q < runs; q += NR)
+        keep(q, tops[q]);
     __syncthreads();
     const int found = sRuns;
     const int each = a.per / NT;  // pieces of a run
@@ -288,19 +299,33 @@ __global__ __launch_bounds__(NR) void row_kernel(LogprobArgs a)
                     }
                 }
         }
+    sums();
     __syncthreads();
+    const float m = sSum[0], log_l = sSum[1];
+    if (log_l != log_l || m == -kInf) {
+        if (tid < top) {
+            ids[tid] = -1;
+            probs[tid] = log_l != log_l ? log_l : -kInf;
+        }
+        return;
+    }
     const int count = sCount;
     if (found <= kList && count <= kList) {
-        for (int n = tid; n < count; n += NR) {
+        // a wave ranks a logit at a time, its lanes holding the others
+        for (int n = wave; n < count; n += kWaves) {
             const float x = sValue[n];
             const int token = sToken[n];
             int rank = 0;
-            for (int k = 0; k < count; ++k)
-                rank += before(sValue[k], sToken[k], x, token);
-            if (rank < top) {
+            for (int k = lane; k < count + 63 - (count + 63) % 64; k += 64)
+                rank += __popcll(__ballot(k < count && before(sValue[k], sToken[k], x, token)));
+            if (rank < top && lane == 0) {
                 ids[rank] = token;
-                probs[rank] = logprob(x);
+                probs[rank] = logprob(x, m, log_l);
             }
+        }
+        for (int k = count + tid; k < top; k += NR) {  // fewer than asked for
+            ids[k] = -1;
+            probs[k] = -kInf;
         }
         return;
     }
@@ -344,11 +369,9 @@ __global__ __launch_bounds__(NR) void row_kernel(LogprobArgs a)
                 token = sI[w];
             }
         __syncthreads();
-        if (x == -kInf)
-            return;  // (uniform)
         if (tid == 0) {
-            ids[k] = token;
-            probs[k] = logprob(x);
+            ids[k] = x == -kInf ? -1 : token;
+            probs[k] = logprob(x, m, log_l);
         }
         last = x;
         last_token = token;
@@ -373,11 +396,11 @@ hipError_t launch_typed(const kvr_ctx *c, const LogprobArgs &a, hipStream_t s)
                                 dim3((unsigned)((int64_t)a.c.n * a.shares)), dim3(NT), 0, s, a);
     if (e != hipSuccess)
         return e;
-    if (a.shares * NT <= 256 * kTops)
-        return launch(c, KVR_KERNEL_LOGPROB, row_kernel<T, 256>, dim3((unsigned)a.c.n), dim3(256), 0,
-                      s, a);
-    return launch(c, KVR_KERNEL_LOGPROB, row_kernel<T, 1024>, dim3((unsigned)a.c.n), dim3(1024), 0, s,
-                  a);
+    if (a.shares <= 16)
+        return launch(c, KVR_KERNEL_LOGPROB, row_kernel<T, 256, 16>, dim3((unsigned)a.c.n),
+                      dim3(256), 0, s, a);
+    return launch(c, KVR_KERNEL_LOGPROB, row_kernel<T, 1024, 16>, dim3((unsigned)a.c.n), dim3(1024),
+                  0, s, a);
 }
 
 }  // namespace

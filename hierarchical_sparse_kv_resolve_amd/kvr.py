@@ -315,8 +315,10 @@ def _pinned(x, name: str, nbytes: int = 0) -> int | None:
     raise TypeError(f"{name}: expected a pinned host tensor or an address, got {type(x)}")
 
 
-def _stream(stream) -> int | None:
+def _stream(stream, here: int | None = None) -> int | None:
     if stream is None:
+        if _raw_stream is not None and here is not None:
+            return _raw_stream(here)
         import torch
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         if raw is not None:  # without building a Stream object for each call
@@ -333,15 +335,31 @@ def _check(rc: int):
     return rc
 
 
+_get_device = _raw_stream = None  # torch's, once it has initialised the GPU
+
+
 def _here() -> int:
     """The current device (which the library requires to be the context's)."""
-    import torch
-    return torch.cuda.current_device()
+    global _get_device, _raw_stream
+    if _get_device is None:
+        import torch
+        here = torch.cuda.current_device()
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        return here
+    return _get_device()
 
 
 def _typed(x, name: str, dtypes, here: int | None = None, shape=None):
     """A strided tensor on the current device (`here`), of one of the dtypes
     (names), whose last dimension is contiguous; its dtype's name."""
+    try:  # (all as it should be, in few steps; else what is wrong is found below)
+        kind = _DTYPE_NAMES[x.dtype]
+        if (kind in dtypes and x.get_device() == here and (shape is None or x.shape == shape)
+                and (x.is_contiguous() or x.stride(-1) == 1)):
+            return kind
+    except (AttributeError, KeyError, IndexError, RuntimeError):
+        pass
     if not getattr(x, "is_cuda", False):
         what = f"one on {x.device}" if hasattr(x, "is_cuda") else type(x)
         raise TypeError(f"{name}: expected a GPU tensor, got {what}")
@@ -359,6 +377,7 @@ def _typed(x, name: str, dtypes, here: int | None = None, shape=None):
 
 
 _DTYPE_NAMES: dict = {}
+_NO_PART = (None, None, 0, 0, 0, 0, 0, 0, 0, 0)
 
 
 def _same_device(x, name: str, here: int | None = None):
@@ -371,6 +390,14 @@ def _same_device(x, name: str, here: int | None = None):
     return x
 
 
+def _full(x, name: str, kind: str, here: int, shape) -> int:
+    """Address of a contiguous tensor of one dtype (by name) and shape on the
+    current device."""
+    if _typed(x, name, (kind,), here, shape) and x.is_contiguous():
+        return x.data_ptr()
+    return _dev(x, name)
+
+
 def _dev_here(x, name: str, nbytes: int = 0, here: int | None = None) -> int | None:
     if x is None or isinstance(x, int):
         return x
@@ -381,6 +408,12 @@ def _words(x, name: str, n: int, here: int | None = None) -> int | None:
     """Address of n 32-bit integers on the current device."""
     if x is None or isinstance(x, int):
         return x
+    try:
+        if (_DTYPE_NAMES[x.dtype] in ("int32", "uint32") and x.get_device() == here
+                and x.is_contiguous() and x.numel() >= n):
+            return x.data_ptr()
+    except (AttributeError, KeyError, RuntimeError):
+        pass
     if hasattr(x, "is_cuda"):
         kind = _DTYPE_NAMES.get(x.dtype)
         if kind is None:
@@ -764,32 +797,42 @@ class Context:
         contiguous; x and key of one type, bf16, fp16 or fp32.  See
         kvr_rotate_rows."""
         here = _here()
-        kind = None
-        parts = []
-        for name, src, dst, first in (("x", x, out, at), ("key", key, key_out, key_at)):
-            if src is None:
-                if dst is not None:
-                    raise ValueError(f"{name}: an output without an input")
-                parts.append(RotatePart())
-                continue
-            dst = src if dst is None else dst
-            if getattr(src, "ndim", 3) != 3:
-                raise ValueError(f"{name}: {src.ndim} dimensions, the call needs "
-                                 "[n, heads, d_head]")
-            kind = _typed(src, name, _VALUE_TYPES if kind is None else (kind,), here)
-            _typed(dst, f"{name}'s output", (kind,), here, src.shape)
-            if src.shape[0] != n:
-                raise ValueError(f"{name}: {src.shape[0]} tokens, the call has {n}")
-            a, b = src.stride(), dst.stride()
-            parts.append(RotatePart(src.data_ptr(), dst.data_ptr(), a[0], a[1], b[0], b[1],
-                                    src.shape[1], src.shape[2], first, 0))
-        if kind is None:
-            raise ValueError("x or key is required")
-        _typed(frequencies, "frequencies", ("float64",), here, (d_rot // 2,))
+        if x is None:
+            if out is not None:
+                raise ValueError("x: an output without an input")
+            if key is None:
+                raise ValueError("x or key is required")
+            kind, first = None, _NO_PART
+        else:
+            kind, first = self._rotate_part(n, x, out, at, "x", _VALUE_TYPES, here)
+        if key is None:
+            if key_out is not None:
+                raise ValueError("key: an output without an input")
+            second = _NO_PART
+        else:
+            kind, second = self._rotate_part(n, key, key_out, key_at, "key",
+                                             _VALUE_TYPES if kind is None else (kind,), here)
+        freq = _full(frequencies, "frequencies", "float64", here, (d_rot // 2,))
         call = RotateCall(_VALUE_TYPES[kind], _choice(layout, "layout", ROPE_LAYOUTS), n, d_rot,
-                          magnitude, int(inverse), _words(positions, "positions", n, here),
-                          frequencies.data_ptr(), *parts)
-        _check(lib().kvr_rotate_rows(self.handle, ctypes.byref(call), _stream(stream)))
+                          magnitude, inverse, _words(positions, "positions", n, here), freq, first,
+                          second)
+        _check(lib().kvr_rotate_rows(self.handle, ctypes.byref(call), _stream(stream, here)))
+
+    @staticmethod
+    def _rotate_part(n, src, dst, at, name, kinds, here):
+        if getattr(src, "ndim", 3) != 3:
+            raise ValueError(f"{name}: {src.ndim} dimensions, the call needs [n, heads, d_head]")
+        kind = _typed(src, name, kinds, here)
+        shape, a = src.shape, src.stride()
+        if shape[0] != n:
+            raise ValueError(f"{name}: {shape[0]} tokens, the call has {n}")
+        if dst is None:
+            p = src.data_ptr()
+            return kind, (p, p, a[0], a[1], a[0], a[1], shape[1], shape[2], at, 0)
+        _typed(dst, f"{name}'s output", (kind,), here, shape)
+        b = dst.stride()
+        return kind, (src.data_ptr(), dst.data_ptr(), a[0], a[1], b[0], b[1], shape[1], shape[2],
+                      at, 0)
 
     @staticmethod
     def logprob_workspace(n, vocab) -> int:
@@ -813,25 +856,28 @@ class Context:
         if (tokens is None) != (logprob is None) or (top_ids is None) != (top_logprob is None):
             raise ValueError("tokens go with logprob, and top_ids with top_logprob")
         if tokens is not None:
-            _typed(tokens, "tokens", ("int32",), here)
-            m = tokens.shape[1] if tokens.ndim == 2 else -1
-            _typed(tokens, "tokens", ("int32",), here, (n, m))
-            _typed(logprob, "logprob", ("float32",), here, (n, m))
+            if getattr(tokens, "ndim", 2) != 2:
+                raise ValueError(f"tokens: {tokens.ndim} dimensions, the call needs [n, m]")
+            shape = (n, int(tokens.shape[1]) if hasattr(tokens, "shape") else 0)
+            m = shape[1]
+            tokens = _full(tokens, "tokens", "int32", here, shape)
+            logprob = _full(logprob, "logprob", "float32", here, shape)
         if top_ids is not None:
-            _typed(top_ids, "top_ids", ("int32",), here)
-            top = top_ids.shape[1] if top_ids.ndim == 2 else -1
-            _typed(top_ids, "top_ids", ("int32",), here, (n, top))
-            _typed(top_logprob, "top_logprob", ("float32",), here, (n, top))
-        for name, t in (("lse", lse), ("entropy", entropy)):
-            if t is not None:
-                _typed(t, name, ("float32",), here, (n,))
+            if getattr(top_ids, "ndim", 2) != 2:
+                raise ValueError(f"top_ids: {top_ids.ndim} dimensions, the call needs [n, top]")
+            shape = (n, int(top_ids.shape[1]) if hasattr(top_ids, "shape") else 0)
+            top = shape[1]
+            top_ids = _full(top_ids, "top_ids", "int32", here, shape)
+            top_logprob = _full(top_logprob, "top_logprob", "float32", here, shape)
+        if lse is not None:
+            lse = _full(lse, "lse", "float32", here, (n,))
+        if entropy is not None:
+            entropy = _full(entropy, "entropy", "float32", here, (n,))
         ws, ws_bytes = _workspace(workspace, here)
         call = LogprobCall(_VALUE_TYPES[kind], n, logits.shape[1], m, top, scale,
-                           logits.data_ptr(), logits.stride(0), _dev(tokens, "tokens"),
-                           _dev(logprob, "logprob"), _dev(lse, "lse"), _dev(entropy, "entropy"),
-                           _dev(top_ids, "top_ids"), _dev(top_logprob, "top_logprob"), ws,
-                           ws_bytes)
-        _check(lib().kvr_token_logprobs(self.handle, ctypes.byref(call), _stream(stream)))
+                           logits.data_ptr(), logits.stride(0), tokens, logprob, lse, entropy,
+                           top_ids, top_logprob, ws, ws_bytes)
+        _check(lib().kvr_token_logprobs(self.handle, ctypes.byref(call), _stream(stream, here)))
 
     # ------------------------------------------- pages shared by requests
 
@@ -1019,7 +1065,8 @@ class DraftRing:
             raise ValueError(f"k: {k.ndim} dimensions, the call needs [n, rows, kv_heads, d_head]")
         kind = _typed(k, "k", _VALUE_TYPES, here)
         shape = (n, int(k.shape[1]), self.kv_heads, self.d_head)
-        _typed(k, "k", (kind,), here, shape)
+        if k.shape != shape:
+            _typed(k, "k", (kind,), here, shape)
         _typed(v, "v", (kind,), here, shape)
         ks, vs = k.stride(), v.stride()
         call = DraftWriteCall(layer, _VALUE_TYPES[kind], n, shape[1],
@@ -1027,7 +1074,7 @@ class DraftRing:
                               _words(count, "count", n, here), k.data_ptr(), v.data_ptr(),
                               ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
                               _words(status, "status", n, here))
-        _check(lib().kvr_draft_write_kv(self.handle, ctypes.byref(call), _stream(stream)))
+        _check(lib().kvr_draft_write_kv(self.handle, ctypes.byref(call), _stream(stream, here)))
 
     def read_kv(self, layer, n, req_ids, k, v, visible=None, status=None, stream=None):
         """The visible rows of a layer, oldest first, into k and v [n, window,
@@ -1036,11 +1083,11 @@ class DraftRing:
         here = _here()
         shape = (n, self.window_rows, self.kv_heads, self.d_head)
         kind = _typed(k, "k", _VALUE_TYPES, here, shape)
-        _typed(v, "v", (kind,), here, shape)
         _check(lib().kvr_draft_read_kv(self.handle, layer, n, _words(req_ids, "req_ids", n, here),
-                                       _VALUE_TYPES[kind], _dev(k, "k"), _dev(v, "v"),
+                                       _VALUE_TYPES[kind], _full(k, "k", kind, here, shape),
+                                       _full(v, "v", kind, here, shape),
                                        _words(visible, "visible", n, here),
-                                       _words(status, "status", n, here), _stream(stream)))
+                                       _words(status, "status", n, here), _stream(stream, here)))
 
     def advance(self, n, req_ids, rows, count=None, status=None, stream=None):
         """The tokens written to the K/V layers (count of each entry, or rows) become
@@ -1048,7 +1095,7 @@ class DraftRing:
         here = _here()
         _check(lib().kvr_draft_advance(self.handle, n, _words(req_ids, "req_ids", n, here), rows,
                                        _words(count, "count", n, here),
-                                       _words(status, "status", n, here), _stream(stream)))
+                                       _words(status, "status", n, here), _stream(stream, here)))
 
     def attend_workspace(self, n, nq, heads) -> int:
         """Workspace bytes for attend calls of up to these sizes."""
@@ -1064,21 +1111,20 @@ class DraftRing:
         here = _here()
         if getattr(q, "ndim", 4) != 4:
             raise ValueError(f"q: {q.ndim} dimensions, the call needs [n, nq, heads, d_head]")
-        kind = ("bfloat16",)
-        _typed(q, "q", kind, here)
+        _typed(q, "q", ("bfloat16",), here)
         shape = (n, int(q.shape[1]), int(q.shape[2]), self.d_head)
-        _typed(q, "q", kind, here, shape)
-        _typed(out, "out", kind, here, shape)
+        if q.shape != shape:
+            _typed(q, "q", ("bfloat16",), here, shape)
+        out = _full(out, "out", "bfloat16", here, shape)
         if lse is not None:
-            _typed(lse, "lse", ("float32",), here, shape[:3])
+            lse = _full(lse, "lse", "float32", here, shape[:3])
         ws, ws_bytes = _workspace(workspace, here)
         qs = q.stride()
         call = DraftAttendCall(layer, _choice(mask, "mask", DRAFT_MASKS), n, shape[1], shape[2],
                                scale, _words(req_ids, "req_ids", n, here),
                                _words(count, "count", n, here), q.data_ptr(), qs[0], qs[1], qs[2],
-                               _dev(out, "out"), _dev(lse, "lse"),
-                               _words(status, "status", n, here), ws, ws_bytes)
-        _check(lib().kvr_draft_attend(self.handle, ctypes.byref(call), _stream(stream)))
+                               out, lse, _words(status, "status", n, here), ws, ws_bytes)
+        _check(lib().kvr_draft_attend(self.handle, ctypes.byref(call), _stream(stream, here)))
 
 
 class StagingPool:

@@ -157,6 +157,7 @@ def test_rows_that_are_not_finite(bad):
     for i, at in enumerate((0, 12345, 19999)):
         x[i, at] = bad
     x[1, 5:9] = -float("inf")
+    x[2, :19999] = -float("inf")  # nothing but the bad one
     tokens = torch.zeros(5, 1, dtype=torch.int32, device=DEV)
     check(x, tokens, 8, 1.0, call(x, tokens, 8))
 
