@@ -36,10 +36,47 @@ struct WriteArgs {
     bool wide;
 };
 
-// The smallest e, as a scale byte, with top <= 448 * 2^e.
-__device__ __forceinline__ int scale_for(float top)
+constexpr uint32_t kInfBits = 0x7F800000u;
+
+// 16 consecutive values.
+template <typename T>
+struct Run {
+    static constexpr int kPer = 16 / sizeof(T);  // values of 16 bytes
+    typedef T vec __attribute__((ext_vector_type(kPer)));
+    vec v[16 / kPer];
+
+    __device__ __forceinline__ float at(int i) const { return (float)v[i / kPer][i % kPer]; }
+    __device__ __forceinline__ void set(int i, float x) { v[i / kPer][i % kPer] = (T)x; }
+    __device__ __forceinline__ void load(const T *p, bool wide)
+    {
+        if (wide) {
+#pragma unroll
+            for (int i = 0; i < 16 / kPer; ++i)
+                v[i] = *reinterpret_cast<const vec *>(p + i * kPer);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                v[i / kPer][i % kPer] = p[i];
+        }
+    }
+};
+
+// The largest magnitude, as the bits of a float.
+template <typename T>
+__device__ __forceinline__ uint32_t largest(const Run<T> &x)
 {
-    const uint32_t u = __float_as_uint(top);  // >= 0 and finite
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const uint32_t u = __float_as_uint(x.at(i)) & 0x7FFFFFFFu;
+        top = top > u ? top : u;
+    }
+    return top;
+}
+
+// The smallest e, as a scale byte, with top <= 448 * 2^e, top's bits being u.
+__device__ __forceinline__ int scale_for(uint32_t u)
+{
     // 448 = 1.75 * 2^8
     const int e = (int)(u >> 23) - 8 + ((u & 0x7FFFFFu) > 0x600000u);
     return e > kMinScale ? e : kMinScale;
@@ -74,6 +111,17 @@ __device__ __forceinline__ u32x4 narrow16(const float (&x)[16], float inv)
     return v;
 }
 
+template <typename T>
+__device__ __forceinline__ u32x4 narrow(const Run<T> &x, float inv)
+{
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = pack_e4m3(x.at(4 * i) * inv, x.at(4 * i + 1) * inv, x.at(4 * i + 2) * inv,
+                         x.at(4 * i + 3) * inv);
+    return v;
+}
+
 // Codes of 16 tokens, all but those of `keep` set to 0.
 __device__ __forceinline__ u32x4 keep_bytes(u32x4 v, uint32_t keep)
 {
@@ -86,6 +134,11 @@ __device__ __forceinline__ u32x4 keep_bytes(u32x4 v, uint32_t keep)
         v[i] &= m;
     }
     return v;
+}
+
+__device__ __forceinline__ bool differ(const u32x4 &a, const u32x4 &b)
+{
+    return ((a[0] ^ b[0]) | (a[1] ^ b[1]) | (a[2] ^ b[2]) | (a[3] ^ b[3])) != 0;
 }
 
 template <int D, typename T>
@@ -136,37 +189,38 @@ __global__ __launch_bounds__(NT) void write_kernel(WriteArgs a)
         old_k = scales[0];
         old_v = scales[1];
     }
-    float nk[kPieces][16], nv[kPieces][16];
+    Run<T> nk[kPieces], nv[kPieces];  // (kept in their type: half the registers)
 #pragma unroll
     for (int p = 0; p < kPieces; ++p) {
         const int q = p * NT + tid, tok = q / kRow, d = q % kRow * 16;
         if ((fresh >> tok) & 1) {
             const int64_t j = first + tok - e.length;
-            load_run<16>(static_cast<const T *>(a.c.k) + i * a.c.k_stride_entry +
-                             j * a.c.k_stride_token + h * a.c.k_stride_head + d, a.wide, nk[p]);
-            load_run<16>(static_cast<const T *>(a.c.v) + i * a.c.v_stride_entry +
-                             j * a.c.v_stride_token + h * a.c.v_stride_head + d, a.wide, nv[p]);
+            nk[p].load(static_cast<const T *>(a.c.k) + i * a.c.k_stride_entry +
+                           j * a.c.k_stride_token + h * a.c.k_stride_head + d, a.wide);
+            nv[p].load(static_cast<const T *>(a.c.v) + i * a.c.v_stride_entry +
+                           j * a.c.v_stride_token + h * a.c.v_stride_head + d, a.wide);
         }
     }
     __syncthreads();
-    float top_k = 0.f, top_v = 0.f, piece_k[kPieces];
+    // maxima as bits, in which an infinity or a NaN is above all
+    uint32_t top_k = 0, top_v = 0, piece_k[kPieces];
 #pragma unroll
     for (int p = 0; p < kPieces; ++p) {
         const int tok = (p * NT + tid) / kRow;
-        piece_k[p] = 0.f;
+        piece_k[p] = 0;
         if ((fresh >> tok) & 1) {
-            bool bad = false;
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-                const bool k_ok = fabsf(nk[p][x]) < __builtin_inff();
-                const bool v_ok = fabsf(nv[p][x]) < __builtin_inff();
-                bad |= !k_ok || !v_ok;
-                nv[p][x] = v_ok ? nv[p][x] : 0.f;
-                piece_k[p] = fmaxf(piece_k[p], fabsf(nk[p][x]));
-                top_v = fmaxf(top_v, fabsf(nv[p][x]));
-            }
+            piece_k[p] = largest(nk[p]);
+            uint32_t piece_v = largest(nv[p]);
+            const bool bad = piece_k[p] >= kInfBits || piece_v >= kInfBits;
             if (bad)
                 atomicOr(&sBad[tok / 32], 1u << (tok % 32));
+            if (piece_v >= kInfBits) {
+#pragma unroll
+                for (int x = 0; x < 16; ++x)
+                    nv[p].set(x, fabsf(nv[p].at(x)) < __builtin_inff() ? nv[p].at(x) : 0.f);
+                piece_v = largest(nv[p]);
+            }
+            top_v = top_v > piece_v ? top_v : piece_v;
         }
     }
     __syncthreads();
@@ -175,10 +229,10 @@ __global__ __launch_bounds__(NT) void write_kernel(WriteArgs a)
     for (int p = 0; p < kPieces; ++p) {
         const int tok = (p * NT + tid) / kRow;
         if ((fresh & ~bad) >> tok & 1)
-            top_k = fmaxf(top_k, piece_k[p]);
+            top_k = top_k > piece_k[p] ? top_k : piece_k[p];
     }
     if (live) {
-        const float k_unit = scale_value(old_k), v_unit = scale_value(old_v);
+        float old_top_k = 0.f, old_top_v = 0.f;
 #pragma unroll
         for (int p = 0; p < kPieces; ++p) {
             const int q = p * NT + tid;
@@ -187,26 +241,30 @@ __global__ __launch_bounds__(NT) void write_kernel(WriteArgs a)
                 widen16(ok[p], x);
 #pragma unroll
                 for (int y = 0; y < 16; ++y)
-                    top_k = fmaxf(top_k, fabsf(x[y]) * k_unit);  // (a NaN is no maximum)
+                    old_top_k = fmaxf(old_top_k, fabsf(x[y]));  // (a NaN is no maximum)
             }
-            ov[p] = keep_bytes(ov[p], (uint32_t)(live >> (q % 4 * 16)));
-            widen16(ov[p], x);
+            widen16(keep_bytes(ov[p], (uint32_t)(live >> (q % 4 * 16))), x);
 #pragma unroll
             for (int y = 0; y < 16; ++y)
-                top_v = fmaxf(top_v, fabsf(x[y]) * v_unit);
+                old_top_v = fmaxf(old_top_v, fabsf(x[y]));
         }
+        const uint32_t k = __float_as_uint(old_top_k * scale_value(old_k));
+        const uint32_t v = __float_as_uint(old_top_v * scale_value(old_v));
+        top_k = top_k > k ? top_k : k;
+        top_v = top_v > v ? top_v : v;
     }
 #pragma unroll
     for (int m = 32; m >= 1; m >>= 1) {
-        top_k = fmaxf(top_k, __shfl_xor(top_k, m));
-        top_v = fmaxf(top_v, __shfl_xor(top_v, m));
+        const uint32_t k = __shfl_xor(top_k, m), v = __shfl_xor(top_v, m);
+        top_k = top_k > k ? top_k : k;
+        top_v = top_v > v ? top_v : v;
     }
     if (lane_id() == 0) {
-        atomicMax(&sTop[0], __float_as_uint(top_k));
-        atomicMax(&sTop[1], __float_as_uint(top_v));
+        atomicMax(&sTop[0], top_k);
+        atomicMax(&sTop[1], top_v);
     }
     __syncthreads();
-    const int e_k = scale_for(__uint_as_float(sTop[0])), e_v = scale_for(__uint_as_float(sTop[1]));
+    const int e_k = scale_for(sTop[0]), e_v = scale_for(sTop[1]);
     // 2^-e; e is in [-100, 120]
     const float inv_k = scale_value(2 * kBias - e_k), inv_v = scale_value(2 * kBias - e_v);
     const float move_k = move_between(old_k, e_k), move_v = move_between(old_v, e_v);
@@ -216,14 +274,18 @@ __global__ __launch_bounds__(NT) void write_kernel(WriteArgs a)
         u32x4 v = {};
         if ((fresh >> tok) & 1) {
             v = (bad >> tok) & 1 ? u32x4{0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu}
-                                 : narrow16(nk[p], inv_k);
-            *reinterpret_cast<u32x4 *>(&sV[tok][d]) = narrow16(nv[p], inv_v);
+                                 : narrow(nk[p], inv_k);
+            *reinterpret_cast<u32x4 *>(&sV[tok][d]) = narrow(nv[p], inv_v);
         } else if ((live >> tok) & 1) {
-            float x[16];
-            widen16(ok[p], x);
-            v = narrow16(x, move_k);
+            v = ok[p];
+            if (e_k != old_k) {
+                float x[16];
+                widen16(v, x);
+                v = narrow16(x, move_k);
+            }
         }
-        *reinterpret_cast<u32x4 *>(codes + q * 16) = v;
+        if (!live || differ(v, ok[p]))
+            *reinterpret_cast<u32x4 *>(codes + q * 16) = v;
     }
     __syncthreads();
 #pragma unroll
@@ -231,16 +293,20 @@ __global__ __launch_bounds__(NT) void write_kernel(WriteArgs a)
         const int q = p * NT + tid, d = q / 4, t0 = q % 4 * 16;
         u32x4 v = {};
         if (live) {
-            float x[16];
-            widen16(ov[p], x);
-            v = narrow16(x, move_v);
+            v = keep_bytes(ov[p], (uint32_t)(live >> t0));
+            if (e_v != old_v) {
+                float x[16];
+                widen16(v, x);
+                v = narrow16(x, move_v);
+            }
         }
         const uint32_t take = (uint32_t)(fresh >> t0) & 0xFFFFu;
 #pragma unroll
         for (int y = 0; y < 16; ++y)
             if ((take >> y) & 1)
                 v[y / 4] |= (uint32_t)sV[t0 + y][d] << (y % 4 * 8);
-        *reinterpret_cast<u32x4 *>(codes + kBlock * D + q * 16) = v;
+        if (!live || differ(v, ov[p]))
+            *reinterpret_cast<u32x4 *>(codes + kBlock * D + q * 16) = v;
     }
     if (tid == 0) {
         scales[0] = (uint8_t)e_k;
