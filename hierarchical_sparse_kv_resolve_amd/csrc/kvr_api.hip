@@ -1031,6 +1031,8 @@ static int check_rotate_part(const kvr_rotate_call &c, const kvr_rotate_part &p,
     if (p.x == p.out && (p.x_stride_token != p.out_stride_token ||
                          p.x_stride_head != p.out_stride_head))
         return fail(KVR_E_ARG, "%s: in place, x and out have the same strides", name);
+    if ((c.n > 1 && p.out_stride_token == 0) || (p.heads > 1 && p.out_stride_head == 0))
+        return fail(KVR_E_ARG, "%s: an output stride of 0", name);
     return KVR_OK;
 }
 

@@ -208,13 +208,13 @@ __global__ __launch_bounds__(NR) void row_kernel(LogprobArgs a)
     auto logprob = [&](float x, float m, float log_l) {
         return log_l != log_l ? log_l : x == -kInf ? -kInf : (x - m) * a.c.scale - log_l;
     };
+    auto logit = [&](int k) {
+        const int token = a.c.tokens[r * a.c.m + k];
+        return token >= 0 && token < a.c.vocab ? (float)row[token] : -kInf;
+    };
     auto sums = [&]() {
         if (wave != kWaves - 1)
             return;
-        auto logit = [&](int k) {
-            const int token = a.c.tokens[r * a.c.m + k];
-            return token >= 0 && token < a.c.vocab ? (float)row[token] : -kInf;
-        };
         const float given = lane < a.c.m ? logit(lane) : 0.f;
         float m = -kInf, l = 0.f, u = 0.f;
         const float *parts = a.parts + r * a.shares * 4;
@@ -239,11 +239,18 @@ __global__ __launch_bounds__(NR) void row_kernel(LogprobArgs a)
             if (a.c.entropy)
                 a.c.entropy[r] = bad ? log_l : m == -kInf ? 0.f : log_l + kLn2 * (u / l);
         }
-        for (int k = lane; k < a.c.m; k += 64)
-            a.c.logprob[r * a.c.m + k] = logprob(k == lane ? given : logit(k), m, log_l);
+        if (lane < a.c.m)
+            a.c.logprob[r * a.c.m + lane] = logprob(given, m, log_l);
+    };
+    // Given tokens past the 64th, once the sums are there.
+    auto others = [&]() {
+        for (int k = 64 + tid; k < a.c.m; k += NR)
+            a.c.logprob[r * a.c.m + k] = logprob(logit(k), sSum[0], sSum[1]);
     };
     if (top == 0) {
         sums();
+        __syncthreads();
+        others();
         return;
     }
     int32_t *ids = a.c.top_ids + r * top;
@@ -301,6 +308,7 @@ __global__ __launch_bounds__(NR) void row_kernel(LogprobArgs a)
         }
     sums();
     __syncthreads();
+    others();
     const float m = sSum[0], log_l = sSum[1];
     if (log_l != log_l || m == -kInf) {
         if (tid < top) {

@@ -584,7 +584,8 @@ typedef enum kvr_rope_layout {
  * value type, strides in elements, the last dimension contiguous; values
  * [at, at + d_rot) of each head are rotated, the others copied.  out == x (with
  * x's strides) rotates in place and leaves the others alone; otherwise out is
- * disjoint from the inputs.  heads 0: no such tensor. */
+ * disjoint from the inputs.  Heads of out do not overlap (strides of 0 are
+ * refused; x's may be 0).  heads 0: no such tensor. */
 typedef struct kvr_rotate_part {
     const void *x;
     void *out;
@@ -890,8 +891,11 @@ int kvr_draft_window(kvr_draft *d, int32_t n, const int32_t *req_ids, void *out,
  *     kvr_draft_window; code * scale in the type asked for (exact in 32 bits
  *     and in bf16).
  *   kvr_draft_advance: length += count and high follows, once the layers have
- *     written their tokens.  What is drafted and rejected is dropped with
- *     kvr_draft_rollback.
+ *     written their tokens (kvr_draft_append does the same, for a drafter with
+ *     rows of both kinds: its K/V layers are written first).  What is drafted and
+ *     rejected is dropped with kvr_draft_rollback: written tokens overwrite the
+ *     rows C positions before them, which high has to know of, so they are
+ *     advanced over before others are written in their place.
  * count (device) int32 [n] or NULL (= rows): new tokens of entry i, 0 to rows;
  * the inputs and outputs of the others are neither read nor written.
  * status (device) int32 [n] or NULL: KVR_OK; KVR_E_ARG for a request or a count

@@ -391,6 +391,25 @@ def test_large_scores():
     check_attend(R, [0], q, "kept", out, lse)
 
 
+def test_a_scale_of_zero():
+    """Every row seen weighs the same; rows left out still weigh nothing."""
+    R = filled(12, 3, 100, 192, 1, 64, [0, 30, 150], 2)
+    q = torch.randn(3, 2, 2, 64, device=DEV).bfloat16()
+    out = torch.zeros_like(q)
+    lse = torch.zeros(3, 2, 2, device=DEV)
+    ws = torch.zeros(R.ring.attend_workspace(3, 2, 2), dtype=torch.uint8, device=DEV)
+    R.ring.attend(0, 3, None, q, out, scale=0.0, lse=lse, workspace=ws)
+    for r, m in enumerate([0, 30, 150]):
+        for j in range(2):
+            lo, hi = ref.span("causal", m, 2, j, 100)
+            v = R.ref.rows(r, lo, hi)[1][0]
+            got = out[r, j].double().cpu().numpy()
+            # weights of 1, exact in bf16; sums of 100 values and the output's rounding
+            assert (np.abs(got - v.mean(0)) <= H * np.abs(v.mean(0)) + 128 * EPS32 *
+                    np.abs(v).mean(0)).all()
+            assert (lse[r, j].cpu() - np.log(hi - lo)).abs().max() <= 16 * EPS32 * (1 + np.log(100))
+
+
 def test_rows_overwritten_after_a_rollback():
     """A query that would see a row that a dropped one has overwritten: the entry is
     refused, the others are not."""

@@ -123,8 +123,10 @@ def test_rows(typ, n, vocab):
 def test_tokens_out_of_range_and_many(typ):
     rng = np.random.default_rng(1)
     x = rows(rng, 2, 500, typ)
-    tokens = torch.from_numpy(rng.integers(-3, 503, (2, 900)).astype(np.int32)).to(DEV)
-    check(x, tokens, 3, 1.0, call(x, tokens, 3))
+    for m in (64, 65, 900):
+        tokens = torch.from_numpy(rng.integers(-3, 503, (2, m)).astype(np.int32)).to(DEV)
+        for top in (0, 3):
+            check(x, tokens, top, 1.0, call(x, tokens, top))
 
 
 @pytest.mark.parametrize("typ", ["bf16", "f16", "f32"])

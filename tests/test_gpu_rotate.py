@@ -235,6 +235,10 @@ def test_refusals():
     refused(ValueError, "x or key", x=None)
     refused(ValueError, "last dimension",
             x=torch.zeros(4, 128, 2, dtype=torch.bfloat16, device=DEV).transpose(1, 2))
+    one = torch.zeros(1, 2, 128, dtype=torch.bfloat16, device=DEV).expand(4, 2, 128)
+    refused(KvrError, "an output stride of 0", x=one)
+    refused(KvrError, "an output stride of 0", out=one)
+    refused(KvrError, "key: an output stride of 0", key=one)
     with pytest.raises(KvrError, match="same strides"):
         c.rotate_rows(**{**good, "out": x.view(-1)[:4 * 2 * 128].as_strided((4, 2, 128),
                                                                           (128, 512, 1))})
