@@ -386,13 +386,23 @@ __global__ __launch_bounds__(NR) void row_kernel(LogprobArgs a)
     }
 }
 
-// A row's shares: a piece for each thread at least, and enough workgroups for
-// the compute units.
+// Shares of a row in which a thread has `pieces` pieces.
+int64_t shares_with(int32_t vocab, int pieces)
+{
+    return ((int64_t)vocab + kRun * NT * pieces - 1) / (kRun * NT * pieces);
+}
+
+// A row's shares: a piece for each thread while that makes up to 512 workgroups;
+// else two at least, and up to 1024 workgroups (16 rows of 131072 logits: 10.7 us
+// with two pieces, 11.7 with one, 11.2 with four; 128 rows: 18.3 with 1024
+// workgroups, 20.2 with 512, 19.9 with 2048).
 int32_t shares_of(int32_t n, int32_t vocab)
 {
-    const int64_t most = ((int64_t)vocab + kRun * NT - 1) / (kRun * NT);
+    const int64_t one = shares_with(vocab, 1), two = shares_with(vocab, 2);
+    if (n * one <= 512)
+        return (int32_t)one;
     const int64_t want = 1024 / n;
-    return (int32_t)(want < 1 ? 1 : want < most ? want : most);
+    return (int32_t)(want < 1 ? 1 : want < two ? want : two);
 }
 
 constexpr int64_t kShareBytes = (NT + 4) * sizeof(float);
@@ -404,8 +414,10 @@ hipError_t launch_typed(const kvr_ctx *c, const LogprobArgs &a, hipStream_t s)
                                 dim3((unsigned)((int64_t)a.c.n * a.shares)), dim3(NT), 0, s, a);
     if (e != hipSuccess)
         return e;
-    if (a.shares <= 16)
-        return launch(c, KVR_KERNEL_LOGPROB, row_kernel<T, 256, 16>, dim3((unsigned)a.c.n),
+    // (512 rows of 32000 logits, 2 shares: 20.0 us with 256 threads a row, 21.2 with
+    // 1024; 128 rows of 131072, 8 shares: 18.6, 17.6; one row, 64 shares: 26, 9.8)
+    if (a.shares <= 4)
+        return launch(c, KVR_KERNEL_LOGPROB, row_kernel<T, 256, 4>, dim3((unsigned)a.c.n),
                       dim3(256), 0, s, a);
     return launch(c, KVR_KERNEL_LOGPROB, row_kernel<T, 1024, 16>, dim3((unsigned)a.c.n), dim3(1024),
                   0, s, a);
@@ -421,7 +433,7 @@ int64_t logprob_workspace(int32_t n, int32_t vocab)
 
 int64_t logprob_workspace_bound(int32_t n, int32_t vocab)
 {
-    const int64_t most = ((int64_t)vocab + kRun * NT - 1) / (kRun * NT) * n;
+    const int64_t most = shares_with(vocab, 1) * n;
     const int64_t many = n > 1024 ? n : 1024;
     return (most < many ? most : many) * kShareBytes;
 }

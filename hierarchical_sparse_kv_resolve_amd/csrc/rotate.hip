@@ -155,15 +155,21 @@ hipError_t launch_rotate(const kvr_ctx *c, const kvr_rotate_call &r, hipStream_t
     if (units == 0)
         return hipSuccess;
     const int pairs = r.d_rot / 2;
-    // tokens of a workgroup: as many as the table holds, while every compute unit
-    // has some
-    int64_t tokens = kTable / pairs < 8 ? kTable / pairs : 8;
-    while (tokens > 1 && r.n / tokens < 1024)
-        tokens /= 2;
+    // Tokens of a workgroup: until each thread has a unit, no more than the table
+    // holds, and fewer where there are not 1024 workgroups.  32768 tokens of 40 heads
+    // of 128 (320 units a token) 115 us with one token, 130 with 8; of 20 heads 61
+    // with 2, 64 with 1 and 65 with 8; 4096 tokens of 16 heads of 576, 64 of them
+    // turned, 38 with 1, 42 with 8.
+    int64_t tokens = 1;
+    while (tokens * units < NT && 2 * tokens <= kTable / pairs && r.n / (2 * tokens) >= 1024)
+        tokens *= 2;
     a.tokens = (int32_t)tokens;
     const int64_t groups = (r.n + tokens - 1) / tokens;
-    int64_t splits = 512 / groups;
-    const int64_t most = (tokens * units + NT - 1) / NT;
+    // Workgroups share tokens that are two rounds or more for one, up to 1024 of them
+    // and a round each (1160 units: 64 tokens in a workgroup each 5.9 us, in 5 3.7, 192
+    // tokens 6.2 and 4.4, 400 8.4 and 7.2; 320 units: 256 tokens 3.8, in two 4.6).
+    int64_t splits = 1024 / groups;
+    const int64_t most = tokens * units < 2 * NT ? 1 : (tokens * units + NT - 1) / NT;
     splits = splits < most ? splits : most;
     a.splits = (int32_t)(splits < 1 ? 1 : splits);
     const dim3 grid((unsigned)(groups * a.splits));
