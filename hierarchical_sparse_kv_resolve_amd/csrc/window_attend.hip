@@ -30,12 +30,13 @@
 //
 // What bounds them (one MI355X):
 //   64 requests x 32 heads (8 K/V) of 128, windows of 4096    97 us, 5.5 TB/s: HBM
-//   one prompt chunk of 2048 tokens, the same heads and window  140 us, 980
+//   one prompt chunk of 2048 tokens, the same heads and window  139 us, 990
 //   TFLOP/s, 0.81 of a large bf16 product: by its counters the matrix units are
 //   busy for 45 % of the cycles and vector instructions issue in 56 %; a matrix
 //   instruction keeps the issue port for half of its time, so the two hardly
 //   overlap
-//   one request's token, window 1024   11 us: latency of 3 blocks a wave
+//   one request's token, window 1024   9 us: latency of 3 blocks a wave, which 8
+//   compute units read
 // (Tried for the prompt chunk: every wave on its own from memory 186 us, its
 // loads a key apart; codes in LDS, converted by each wave, 146; with the
 // exponentials beside the next block's products 154; 4 waves a workgroup 153.)
@@ -388,16 +389,29 @@ __device__ __forceinline__ void write_sums(const AttendArgs &a, const Job &job, 
 }
 
 // Few query rows: the NW waves of a workgroup have the same ones and take every
-// NW-th block of tokens, straight from memory into registers (the next keys once
-// the scores are taken, the next values after the products); their sums are joined
-// through LDS.
+// NW-th block of tokens, from memory into registers (the next keys once the scores
+// are taken, the next values after the products); their sums are joined through LDS.
+//
+// A lane's pieces of a block's values, or of keys of 64, lie in whole lines that one
+// load of the wave takes; those of longer keys would leave each line half read (some
+// 20 bytes a cycle and compute unit), so keys of 128 and 256 are loaded in their order
+// and change lanes through LDS: 8 K/V heads of 128 of one request, window 1024, 8.9
+// us (10.6 without), 1024 tokens 94 (102), but 16 requests of 16 queries x 4 heads 25
+// (24); values as well 9.2, keys of 64 as well 10.0 (9.6: 32 requests of 4 queries).
 template <int D, int MB, int NW>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 2)))
 void split_kernel(AttendArgs a)
 {
     typedef Rows<D, MB> R;
     constexpr int kRows = 16 * MB, kStride = D + 4;
-    __shared__ __attribute__((aligned(16))) float sO[NW * kRows * kStride];
+    constexpr int kPieces = D / 16;  // of a key, and of a lane in a block's keys or values
+    constexpr bool kTurn = D >= 128;
+    // 16-byte pieces of a key lie at piece ^ this, so that the 8 keys which a lane
+    // group reads at once (key_at + 4 j, below) are in different banks
+    auto key_swizzle = [](int t) { return (t & 3) | (t >> 2 & 4); };
+    // a wave's keys; at the end the waves' sums
+    __shared__ __attribute__((aligned(128))) float sO[NW * kRows * kStride];
+    static_assert(!kTurn || sizeof(sO) >= NW * kBlock * D, "a block for each wave");
     __shared__ float sStat[NW * kRows * 2];
     const int lane = lane_id(), col = lane & 15, grp = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(wave_id());
@@ -415,24 +429,25 @@ void split_kernel(AttendArgs a)
     R r;
     r.init(a, e, job.i, job.kvh, x0, rows);
 
-    u32x4 k[4][R::kKeys], v[R::kCols];
+    u32x4 k[kPieces], v[kPieces];
     uint32_t k_scale = 0, v_scale = 0;
     const int64_t head_bytes = 2 * kBlock * D;
     const int64_t first = (int64_t)e.r * a.w.blocks * a.w.kv_heads + job.kvh;
-    const int k_at = ((col >> 2) * 16 + (col & 3)) * D + grp * 16;
-    const int v_at = kBlock * D + col * kBlock + grp * 16;
+    // the lane's operands are pieces n of keys key_at + 4 j, and of values 16 c + col
+    const int key_at = (col >> 2) * 16 + (col & 3);
+    uint8_t *tile = reinterpret_cast<uint8_t *>(sO) + wave * (kBlock * D);
     auto at_block = [&](int b) { return first + (int64_t)(b % a.w.blocks) * a.w.kv_heads; };
     auto load_keys = [&](int64_t at) __attribute__((always_inline)) {
-        const uint8_t *from = a.w.codes + at * head_bytes + k_at;
+        const uint8_t *from = a.w.codes + at * head_bytes;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int n = 0; n < R::kKeys; ++n)
-                k[j][n] = *reinterpret_cast<const u32x4 *>(from + j * 4 * D + n * 64);
+        for (int n = 0; n < kPieces; ++n)
+            k[n] = *reinterpret_cast<const u32x4 *>(
+                from + (kTurn ? n * 1024 + lane * 16
+                              : (key_at + n / R::kKeys * 4) * D + (n % R::kKeys * 4 + grp) * 16));
         k_scale = a.w.scales[at * 2];
     };
     auto load_values = [&](int64_t at) __attribute__((always_inline)) {
-        const uint8_t *from = a.w.codes + at * head_bytes + v_at;
+        const uint8_t *from = a.w.codes + at * head_bytes + kBlock * D + col * kBlock + grp * 16;
 #pragma unroll
         for (int c = 0; c < R::kCols; ++c)
             v[c] = *reinterpret_cast<const u32x4 *>(from + c * 16 * kBlock);
@@ -447,11 +462,27 @@ void split_kernel(AttendArgs a)
         typename R::Scores s;
         float top[MB];
         auto alone = [](int) {};
+        u32x4 turned[kTurn ? kPieces : 1];
+        if constexpr (kTurn) {
+#pragma unroll
+            for (int n = 0; n < kPieces; ++n) {
+                const int t = (n * 64 + lane) / kPieces, piece = lane % kPieces;
+                *reinterpret_cast<u32x4 *>(tile + t * D + (piece ^ key_swizzle(t)) * 16) = k[n];
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+            for (int n = 0; n < kPieces; ++n) {
+                const int t = key_at + n / R::kKeys * 4, piece = n % R::kKeys * 4 + grp;
+                turned[n] =
+                    *reinterpret_cast<const u32x4 *>(tile + t * D + (piece ^ key_swizzle(t)) * 16);
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        }
         r.template scores<1>(
             [&](int g) __attribute__((always_inline)) {
-                const int st = g % R::kSteps;
-                const u32x4 w = k[g / R::kSteps][st / 2];
-                return widen(w[st % 2 * 2], w[st % 2 * 2 + 1], 1.f);
+                const int n = g / 2, half = g % 2 * 2;
+                const u32x4 w = kTurn ? turned[kTurn ? n : 0] : k[n];
+                return widen(w[half], w[half + 1], 1.f);
             },
             s, alone);
         const float factor = score_factor(a.c.scale, k_scale);
@@ -474,6 +505,8 @@ void split_kernel(AttendArgs a)
             load_values(at_next);
     }
 
+    if constexpr (kTurn)
+        __syncthreads();  // (the sums take the tiles' place)
     r.total();
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
@@ -800,21 +833,22 @@ DraftPlan draft_plan(int32_t n, int32_t nq, int32_t heads, int32_t kv_heads, int
     const int64_t units = (int64_t)n * kv_heads;
     const int64_t blocks = ((int64_t)tokens + kBlock - 1) / kBlock + 1;
     // shared_kernel takes whole rounds of the compute units (256 query rows a
-    // workgroup): a chunk of 1024 tokens (128 workgroups) 134 us against 101 split,
-    // 1500 (188) 135 against 149, 2048 (256) 140 against 195, 2400 (300) 262 against
-    // 242, 3000 (375) 264 against 290.  So with 0.7 of its rounds full.  Heads of 256
-    // (128 query rows a workgroup) gain from it, with shares, at any number (chunks of
-    // 128 and 1024 tokens, 16 heads: 41 and 140 us, split 41 and 238), heads of 64 at
-    // none (1024 tokens of 64 heads 101, split 95).
+    // workgroup, with heads of 256 128).  Heads of 128, windows of 4096: a chunk of 1024
+    // tokens (128 workgroups) 118 us against 93 split, 1500 (188) 135, 134, 1700 (213)
+    // 136, 155, 2048 (256) 139, 177, 2400 (300) 261, 216, 3000 (375) 263, 259: so with
+    // 0.75 of its rounds full.  Heads of 256, whose shares fill what half a round
+    // leaves: 512 tokens (64 workgroups) 84, 88, with windows of 1024 47, 37, 700 (88) 133,
+    // 128, 1024 (128) 140, 172: so with half.  Heads of 64 gain from it at no number
+    // (1024 tokens of 64 heads 101, split 99).
     const int64_t shared = 16 * 2 * shared_waves(d_head);
     const int64_t full = units * ((rows + shared - 1) / shared);
-    const int64_t rounds = (full + kUnits - 1) / kUnits;
-    p.split = d_head == 64 || rows < shared || (d_head == 128 && 10 * full < 7 * kUnits * rounds);
+    const int64_t room = (full + kUnits - 1) / kUnits * kUnits;
+    p.split = d_head == 64 || rows < shared || (d_head == 128 ? 4 * full < 3 * room : 2 * full < room);
+    // (blocks of 16 while that leaves no workgroup waiting: 8 requests of 8 queries
+    // x 4 heads, windows of 1024, 11 us, in blocks of 32 17; 64 requests of 5 38, 34)
     p.blocks_of_16 = !p.split ? 2
                      : rows <= 16 || units * ((rows + 15) / 16) <= kUnits ? 1
                                                                           : split_rows(d_head);
-    // (blocks of 16 while that leaves no workgroup waiting: 8 requests of 8 queries
-    // x 4 heads 12 us, in blocks of 32 15; 16 requests of 16 queries x 4 heads 31, 23)
     const int64_t tile = p.split ? 16 * p.blocks_of_16 : shared;
     p.tiles = (int32_t)((rows + tile - 1) / tile);
     const int64_t groups = units * p.tiles;
@@ -823,12 +857,13 @@ DraftPlan draft_plan(int32_t n, int32_t nq, int32_t heads, int32_t kv_heads, int
         p.waves = 4;
     // (8 waves where there are few workgroups: 32 requests of 4 queries x 7 heads of 64
     // 10 us, with 4 waves 12; 512 workgroups, window 256: 15, 12)
-    // Shares where they take 24 blocks of 16 KB or more off a workgroup, which pays
-    // for the join: one request x 32 heads, window 4096, 26 us in one share, 11 in 8
-    // (8 workgroups); 16 requests 34, 33 in 2; window 1024: 16 requests 12, 14 in 2.
+    // Shares where there are three or more and they take 24 blocks of 16 KB off a
+    // workgroup, which pays for the join (8 K/V heads, windows of 4096): one request 18
+    // us in one share, 11 in 8; 8 requests 20, 19 in 4; 16 requests 31, 34 in 2; windows
+    // of 2048: one 11.8, 10.5 in 4; of 1024: 8.8, 9.8 in 4.
     int64_t shares = kUnits / groups;
     shares = shares < blocks / p.waves ? shares : blocks / p.waves;
-    if (shares < 2 || (blocks - blocks / shares) * d_head < 24 * 128)
+    if (shares < (p.split ? 3 : 2) || (blocks - blocks / shares) * d_head < 24 * 128)
         shares = 1;
     p.shares = (int32_t)shares;
     p.workspace = p.shares > 1 ? partial_bytes(units * p.shares * rows, d_head) : 0;

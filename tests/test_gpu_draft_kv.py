@@ -333,7 +333,9 @@ def test_attend_prompts(mask, d, kv, group, nq):
 
 
 @pytest.mark.parametrize("d,n,kv,group,nq,W", [(128, 45, 4, 4, 64, 100), (128, 23, 8, 1, 256, 70),
-                                               (256, 1, 1, 1, 140, 2500), (256, 3, 2, 3, 60, 130)])
+                                               (256, 1, 1, 1, 140, 2500), (256, 3, 2, 3, 60, 130),
+                                               (128, 49, 4, 4, 64, 100), (128, 25, 8, 1, 256, 70),
+                                               (256, 44, 3, 3, 43, 130), (256, 1, 4, 16, 250, 2000)])
 @pytest.mark.parametrize("mask", ["causal", "block"])
 def test_attend_rows_that_share_blocks(d, n, kv, group, nq, W, mask):
     """Enough query rows for the waves of a workgroup to share each block: full ones, and
