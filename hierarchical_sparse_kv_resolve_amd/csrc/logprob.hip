@@ -20,6 +20,13 @@
 // first), which needs no order of arrival.  Rows with so many that the list
 // overflows (equal logits, or large ones that all fell to one group) are
 // searched once for each alternative instead.
+//
+// What they take (one MI355X, 131072 bf16 logits, 20 alternatives): 128 rows 11.0 us,
+// 34 MB at 3.0 TB/s, and 7.0; one row 3.5 and 6.9, the latency of reading the maxima,
+// of three barriers and of reading the runs that reach the bound.  64 alternatives of
+// 64 rows take 8.1 and 10.5 (with 64 groups, of whose maxima the 64th bounds next to
+// nothing, the list overflowed: 190 in all).  128 rows with 8 pieces of a thread in
+// flight 20.1 in all, with 4 18.7.
 #include "block.h"
 #include "kvr_internal.h"
 #include "values.h"

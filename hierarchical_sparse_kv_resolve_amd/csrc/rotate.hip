@@ -4,8 +4,12 @@
 //
 // p f_i is taken in 64 bits and loses its whole turns there (32 bits would leave
 // an error of p 2^-24 turns); sines and cosines are 32-bit.  A workgroup first
-// puts those of its tokens into LDS, then walks their heads, 16 bytes a thread
-// where addresses allow.  Bound by HBM: every value is read and written once.
+// puts those of its tokens into LDS, once for all heads (a 64-bit product, a sine and
+// a cosine a pair would cost more than the turn itself), then walks the heads, 16
+// bytes a thread where addresses allow.  Bound by HBM, every value being read and
+// written once: 32768 tokens of 20 heads of 128 bf16 values 60 us, 336 MB at 5.6 TB/s
+// (partly from the Infinity Cache); 64 tokens of 16 heads of 576 4.9 us, a launch and
+// two dependent loads.
 #include "block.h"
 #include "kvr_internal.h"
 #include "values.h"

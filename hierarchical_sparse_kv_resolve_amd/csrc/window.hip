@@ -14,7 +14,14 @@
 // Writing: one workgroup for each touched block and head.  It reads the block's
 // codes if rows of it are kept, finds what is not finite, the maxima and the
 // scales, then writes the 16-byte pieces that changed.  Values turn through LDS
-// (codes of [token][d] to [d][token]).
+// (codes of [token][d] to [d][token]).  A block and head is the unit because its
+// scale depends on all of it: nothing is exchanged between workgroups.
+//
+// What they take (one MI355X, 8 heads of 128, bf16): 8 chunks of 4096 tokens 49 us,
+// 201 MB read and written at 4.1 TB/s; one token of 64 requests 6.8 us (8.2 with every
+// piece written), latency: lengths, then codes and new values, then three exchanges
+// through LDS.  32 windows of 4096 rows read back 165 us, 805 MB at 4.9 TB/s, the rate
+// of a large copy; one of 1024 rows 5.0 us.
 #include "block.h"
 #include "draft.h"
 #include "kvr_internal.h"

@@ -710,9 +710,13 @@ void shared_kernel(AttendArgs a)
 }
 
 // Joins the shares of each query row: a workgroup per row, its waves taking
-// every fourth share, their sums added in wave order.
+// every fourth share, their sums added in wave order; or, with two shares, a wave
+// per row.  Bound by launch and latency (32 rows of 128 in 8 shares 4.2 us), or by
+// reading the shares (16384 rows of 256 in two 10.5 us, with a workgroup per row
+// 23.5; with 8 shares a wave per row is slower, 4 requests of 32 heads 15.5 us in all
+// against 14.3).
 constexpr int kJoinWaves = 4;
-template <int D>
+template <int D, int PER>  // waves of a row
 __global__ __launch_bounds__(kJoinWaves * 64) void join_kernel(AttendArgs a)
 {
     constexpr int N = D / 64;   // columns of a lane
@@ -720,16 +724,19 @@ __global__ __launch_bounds__(kJoinWaves * 64) void join_kernel(AttendArgs a)
     typedef float vec __attribute__((ext_vector_type(N)));
     __shared__ float sL[kJoinWaves];
     __shared__ vec sO[kJoinWaves][64];
-    const int lane = lane_id(), wave = wave_id();
+    const int lane = lane_id(), wave = wave_id() % PER;
     const int unit_rows = a.c.nq * a.group;
-    const int64_t unit = blockIdx.x / unit_rows;
-    const int x = (int)(blockIdx.x % unit_rows);
-    const int i = (int)(unit / a.w.kv_heads), kvh = (int)(unit % a.w.kv_heads);
+    const uint32_t at_row = blockIdx.x * (kJoinWaves / PER) + wave_id() / PER;
+    const uint32_t unit = at_row / (uint32_t)unit_rows;
+    const int x = (int)(at_row % (uint32_t)unit_rows);
+    const int i = (int)(unit / (uint32_t)a.w.kv_heads), kvh = (int)(unit % (uint32_t)a.w.kv_heads);
+    if (i >= a.c.n)
+        return;
     const Entry e = attend_entry(a, i);
     const int j = x / a.group, h = kvh * a.group + x % a.group;
     if (e.status != KVR_OK || j >= e.count)
         return;
-    const int64_t first = unit * a.shares * unit_rows + x;
+    const int64_t first = (int64_t)unit * a.shares * unit_rows + x;
     auto stat = [&](int s) {
         return *reinterpret_cast<const float2 *>(a.stat + 2 * (first + (int64_t)s * unit_rows));
     };
@@ -741,12 +748,12 @@ __global__ __launch_bounds__(kJoinWaves * 64) void join_kernel(AttendArgs a)
         m = fmaxf(m, __shfl_xor(m, k));
     float l = 0.f;
     vec o = {};
-    for (int s0 = wave; s0 < a.shares; s0 += kJoinWaves * kFlight) {
+    for (int s0 = wave; s0 < a.shares; s0 += PER * kFlight) {
         vec part[kFlight];
         float w[kFlight], ls[kFlight];
 #pragma unroll
         for (int f = 0; f < kFlight; ++f) {
-            const int s = s0 + f * kJoinWaves;
+            const int s = s0 + f * PER;
             w[f] = 0.f;
             ls[f] = 0.f;
             part[f] = vec{};
@@ -764,16 +771,18 @@ __global__ __launch_bounds__(kJoinWaves * 64) void join_kernel(AttendArgs a)
             o += w[f] * part[f];
         }
     }
-    sO[wave][lane] = o;
-    if (lane == 0)
-        sL[wave] = l;
-    __syncthreads();
-    if (wave != 0)
-        return;
+    if constexpr (PER > 1) {
+        sO[wave][lane] = o;
+        if (lane == 0)
+            sL[wave] = l;
+        __syncthreads();
+        if (wave != 0)
+            return;
 #pragma unroll
-    for (int k = 1; k < kJoinWaves; ++k) {
-        l += sL[k];
-        o += sO[k][lane];
+        for (int k = 1; k < PER; ++k) {
+            l += sL[k];
+            o += sO[k][lane];
+        }
     }
     const int64_t at = ((int64_t)i * a.c.nq + j) * a.c.heads + h;
     const float inv = m == -__builtin_inff() && l == 0.f ? 0.f : 1.f / l;
@@ -820,7 +829,13 @@ hipError_t launch_dim(const AttendArgs &a, const DraftPlan &p, dim3 grid, hipStr
     if (e != hipSuccess || a.shares == 1)
         return e;
     const int64_t rows = (int64_t)a.c.n * a.c.nq * a.c.heads;
-    return launch(nullptr, 0, join_kernel<D>, dim3((unsigned)rows), dim3(kJoinWaves * 64), 0, s, a);
+    if constexpr (D == 256)  // (only its shared_kernel makes two shares)
+        if (a.shares == 2)
+            return launch(nullptr, 0, join_kernel<D, 1>,
+                          dim3((unsigned)((rows + kJoinWaves - 1) / kJoinWaves)),
+                          dim3(kJoinWaves * 64), 0, s, a);
+    return launch(nullptr, 0, join_kernel<D, kJoinWaves>, dim3((unsigned)rows),
+                  dim3(kJoinWaves * 64), 0, s, a);
 }
 
 }  // namespace
@@ -838,7 +853,7 @@ DraftPlan draft_plan(int32_t n, int32_t nq, int32_t heads, int32_t kv_heads, int
     // 136, 155, 2048 (256) 139, 177, 2400 (300) 261, 216, 3000 (375) 263, 259: so with
     // 0.75 of its rounds full.  Heads of 256, whose shares fill what half a round
     // leaves: 512 tokens (64 workgroups) 84, 88, with windows of 1024 47, 37, 700 (88) 133,
-    // 128, 1024 (128) 140, 172: so with half.  Heads of 64 gain from it at no number
+    // 128, 1024 (128) 128, 172: so with half.  Heads of 64 gain from it at no number
     // (1024 tokens of 64 heads 101, split 99).
     const int64_t shared = 16 * 2 * shared_waves(d_head);
     const int64_t full = units * ((rows + shared - 1) / shared);
