@@ -1140,8 +1140,8 @@ int kvr_token_logprobs(kvr_ctx *ctx, const kvr_logprob_call *call, void *stream)
     if (c.m < 0 || c.m > (1 << 16) || c.top < 0 || c.top > 64 ||
         (int64_t)c.n * c.m > INT32_MAX)
         return fail(KVR_E_ARG, "m must be in [0, 2^16], top in [0, 64], n * m below 2^31");
-    if (!(c.scale > 0.f) || !std::isfinite(c.scale))
-        return fail(KVR_E_ARG, "scale must be finite and above 0");
+    if (!(c.scale > 0.f) || !(c.scale < 0x1p127f))
+        return fail(KVR_E_ARG, "scale must be finite, above 0 and below 2^127");
     if (c.logits_stride < 0)
         return fail(KVR_E_ARG, "negative stride");
     if (c.n > 0 && (!c.logits || (c.m > 0 && (!c.tokens || !c.logprob)) ||

@@ -630,6 +630,8 @@ int kvr_draft_attend(kvr_draft *d, const kvr_draft_attend_call *call, void *stre
         (int64_t)c.n * c.nq * c.heads > (1 << 22))
         return kvr::api_fail(KVR_E_ARG, "nq must be >= 1, heads a multiple of the K/V heads up to "
                                         "4096, n * nq * heads at most 2^22");
+    if (!(fabsf(c.scale) < 0x1p127f))
+        return kvr::api_fail(KVR_E_ARG, "scale must be finite and below 2^127");
     if (c.mask == KVR_DRAFT_CAUSAL && c.nq > d->C - d->W + 1)
         return kvr::api_fail(KVR_E_ARG, "%d causal queries: the ring keeps the rows of %d", c.nq,
                              d->C - d->W + 1);

@@ -652,7 +652,7 @@ int kvr_rope_frequencies(int32_t d_rot, double base, int32_t scaling, double fac
 
 /* Arguments of kvr_token_logprobs.
  *   logits (device) [n][vocab] of value_type, rows logits_stride elements apart
- *   scale  multiplies the logits (1 / temperature); finite and above 0
+ *   scale  multiplies the logits (1 / temperature); above 0, below 2^127
  *   tokens (device) int32 [n][m]: given tokens of each row, such as the one a
  *     drafter proposed; logprob (device) float [n][m] out
  *   lse, entropy (device) float [n] out, or NULL
@@ -962,8 +962,8 @@ typedef enum kvr_draft_mask {
  *     kvr_draft_attend_workspace(d, n, nq, heads) bytes; written by the call, so
  *     calls that may run at once each need their own
  * heads is a multiple of kv_heads, at most 4096; n * nq * heads at most 2^22;
- * with KVR_DRAFT_CAUSAL nq is at most C - W + 1, with KVR_DRAFT_WHOLE at
- * most C. */
+ * |scale| below 2^127; with KVR_DRAFT_CAUSAL nq is at most C - W + 1, with
+ * KVR_DRAFT_WHOLE at most C. */
 typedef struct kvr_draft_attend_call {
     int32_t layer;
     int32_t mask;  /* kvr_draft_mask */

@@ -647,6 +647,8 @@ def test_refusals():
     refused(a, KvrError, "193 new tokens", good, q=wide, out=wide.clone(), mask="block")
     flat = torch.zeros(q.numel() + 8, dtype=torch.bfloat16, device=DEV)
     refused(a, KvrError, "not aligned", good, out=flat[4:-4].view(q.shape))
+    for scale in (float("nan"), float("inf"), -float("inf"), 2.0 ** 127):
+        refused(a, KvrError, "scale must be finite", good, scale=scale)
     R2 = filled(10, 1, 8000, 8128, 1, 64, [8000], 1)
     q1 = torch.zeros(1, 1, 4, 64, dtype=torch.bfloat16, device=DEV)
     refused(R2.ring.attend, KvrError, "the workspace has 0 bytes", dict(

@@ -274,7 +274,7 @@ def test_refusals():
         with pytest.raises(error, match=match):
             c.token_logprobs(**{**good, **kw})
 
-    for scale in (0.0, -1.0, float("inf"), float("nan")):
+    for scale in (0.0, -1.0, float("inf"), float("nan"), 2.0 ** 127):
         refused(KvrError, "scale must be finite", scale=scale)
     refused(ValueError, "logits: 2 rows", n=3)
     refused(ValueError, "dimensions", logits=x[0])
