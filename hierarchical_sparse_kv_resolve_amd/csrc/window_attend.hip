@@ -710,11 +710,11 @@ void shared_kernel(AttendArgs a)
 }
 
 // Joins the shares of each query row: a workgroup per row, its waves taking
-// every fourth share, their sums added in wave order; or, with two shares, a wave
-// per row.  Bound by launch and latency (32 rows of 128 in 8 shares 4.2 us), or by
-// reading the shares (16384 rows of 256 in two 10.5 us, with a workgroup per row
-// 23.5; with 8 shares a wave per row is slower, 4 requests of 32 heads 15.5 us in all
-// against 14.3).
+// every fourth share, their sums added in wave order; or, of the thousands of rows
+// that shared_kernel leaves, a wave per row.  Bound by launch and latency (32 rows of
+// 128 in 8 shares 4.2 us), or by reading the shares (16384 rows of 256 in two 10.5
+// us, with a workgroup per row 23.5; of few rows a wave per row is slower, 4 requests
+// of 32 heads in 8 shares 15.5 us in all against 14.3).
 constexpr int kJoinWaves = 4;
 template <int D, int PER>  // waves of a row
 __global__ __launch_bounds__(kJoinWaves * 64) void join_kernel(AttendArgs a)
@@ -829,8 +829,8 @@ hipError_t launch_dim(const AttendArgs &a, const DraftPlan &p, dim3 grid, hipStr
     if (e != hipSuccess || a.shares == 1)
         return e;
     const int64_t rows = (int64_t)a.c.n * a.c.nq * a.c.heads;
-    if constexpr (D == 256)  // (only its shared_kernel makes two shares)
-        if (a.shares == 2)
+    if constexpr (D == 256)  // (the only one whose shared_kernel makes shares)
+        if (!p.split)
             return launch(nullptr, 0, join_kernel<D, 1>,
                           dim3((unsigned)((rows + kJoinWaves - 1) / kJoinWaves)),
                           dim3(kJoinWaves * 64), 0, s, a);
@@ -851,14 +851,18 @@ DraftPlan draft_plan(int32_t n, int32_t nq, int32_t heads, int32_t kv_heads, int
     // workgroup, with heads of 256 128).  Heads of 128, windows of 4096: a chunk of 1024
     // tokens (128 workgroups) 118 us against 93 split, 1500 (188) 135, 134, 1700 (213)
     // 136, 155, 2048 (256) 139, 177, 2400 (300) 261, 216, 3000 (375) 263, 259: so with
-    // 0.75 of its rounds full.  Heads of 256, whose shares fill what half a round
-    // leaves: 512 tokens (64 workgroups) 84, 88, with windows of 1024 47, 37, 700 (88) 133,
-    // 128, 1024 (128) 128, 172: so with half.  Heads of 64 gain from it at no number
-    // (1024 tokens of 64 heads 101, split 99).
+    // 0.75 of its rounds full.  Heads of 256, whose shares fill a part of one round: 256
+    // tokens (32 workgroups, one round of the other kernel) 53, 46, 300 (40) 58, 85, 512
+    // (64) 78, 89, with windows of 1024 41, 37, 1024 (128) 128, 172; 2400 (300) 415, 414,
+    // 2700 (340) 415, 457: so past an eighth, and past one round with 0.6.  Heads of 64
+    // gain from it at no number (1024 tokens of 64 heads 101, split 99).
     const int64_t shared = 16 * 2 * shared_waves(d_head);
     const int64_t full = units * ((rows + shared - 1) / shared);
     const int64_t room = (full + kUnits - 1) / kUnits * kUnits;
-    p.split = d_head == 64 || rows < shared || (d_head == 128 ? 4 * full < 3 * room : 2 * full < room);
+    p.split = d_head == 64 || rows < shared ||
+              (d_head == 128    ? 4 * full < 3 * room
+               : full <= kUnits ? 8 * full <= kUnits
+                                : 5 * full < 3 * room);
     // (blocks of 16 while that leaves no workgroup waiting: 8 requests of 8 queries
     // x 4 heads, windows of 1024, 11 us, in blocks of 32 17; 64 requests of 5 38, 34)
     p.blocks_of_16 = !p.split ? 2

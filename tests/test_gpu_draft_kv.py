@@ -335,7 +335,8 @@ def test_attend_prompts(mask, d, kv, group, nq):
 @pytest.mark.parametrize("d,n,kv,group,nq,W", [(128, 45, 4, 4, 64, 100), (128, 23, 8, 1, 256, 70),
                                                (256, 1, 1, 1, 140, 2500), (256, 3, 2, 3, 60, 130),
                                                (128, 49, 4, 4, 64, 100), (128, 25, 8, 1, 256, 70),
-                                               (256, 44, 3, 3, 43, 130), (256, 1, 4, 16, 250, 2000)])
+                                               (256, 44, 3, 3, 43, 130), (256, 1, 4, 16, 250, 2000),
+                                               (256, 1, 4, 4, 320, 900)])
 @pytest.mark.parametrize("mask", ["causal", "block"])
 def test_attend_rows_that_share_blocks(d, n, kv, group, nq, W, mask):
     """Enough query rows for the waves of a workgroup to share each block: full ones, and
@@ -349,6 +350,22 @@ def test_attend_rows_that_share_blocks(d, n, kv, group, nq, W, mask):
     q = torch.randn(n, nq, kv * group, d, device=DEV).bfloat16()
     out, lse = attend(R, list(range(n)), q, mask, count)
     check_attend(R, list(range(n)), q, mask, out, lse, count)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_a_workspace_covers_smaller_calls(d):
+    kv, W = 2, 3000
+    ring = filled(d, 6, W, 3456, kv, d, [W] * 6, 1).ring
+    big = (6, 300, 16)
+    ws = torch.empty(ring.attend_workspace(*big), dtype=torch.uint8, device=DEV)
+    for n in (1, 2, 3, 5, 6):
+        for nq in (1, 2, 5, 16, 60, 150, 250, 300):
+            for heads in (2, 4, 10, 16):
+                q = torch.zeros(n, nq, heads, d, dtype=torch.bfloat16, device=DEV)
+                for mask in ("causal", "block", "kept"):
+                    ring.attend(0, n, None, q, torch.empty_like(q), scale=1.0, mask=mask,
+                                workspace=ws)
+                assert ring.attend_workspace(n, nq, heads) <= ws.numel()
 
 
 @pytest.mark.parametrize("W,nq,n", [(1, 1, 2), (1, 5, 1), (64, 1, 1), (5000, 1, 1), (3500, 3, 3),
