@@ -172,12 +172,15 @@ __global__ __launch_bounds__(NT) void write_kernel(WriteArgs a)
     uint8_t *codes = a.w.codes + unit * (2 * kBlock * D);
     uint8_t *scales = a.w.scales + unit * 2;
 
-    // which tokens are new, and which slots hold rows that are kept
+    // which tokens are new, and which slots hold rows that are kept: what a slot holds is
+    // the last position below `high` that falls to it (a dropped token may have taken the
+    // place of a row of this lap that is below `length`)
     const int64_t pos = first + lane_id();
     const bool is_new = pos >= e.length && pos < (int64_t)e.length + e.count;
     const int64_t was = pos < e.high ? pos : pos - a.w.C;
     const uint64_t fresh = __ballot(is_new);
-    const uint64_t live = __ballot(!is_new && was >= 0 && was < e.length);
+    const uint64_t live = __ballot(!is_new && was >= 0 && was < e.length &&
+                                   was >= (int64_t)e.high - a.w.C);
     if (tid < 2) {
         sBad[tid] = 0;
         sTop[tid] = 0;
