@@ -44,6 +44,9 @@ struct WriteArgs {
 };
 
 constexpr uint32_t kInfBits = 0x7F800000u;
+// 248 * 2^120: from here on the nearest code of a block's largest scale is 256, which
+// would stand for 2^128.
+constexpr uint32_t kPastBits = 0x7F780000u;
 
 // 16 consecutive values.
 template <typename T>
@@ -79,6 +82,19 @@ __device__ __forceinline__ uint32_t largest(const Run<T> &x)
         top = top > u ? top : u;
     }
     return top;
+}
+
+// Values as codes can hold them: 240 * 2^120 for those past it, 0 for what is no number.
+template <typename T>
+__device__ __forceinline__ void hold(Run<T> &x)
+{
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float y = x.at(i), size = fabsf(y);
+        x.set(i, size < __uint_as_float(kPastBits) ? y
+                 : size < __builtin_inff()         ? copysignf(240.f * 0x1p120f, y)
+                                                   : 0.f);
+    }
 }
 
 // The smallest e, as a scale byte, with top <= 448 * 2^e, top's bits being u.
@@ -224,10 +240,12 @@ __global__ __launch_bounds__(NT) void write_kernel(WriteArgs a)
             const bool bad = piece_k[p] >= kInfBits || piece_v >= kInfBits;
             if (bad)
                 atomicOr(&sBad[tok / 32], 1u << (tok % 32));
-            if (piece_v >= kInfBits) {
-#pragma unroll
-                for (int x = 0; x < 16; ++x)
-                    nv[p].set(x, fabsf(nv[p].at(x)) < __builtin_inff() ? nv[p].at(x) : 0.f);
+            if (piece_k[p] >= kPastBits) {
+                hold(nk[p]);
+                piece_k[p] = largest(nk[p]);
+            }
+            if (piece_v >= kPastBits) {
+                hold(nv[p]);
                 piece_v = largest(nv[p]);
             }
             top_v = top_v > piece_v ? top_v : piece_v;

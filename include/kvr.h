@@ -880,7 +880,9 @@ int kvr_draft_window(kvr_draft *d, int32_t n, const int32_t *req_ids, void *out,
  *     kvr_draft_advance.  A block's scale becomes the smallest power of two
  *     (2^-100 at least) with which its largest value is at most 448, over
  *     the rows it then holds: new ones and those kept.  New values are
- *     rounded once, to the nearest code; codes of rows kept are moved to a
+ *     rounded once, to the nearest code (magnitudes that would become 2^128, from
+ *     248 * 2^120 on, to 240 * 2^120, so that rows read back are finite in 32 bits
+ *     and in bf16); codes of rows kept are moved to a
  *     changed scale, which is exact but for values that fall below the smallest
  *     normal code.  Slots of a touched block that hold no row (not written yet,
  *     or dropped by a rollback) become 0, others are left as they were.  A token

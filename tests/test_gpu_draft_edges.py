@@ -1,5 +1,6 @@
 """The drafter's window in 8 bits at its edges: windows shorter than a block after
-rollbacks that dropped tokens have wrapped past.  Codes and scales bit for bit, as
+rollbacks that dropped tokens have wrapped past, values at the top of the types'
+range.  Codes and scales bit for bit, as
 in test_gpu_draft_kv.py (no tolerance); attention by that file's bounds."""
 from __future__ import annotations
 
@@ -7,7 +8,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_draft_kv import DEV, Ring, attend, check_attend, values
+from tests.test_gpu_draft_kv import DEV, TYPE, Ring, attend, check_attend, values
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +46,39 @@ def test_dropped_rows_that_wrapped_into_the_block(W, C, d, typ):
         out, lse = attend(R, [0, 1], q, "causal")
         check_attend(R, [0, 1], q, "causal", out, lse)
         R.advance([0, 1], rows)
+
+
+@pytest.mark.parametrize("typ", ["bf16", "f32"])
+def test_values_at_the_top_of_the_range(typ):
+    """Magnitudes whose nearest code would stand for 2^128 take the one below it, 240 *
+    2^120: rows read back are finite, and so are queries that do not see them."""
+    rng = np.random.default_rng(9)
+    kv, d, W, C = 2, 64, 64, 192
+    R = Ring(1, W, C, kv, d)
+    most, tie = torch.finfo(TYPE[typ]).max, 248 * 2.0 ** 120
+    hold = lambda x: np.where(np.isfinite(x) & (np.abs(x) >= tie),  # noqa: E731
+                              np.sign(x) * 240 * 2.0 ** 120, x)
+    write = R.ref.write
+    R.ref.write = lambda r, k, v: write(r, hold(k), hold(v))
+    k, v = values(rng, (1, 100, kv, d), 0.3), values(rng, (1, 100, kv, d), 0.3)
+    v[0, 70, 1, :6] = most, -most, tie, 247 * 2.0 ** 120, -2.0 ** 127, 1.0
+    v[0, 71, 0, 5] = np.inf  # (its neighbours of that token stay values)
+    v[0, 71, 0, 6] = -most
+    k[0, 99, 0, :2] = -most, 232 * 2.0 ** 120
+    R.write([0], k, v, typ=typ)
+    R.check()
+    q = torch.randn(1, 70, 4 * kv, d, device=DEV).bfloat16()
+    out, lse = attend(R, [0], q, "causal")  # positions 0 to 69, in the block of the 70th
+    check_attend(R, [0], q, "causal", out, lse)
+    R.advance([0], 100)
+    x = values(rng, (1, 1, kv, d))
+    R.write([0], x, x, typ=typ)  # as rows kept
+    R.check()
+    R.advance([0], 1)
+    got = torch.zeros(1, W, kv, d, device=DEV), torch.zeros(1, W, kv, d, device=DEV)
+    R.ring.read_kv(0, 1, None, *got)
+    for a, b in zip(got, R.ref.rows(0, 101 - W, 101)):
+        b = torch.from_numpy(b).float().transpose(0, 1)
+        nan = a[0].cpu().isnan()
+        assert torch.equal(nan, b.isnan()) and torch.equal(a[0].cpu()[~nan], b[~nan])
+        assert (a[0][~a[0].isnan()].abs() <= 240 * 2.0 ** 120).all()
