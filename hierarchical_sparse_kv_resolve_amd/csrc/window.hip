@@ -359,8 +359,10 @@ __global__ __launch_bounds__(NT) void read_kernel(ReadArgs a)
     __shared__ __attribute__((aligned(16))) uint8_t sV[D][kBlock + 4];
     const int h = blockIdx.y, tid = threadIdx.x;
     const int i = blockIdx.x / a.blocks, t = blockIdx.x % a.blocks;
-    const Entry e = entry_of(a.w, a.req_ids, nullptr, 0, i);
+    Entry e = entry_of(a.w, a.req_ids, nullptr, 0, i);
     const int32_t lo = e.length > a.w.W ? e.length - a.w.W : 0;
+    if (e.status == KVR_OK && lo < e.high - a.w.C)
+        e.status = KVR_E_RANGE;
     if (h == 0 && t == 0 && tid == 0) {
         if (a.status)
             a.status[i] = e.status;

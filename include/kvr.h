@@ -891,7 +891,11 @@ int kvr_draft_window(kvr_draft *d, int32_t n, const int32_t *req_ids, void *out,
  *     see it, and in no others.
  *   kvr_draft_read_kv: the visible rows of one layer, oldest first, as
  *     kvr_draft_window; code * scale in the type asked for (exact in 32 bits
- *     and in bf16).
+ *     and in bf16).  Status KVR_E_RANGE for an entry of which a visible row has
+ *     been overwritten by a later one.  The ring learns of written tokens by
+ *     kvr_draft_advance: before it, where more than C - W are written, the oldest
+ *     rows seen by this call, and by queries of KVR_DRAFT_KEPT, are already those
+ *     tokens, with status KVR_OK.
  *   kvr_draft_advance: length += count and high follows, once the layers have
  *     written their tokens (kvr_draft_append does the same, for a drafter with
  *     rows of both kinds: its K/V layers are written first).  What is drafted and

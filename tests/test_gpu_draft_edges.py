@@ -1,6 +1,6 @@
 """The drafter's window in 8 bits at its edges: windows shorter than a block after
 rollbacks that dropped tokens have wrapped past, values at the top of the types'
-range.  Codes and scales bit for bit, as
+range, windows whose rows are gone.  Codes and scales bit for bit, as
 in test_gpu_draft_kv.py (no tolerance); attention by that file's bounds."""
 from __future__ import annotations
 
@@ -8,7 +8,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_draft_kv import DEV, TYPE, Ring, attend, check_attend, values
+from tests.test_gpu_draft_kv import DEV, TYPE, Ring, attend, check_attend, filled, i32, values
 
 pytestmark = pytest.mark.gpu
 
@@ -82,3 +82,26 @@ def test_values_at_the_top_of_the_range(typ):
         nan = a[0].cpu().isnan()
         assert torch.equal(nan, b.isnan()) and torch.equal(a[0].cpu()[~nan], b[~nan])
         assert (a[0][~a[0].isnan()].abs() <= 240 * 2.0 ** 120).all()
+
+
+def test_read_back_of_overwritten_rows():
+    """A window that reaches below the oldest position the ring still holds is refused;
+    one that ends there is not, and neither are the other entries."""
+    from hierarchical_sparse_kv_resolve_amd import kvr
+    W, C = 100, 192
+    R = filled(3, 3, W, C, 1, 64, [300, 300, 300], 0)
+    for length, want in ((300, 0), (208, 0), (207, kvr.E_RANGE), (120, kvr.E_RANGE)):
+        R.length[1] = length  # below a rollback's limit, 208, from 207 on
+        k, v = (torch.full((3, W, 1, 64), 7.0, device=DEV) for _ in range(2))
+        vis, status = i32([9] * 3), i32([9] * 3)
+        R.ring.read_kv(0, 3, None, k, v, vis, status)
+        torch.cuda.synchronize()
+        assert status.tolist() == [0, want, 0]
+        assert vis.tolist() == [W, 9 if want else W, W]
+        for r in range(3):
+            end = length if r == 1 else 300
+            if r == 1 and want:
+                assert (k[r] == 7).all() and (v[r] == 7).all()
+                continue
+            for got, x in zip((k, v), R.ref.rows(r, end - W, end)):
+                assert torch.equal(got[r].cpu(), torch.from_numpy(x).float().transpose(0, 1))
