@@ -7,6 +7,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <new>
+#include <utility>
 
 #include "kvr_internal.h"
 #include "rowformat.h"
@@ -1009,6 +1010,28 @@ int kvr_attend_rows(kvr_ctx *ctx, const kvr_attend_call *call, void *stream)
 
 // ------------------------------------------------- positions and scores
 
+// Whether heads of d values, token and head strides apart (each above 0 where there
+// are several), overlap: t tokens one way and h heads the other may come within d.
+static bool heads_overlap(int64_t n, int64_t heads, int64_t token, int64_t head, int64_t d)
+{
+    if ((n > 1 && token < d) || (heads > 1 && head < d))
+        return true;
+    typedef __int128 wide;
+    if (n == 1 || heads == 1 || token >= (wide)(heads - 1) * head + d ||
+        head >= (wide)(n - 1) * token + d)
+        return false;
+    if (n < heads) {
+        std::swap(n, heads);
+        std::swap(token, head);
+    }
+    for (int64_t h = 1; h < heads; ++h) {
+        const wide at = (wide)h * head, t = at / token;  // below it and above it
+        if ((t < n && at - t * token < d) || (t + 1 < n && (t + 1) * token - at < d))
+            return true;
+    }
+    return false;
+}
+
 static int check_rotate_part(const kvr_rotate_call &c, const kvr_rotate_part &p, const char *name)
 {
     if (p.heads < 0 || p.heads >= (1 << 24) || p.reserved != 0)
@@ -1033,6 +1056,8 @@ static int check_rotate_part(const kvr_rotate_call &c, const kvr_rotate_part &p,
         return fail(KVR_E_ARG, "%s: in place, x and out have the same strides", name);
     if ((c.n > 1 && p.out_stride_token == 0) || (p.heads > 1 && p.out_stride_head == 0))
         return fail(KVR_E_ARG, "%s: an output stride of 0", name);
+    if (c.n > 0 && heads_overlap(c.n, p.heads, p.out_stride_token, p.out_stride_head, p.d_head))
+        return fail(KVR_E_ARG, "%s: heads of the output overlap", name);
     return KVR_OK;
 }
 

@@ -584,8 +584,8 @@ typedef enum kvr_rope_layout {
  * value type, strides in elements, the last dimension contiguous; values
  * [at, at + d_rot) of each head are rotated, the others copied.  out == x (with
  * x's strides) rotates in place and leaves the others alone; otherwise out is
- * disjoint from the inputs.  Heads of out do not overlap (strides of 0 are
- * refused; x's may be 0).  heads 0: no such tensor. */
+ * disjoint from the inputs.  Strides of out with which its heads would overlap
+ * are refused (x's may be 0).  heads 0: no such tensor. */
 typedef struct kvr_rotate_part {
     const void *x;
     void *out;
