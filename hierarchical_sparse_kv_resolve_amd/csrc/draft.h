@@ -77,7 +77,8 @@ __device__ __forceinline__ Entry entry_of(const Window &w, const int32_t *req_id
 
 int draft_prologue(const kvr_draft *d, int32_t n, hipStream_t s);
 
-// Argument checks of the K/V calls: the ring, its layer, and the stream's device.
+// Argument checks of the K/V calls: the ring and the stream's device; with them the layer.
+int check_draft_stream(const kvr_draft *d, int32_t n, hipStream_t s);
 int check_draft_kv(const kvr_draft *d, int32_t layer, int32_t n, hipStream_t s);
 
 hipError_t launch_draft_write(const kvr_draft *d, const kvr_draft_write_call &c, hipStream_t s);

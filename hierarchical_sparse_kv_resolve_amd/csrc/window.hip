@@ -504,14 +504,10 @@ hipError_t launch_draft_advance(const kvr_draft *d, int32_t n, const int32_t *re
                   n, req_ids, rows, count, d->length, d->high, status);
 }
 
-int check_draft_kv(const kvr_draft *d, int32_t layer, int32_t n, hipStream_t s)
+int check_draft_stream(const kvr_draft *d, int32_t n, hipStream_t s)
 {
     if (int rc = draft_prologue(d, n, s))
         return rc;
-    if (!d->codes)
-        return api_fail(KVR_E_ARG, "no K/V layers bound");
-    if (layer < 0 || layer >= d->kv_layers)
-        return api_fail(KVR_E_ARG, "layer %d outside [0, %d)", layer, d->kv_layers);
     if (s) {
         hipDevice_t dev = -1;
         const hipError_t e = hipStreamGetDevice(s, &dev);
@@ -521,6 +517,17 @@ int check_draft_kv(const kvr_draft *d, int32_t layer, int32_t n, hipStream_t s)
             return api_fail(KVR_E_ARG, "the stream is on device %d, not the ring's device %d",
                             (int)dev, d->device);
     }
+    return KVR_OK;
+}
+
+int check_draft_kv(const kvr_draft *d, int32_t layer, int32_t n, hipStream_t s)
+{
+    if (int rc = check_draft_stream(d, n, s))
+        return rc;
+    if (!d->codes)
+        return api_fail(KVR_E_ARG, "no K/V layers bound");
+    if (layer < 0 || layer >= d->kv_layers)
+        return api_fail(KVR_E_ARG, "layer %d outside [0, %d)", layer, d->kv_layers);
     return KVR_OK;
 }
 
@@ -615,7 +622,7 @@ int kvr_draft_advance(kvr_draft *d, int32_t n, const int32_t *req_ids, int32_t r
                       const int32_t *count, int32_t *status, void *stream)
 {
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if (int rc = kvr::draft_prologue(d, n, s))
+    if (int rc = kvr::check_draft_stream(d, n, s))
         return rc;
     if (rows < 0)
         return kvr::api_fail(KVR_E_ARG, "negative row count");
