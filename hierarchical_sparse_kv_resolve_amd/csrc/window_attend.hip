@@ -210,10 +210,9 @@ struct Rows {
     }
 
     // Products with a block's keys: key(g) is the lane's operand of step g % kSteps of
-    // tile g / kSteps.  Operands are asked for `AHEAD` steps early, and beside(g) is
-    // issued while the matrix unit works on step g (fences keep it so).
-    template <int AHEAD, typename K, typename F>
-    __device__ __forceinline__ void scores(K key, Scores &s, F beside)
+    // tile g / kSteps.  Operands are asked for `AHEAD` steps early (fences keep it so).
+    template <int AHEAD, typename K>
+    __device__ __forceinline__ void scores(K key, Scores &s)
     {
         constexpr int N = 4 * kSteps;
         frag k[N];
@@ -229,7 +228,6 @@ struct Rows {
                 s[j][mb] = mfma(k[g], q[mb][st], st == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : s[j][mb]);
             if (g + AHEAD < N)
                 k[g + AHEAD] = key(g + AHEAD);
-            beside(g);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
@@ -252,11 +250,11 @@ struct Rows {
     }
 
     // Scores relative to the reference, t - m, in place of the products (factor makes
-    // t of one), and the lane's largest of each block of rows: part g of `of`.
-    __device__ __forceinline__ void relative(Scores &s, float factor, float (&top)[MB], int g, int of)
+    // t of one), and the lane's largest of each block of rows.
+    __device__ __forceinline__ void relative(Scores &s, float factor, float (&top)[MB])
     {
 #pragma unroll
-        for (int e = g * 8 * MB / of; e < (g + 1) * 8 * MB / of; ++e) {
+        for (int e = 0; e < 8 * MB; ++e) {
             const int mb = e / 8, j = e / 2 % 4, x = e % 2 * 2;
             const float y0 = fmaf(s[j][mb][x], factor, -ref[mb]);
             const float y1 = fmaf(s[j][mb][x + 1], factor, -ref[mb]);
@@ -300,11 +298,11 @@ struct Rows {
         }
     }
 
-    // Probabilities of a block: part g of `of`, in pairs.
-    __device__ __forceinline__ void probabilities(const Scores &s, int g, int of)
+    // Probabilities of a block, in pairs.
+    __device__ __forceinline__ void probabilities(const Scores &s)
     {
 #pragma unroll
-        for (int e = g * 8 * MB / of; e < (g + 1) * 8 * MB / of; ++e) {
+        for (int e = 0; e < 8 * MB; ++e) {
             const int mb = e / 8, j = e / 2 % 4, x = e % 2 * 2;
             const float y0 = exp2_hw(s[j][mb][x]), y1 = exp2_hw(s[j][mb][x + 1]);
             l[mb] += y0;
@@ -319,8 +317,8 @@ struct Rows {
 
     // Sums over a block's values: value(g) is the lane's operand of tokens 8 (g % 2) ..
     // of each 16, columns 16 (g / 2) ..; as in scores.
-    template <int AHEAD, typename V, typename F>
-    __device__ __forceinline__ void values(V value, F beside)
+    template <int AHEAD, typename V>
+    __device__ __forceinline__ void values(V value)
     {
         constexpr int N = 2 * kCols;
         frag v[N];
@@ -335,7 +333,6 @@ struct Rows {
                 o[g / 2][mb] = mfma(v[g], __builtin_bit_cast(frag, p[g % 2][mb]), o[g / 2][mb]);
             if (g + AHEAD < N)
                 v[g + AHEAD] = value(g + AHEAD);
-            beside(g);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
@@ -461,7 +458,6 @@ void split_kernel(AttendArgs a)
     for (; b < span.b1; b += NW) {
         typename R::Scores s;
         float top[MB];
-        auto alone = [](int) {};
         u32x4 turned[kTurn ? kPieces : 1];
         if constexpr (kTurn) {
 #pragma unroll
@@ -484,7 +480,7 @@ void split_kernel(AttendArgs a)
                 const u32x4 w = kTurn ? turned[kTurn ? n : 0] : k[n];
                 return widen(w[half], w[half + 1], 1.f);
             },
-            s, alone);
+            s);
         const float factor = score_factor(a.c.scale, k_scale);
         const bool more = b + NW < span.b1;
         const int64_t at_next = at_block(b + NW);
@@ -492,15 +488,14 @@ void split_kernel(AttendArgs a)
             load_keys(at_next);
         if (b < span.full0 || b >= span.full1)
             r.mask(s, b);
-        r.relative(s, factor, top, 0, 1);
+        r.relative(s, factor, top);
         r.settle(s, top);
-        r.probabilities(s, 0, 1);
+        r.probabilities(s);
         const float unit = scale_value(v_scale);
         r.template values<1>(
             [&](int g) __attribute__((always_inline)) {
                 return widen(v[g / 2][g % 2 * 2], v[g / 2][g % 2 * 2 + 1], unit);
-            },
-            alone);
+            });
         if (more)
             load_values(at_next);
     }
@@ -565,7 +560,8 @@ void shared_kernel(AttendArgs a)
 {
     typedef Rows<D, MB> R;
     constexpr int kPart = kBlock * D / NW / 16;       // 16-code pieces of a wave, keys or values
-    constexpr int kLoads = (kPart + 63) / 64;
+    constexpr int kLoads = kPart / 64;
+    static_assert(D >= 128 && kPart % 64 == 0, "every lane has pieces, keys take 4 steps or more");
     constexpr int kHalf = 2 * kBlock * D;             // bytes of a block's keys or values
     __shared__ __attribute__((aligned(1024))) uint8_t sTile[2][2 * kHalf];  // keys, values
     const int lane = lane_id(), col = lane & 15, grp = lane >> 4;
@@ -589,9 +585,7 @@ void shared_kernel(AttendArgs a)
     R r;
     r.init(a, e, job.i, job.kvh, idle ? rows - 1 : x0, rows);
 
-    auto key_swizzle = [](int row) {
-        return D == 64 ? (row >> 4 & 3) * 2 + (row >> 1 & 1) : (row >> 4 & 3) * 4 + (row & 3);
-    };
+    auto key_swizzle = [](int row) { return (row >> 4 & 3) * 4 + (row & 3); };
     auto value_swizzle = [](int row) { return row >> 1 & 7; };
     const int64_t first = (int64_t)e.r * a.w.blocks * a.w.kv_heads + job.kvh;
     // (past the last block: that one's again, not used)
@@ -613,16 +607,14 @@ void shared_kernel(AttendArgs a)
             v_to[n][h] = kHalf + value * 128 + ((piece % 4 * 2 + h) ^ value_swizzle(value)) * 16;
         }
     }
-    const bool mine = kPart >= 64 || lane < kPart;
     auto load = [&](int b) __attribute__((always_inline)) {
         const int64_t at = at_block(b);
         const uint8_t *codes = a.w.codes + at * (2 * kBlock * D);
 #pragma unroll
-        for (int n = 0; n < kLoads; ++n)
-            if (mine) {
-                k_raw[n] = *reinterpret_cast<const u32x4 *>(codes + from[n]);
-                v_raw[n] = *reinterpret_cast<const u32x4 *>(codes + kBlock * D + from[n]);
-            }
+        for (int n = 0; n < kLoads; ++n) {
+            k_raw[n] = *reinterpret_cast<const u32x4 *>(codes + from[n]);
+            v_raw[n] = *reinterpret_cast<const u32x4 *>(codes + kBlock * D + from[n]);
+        }
         k_scale = a.w.scales[at * 2];
         v_scale = a.w.scales[at * 2 + 1];
     };
@@ -632,18 +624,17 @@ void shared_kernel(AttendArgs a)
 #pragma unroll
         for (int n = 0; n < kLoads; ++n)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if (mine) {
-                    *reinterpret_cast<frag *>(to + k_to[n][h]) =
-                        widen(k_raw[n][h * 2], k_raw[n][h * 2 + 1], 1.f);
-                    *reinterpret_cast<frag *>(to + v_to[n][h]) =
-                        widen(v_raw[n][h * 2], v_raw[n][h * 2 + 1], unit);
-                }
+            for (int h = 0; h < 2; ++h) {
+                *reinterpret_cast<frag *>(to + k_to[n][h]) =
+                    widen(k_raw[n][h * 2], k_raw[n][h * 2 + 1], 1.f);
+                *reinterpret_cast<frag *>(to + v_to[n][h]) =
+                    widen(v_raw[n][h * 2], v_raw[n][h * 2 + 1], unit);
+            }
         next_scale = k_scale;
     };
-    int k_at[R::kSteps < 4 ? R::kSteps : 4], v_at[2];
+    int k_at[4], v_at[2];
 #pragma unroll
-    for (int st = 0; st < R::kSteps && st < 4; ++st) {
+    for (int st = 0; st < 4; ++st) {
         const int row = (col >> 2) * 16 + (col & 3);
         k_at[st] = row * 2 * D + ((st / 2 * 8 + grp * 2 + st % 2) ^ key_swizzle(row)) * 16;
     }
@@ -665,7 +656,6 @@ void shared_kernel(AttendArgs a)
         store(sTile[t & 1]);
         load(t + 1);
     };
-    auto nothing = [](int) {};
     // (blocks that this wave's rows do not see come before and after those that
     // they do)
     const int b0 = idle || own.b0 > all.b1 ? all.b1 : own.b0;
@@ -683,17 +673,16 @@ void shared_kernel(AttendArgs a)
                 return *reinterpret_cast<const frag *>(tile + k_at[st % 4] + st / 4 * 256 +
                                                        j * 8 * D);
             },
-            s, nothing);
+            s);
         if (b < own.full0 || b >= own.full1)
             r.mask(s, b);
-        r.relative(s, factor, top, 0, 1);
+        r.relative(s, factor, top);
         r.settle(s, top);
-        r.probabilities(s, 0, 1);
+        r.probabilities(s);
         r.template values<4>(
             [&](int g) __attribute__((always_inline)) {
                 return *reinterpret_cast<const frag *>(tile + v_at[g % 2] + g / 2 * 16 * 128);
-            },
-            nothing);
+            });
     }
     while (t < all.b1)
         next();
