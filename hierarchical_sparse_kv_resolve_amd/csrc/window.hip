@@ -13,15 +13,17 @@
 //
 // Writing: one workgroup for each touched block and head.  It reads the block's
 // codes if rows of it are kept, finds what is not finite, the maxima and the
-// scales, then writes the 16-byte pieces that changed.  Values turn through LDS
-// (codes of [token][d] to [d][token]).  A block and head is the unit because its
-// scale depends on all of it: nothing is exchanged between workgroups.
+// scales, then writes the block.  Values turn through LDS (codes of [token][d] to
+// [d][token]).  A block and head is the unit because its scale depends on all of it:
+// nothing is exchanged between workgroups.
 //
-// What they take (one MI355X, 8 heads of 128, bf16): 8 chunks of 4096 tokens 49 us,
-// 201 MB read and written at 4.1 TB/s; one token of 64 requests 6.8 us (8.2 with every
-// piece written), latency: lengths, then codes and new values, then three exchanges
-// through LDS.  32 windows of 4096 rows read back 165 us, 805 MB at 4.9 TB/s, the rate
-// of a large copy; one of 1024 rows 5.0 us.
+// What they take (one MI355X, 8 heads of 128, bf16, other tokens in each call and the
+// lengths advanced after it): 8 chunks of 4096 tokens 47 us, 201 MB read and written at
+// 4.3 TB/s; one token of 64 requests 8.1 us, of one 6.4, latency: lengths, then codes
+// and new values, then three exchanges through LDS.  (Pieces compared with what they
+// replace and written where they differ: 50, 8.1 and 6.8 us.)  32 windows of 4096 rows
+// read back 165 us, 805 MB at 4.9 TB/s, the rate of a large copy; one of 1024 rows 5.0
+// us.
 #include "block.h"
 #include "draft.h"
 #include "kvr_internal.h"
@@ -157,11 +159,6 @@ __device__ __forceinline__ u32x4 keep_bytes(u32x4 v, uint32_t keep)
         v[i] &= m;
     }
     return v;
-}
-
-__device__ __forceinline__ bool differ(const u32x4 &a, const u32x4 &b)
-{
-    return ((a[0] ^ b[0]) | (a[1] ^ b[1]) | (a[2] ^ b[2]) | (a[3] ^ b[3])) != 0;
 }
 
 template <int D, typename T>
@@ -312,8 +309,7 @@ __global__ __launch_bounds__(NT) void write_kernel(WriteArgs a)
                 v = narrow16(x, move_k);
             }
         }
-        if (!live || differ(v, ok[p]))
-            *reinterpret_cast<u32x4 *>(codes + q * 16) = v;
+        *reinterpret_cast<u32x4 *>(codes + q * 16) = v;
     }
     __syncthreads();
 #pragma unroll
@@ -333,8 +329,7 @@ __global__ __launch_bounds__(NT) void write_kernel(WriteArgs a)
         for (int y = 0; y < 16; ++y)
             if ((take >> y) & 1)
                 v[y / 4] |= (uint32_t)sV[t0 + y][d] << (y % 4 * 8);
-        if (!live || differ(v, ov[p]))
-            *reinterpret_cast<u32x4 *>(codes + kBlock * D + q * 16) = v;
+        *reinterpret_cast<u32x4 *>(codes + kBlock * D + q * 16) = v;
     }
     if (tid == 0) {
         scales[0] = (uint8_t)e_k;
