@@ -21,9 +21,11 @@
 // overflows (equal logits, or large ones that all fell to one group) are
 // searched once for each alternative instead.
 //
-// What they take (one MI355X, 131072 bf16 logits, 20 alternatives): 128 rows 11.0 us,
-// 34 MB at 3.0 TB/s, and 7.0; one row 3.5 and 6.9, the latency of reading the maxima,
-// of three barriers and of reading the runs that reach the bound.  64 alternatives of
+// What they take (one MI355X, 131072 bf16 logits, 20 alternatives): 128 rows 11 us, by
+// its counters bound by the issue of vector instructions (14 a logit, in three quarters
+// of its cycles; reading 34 MB alone would take 7; the entropy's part is paid without
+// one as well), and 7 to 8; one row 3.5 and 6.9, the latency of reading the maxima, of
+// three barriers and of reading the runs that reach the bound.  64 alternatives of
 // 64 rows take 8.1 and 10.5 (with 64 groups, of whose maxima the 64th bounds next to
 // nothing, the list overflowed: 190 in all).  128 rows with 8 pieces of a thread in
 // flight 20.1 in all, with 4 18.7.

@@ -18,12 +18,12 @@
 // nothing is exchanged between workgroups.
 //
 // What they take (one MI355X, 8 heads of 128, bf16, other tokens in each call and the
-// lengths advanced after it): 8 chunks of 4096 tokens 47 us, 201 MB read and written at
-// 4.3 TB/s; one token of 64 requests 8.1 us, of one 6.4, latency: lengths, then codes
-// and new values, then three exchanges through LDS.  (Pieces compared with what they
-// replace and written where they differ: 50, 8.1 and 6.8 us.)  32 windows of 4096 rows
-// read back 165 us, 805 MB at 4.9 TB/s, the rate of a large copy; one of 1024 rows 5.0
-// us.
+// lengths advanced after it): 8 chunks of 4096 tokens 45 to 47 us, 201 MB read and
+// written at 4.3 to 4.5 TB/s; one token of 64 requests 8.1 us, of one 6.4, latency:
+// lengths, then codes and new values, then three exchanges through LDS.  (Pieces
+// compared with what they replace and written where they differ: 50, 8.1 and 6.8 us.)
+// 32 windows of 4096 rows read back 165 us, 805 MB at 4.9 TB/s, the rate of a large
+// copy; one of 1024 rows 5.0 us.
 #include "block.h"
 #include "draft.h"
 #include "kvr_internal.h"

@@ -32,7 +32,7 @@
 //   64 requests x 32 heads (8 K/V) of 128, windows of 4096    97 us, 5.5 TB/s: HBM
 //   one prompt chunk of 2048 tokens, the same heads and window  139 us, 990
 //   TFLOP/s, 0.81 of a large bf16 product: by its counters the matrix units are
-//   busy for 45 % of the cycles and vector instructions issue in 56 %; a matrix
+//   busy for 42 % of the cycles and vector instructions issue in 53 %; a matrix
 //   instruction keeps the issue port for half of its time, so the two hardly
 //   overlap
 //   one request's token, window 1024   9 us: latency of 3 blocks a wave, which 8
@@ -307,8 +307,11 @@ struct Rows {
             const float y0 = exp2_hw(s[j][mb][x]), y1 = exp2_hw(s[j][mb][x + 1]);
             l[mb] += y0;
             l[mb] += y1;
-            // rounded to bf16 for the products (at most 2^-8 of it); summed and
-            // rounded here, so that a pair takes one register from now on
+            // rounded to bf16 for the products (at most 2^-8 of it): the matrix
+            // instruction takes 16 bits, and fp16, with three more, does not hold the
+            // values times their block's scale; the sum and with it the lse take them
+            // as they are.  Summed and rounded here, so that a pair takes one register
+            // from now on
             uint32_t pair = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)y0, (__bf16)y1});
             asm volatile("" : "+v"(pair), "+v"(l[mb]));
             p[j / 2][mb][(j & 1) * 2 + x / 2] = pair;
@@ -551,9 +554,11 @@ __device__ __forceinline__ void barrier_lds()
 // While one block is worked on, the next is converted into the other half of LDS,
 // and the codes of the one after it are on their way.
 //
-// 16-byte pieces lie at piece ^ swizzle of their row, so that the 16 rows that a
-// lane group reads at once are in different banks: keys in rows 16 a + 4 j + b (a,
-// b = 0 .. 3) of 2 D bytes, values in 16 consecutive rows of 128.
+// 16-byte pieces lie at piece ^ swizzle of their row: keys in rows 16 a + 4 j + b (a,
+// b = 0 .. 3) of 2 D bytes, values in 16 consecutive rows of 128.  The keys are read
+// without bank conflicts.  Reads of the values take twice their time, 4 cycles more
+// each, and the stores of both 8 more (each pattern counted alone): with heads of 128 96
+// of the 256 LDS cycles of a wave and block.
 template <int D, int MB, int NW>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(NW / 4)))
 void shared_kernel(AttendArgs a)
@@ -818,7 +823,9 @@ hipError_t launch_dim(const AttendArgs &a, const DraftPlan &p, dim3 grid, hipStr
     if (e != hipSuccess || a.shares == 1)
         return e;
     const int64_t rows = (int64_t)a.c.n * a.c.nq * a.c.heads;
-    if constexpr (D == 256)  // (the only one whose shared_kernel makes shares)
+    // (heads of 256 are the only ones whose shared_kernel makes shares; of 128, windows of
+    // 4096, in two: 512 tokens 99 us, split 50; 1024 121, 92; 2400 317, 210)
+    if constexpr (D == 256)
         if (!p.split)
             return launch(nullptr, 0, join_kernel<D, 1>,
                           dim3((unsigned)((rows + kJoinWaves - 1) / kJoinWaves)),
@@ -838,13 +845,16 @@ DraftPlan draft_plan(int32_t n, int32_t nq, int32_t heads, int32_t kv_heads, int
     const int64_t blocks = ((int64_t)tokens + kBlock - 1) / kBlock + 1;
     // shared_kernel takes whole rounds of the compute units (256 query rows a
     // workgroup, with heads of 256 128).  Heads of 128, windows of 4096: a chunk of 1024
-    // tokens (128 workgroups) 118 us against 93 split, 1500 (188) 135, 134, 1700 (213)
-    // 136, 155, 2048 (256) 139, 177, 2400 (300) 261, 216, 3000 (375) 263, 259: so with
+    // tokens (128 workgroups) 134 us against 92 split, 1500 (188) 135, 134, 1700 (213)
+    // 136, 155, 2048 (256) 139, 177, 2400 (300) 262, 210, 3000 (375) 263, 259: so with
     // 0.75 of its rounds full.  Heads of 256, whose shares fill a part of one round: 256
     // tokens (32 workgroups, one round of the other kernel) 53, 46, 300 (40) 58, 85, 512
     // (64) 78, 89, with windows of 1024 41, 37, 1024 (128) 128, 172; 2400 (300) 415, 414,
-    // 2700 (340) 415, 457: so past an eighth, and past one round with 0.6.  Heads of 64
-    // gain from it at no number (1024 tokens of 64 heads 101, split 99).
+    // 2700 (340) 415, 457: so past an eighth, and past one round with 0.6.  Heads of 64,
+    // for which it is not built, lose by it with long windows (64 heads, windows of
+    // 4096: 512 tokens 99, split 53; 1024, a full round, 101, 98; 2048 198, 185; 4096 390,
+    // 360; 1000 of 56 heads, windows of 2000, 57, 51) and would gain by full rounds
+    // and short ones (windows of 1024: 1024 tokens 36, 39, 2048 68, 70; of 256: 34, 43).
     const int64_t shared = 16 * 2 * shared_waves(d_head);
     const int64_t full = units * ((rows + shared - 1) / shared);
     const int64_t room = (full + kUnits - 1) / kUnits * kUnits;
