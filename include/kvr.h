@@ -996,9 +996,11 @@ typedef struct kvr_draft_attend_call {
  * over the rows the query sees; one that sees none gets out = 0 and
  * lse = -infinity.  Codes are exact in bf16; products, sums, maxima and
  * exponentials in 32 bits; probabilities are rounded to bf16 before their product
- * with the values.  Rows may be cut into shares that are joined in a fixed
- * order: results do not vary from run to run (another n, nq or heads may cut
- * them otherwise).  One kernel, or two with shares; n = 0 is a no-op. */
+ * with the values.  Sums are divided at the end and weigh a row by 2^8 at most: they
+ * are sure not to overflow while the values are below 2^120 / W.  Rows may be cut
+ * into shares that are joined in a fixed order: results do not vary from run to run
+ * (another n, nq or heads may cut them otherwise).  One kernel, or two with shares;
+ * n = 0 is a no-op. */
 int kvr_draft_attend(kvr_draft *d, const kvr_draft_attend_call *call, void *stream);
 
 /* Workspace bytes of kvr_draft_attend calls of up to n entries, nq queries and
